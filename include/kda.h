@@ -288,6 +288,147 @@ int kda_state_snapshot(const float *snaps, int64_t n_rows, const int64_t *src_id
                        int dk, int dv, kda_stream_t stream);
 
 /*
+ * The state space layer and draft verification: what a hybrid model runs
+ * beside the KDA layers, on the same kind of batch (packed prompts, single
+ * tokens and short runs on pools of resident states).  These operators are
+ * additions of this library; the pages have no counterpart.
+ *
+ * Conventions, beside the ones above
+ *  - Activation matrices are bf16 with the token as the row; each takes its
+ *    row stride in elements (ld*), so that slices of a wider projection are
+ *    passed as they are.
+ *  - cu_seqlens: device int32 [n + 1] token offsets, or NULL for n runs of
+ *    total_tokens / n tokens each (which must divide).  total_tokens is at
+ *    most 2^31 - 1; offsets into the matrices are 64-bit.
+ *  - `used` (token forms): device int32 [n] or NULL.  Run b is cut to its first
+ *    used[b] tokens: later tokens do not reach the state and their rows of o
+ *    are set to zero.  An entry outside [0, run length] is skipped and
+ *    recorded as KDA_ERR_SHAPE, as a slot outside [0, n_slots) is.
+ *  - Slots must be distinct.  A token form with commit == 0 leaves the pool
+ *    unchanged; with commit != 0, o may be NULL (only the state is advanced).
+ */
+
+/* Flag of the convolution: o = silu(...); 0 = no activation. */
+#define KDA_CONV_SILU 1u
+/* Flag of the scan: dt = softplus(raw + dt_bias); 0 = dt = raw + dt_bias. */
+#define KDA_SSM_DT_SOFTPLUS 1u
+
+/*
+ * kda_conv_fwd - short causal depthwise convolution over packed prompts:
+ *   o_t[c] = act(bias[c] + sum_{w < W} weight[c, w] x_{t - (W - 1) + w}[c]).
+ *   x, o        [total, D] bf16, rows ldx / ldo elements apart.
+ *   weight      [D, W] bf16, W in 2..4 (weight[c, W - 1] meets the token itself);
+ *   bias        [D] bf16 or NULL.
+ *   conv0       [n_seq, W - 1, D] bf16: the inputs in front of each sequence,
+ *               oldest first; NULL = zeros.
+ *   conv_final  [n_seq, W - 1, D] bf16: the last W - 1 inputs of each sequence
+ *               (reaching back into conv0 where it is shorter), or NULL.  Must
+ *               not overlap conv0 (the same pointer is KDA_ERR_SHAPE).
+ * Any D and any alignment of 2 bytes; fastest where D, ldx and ldo are
+ * multiples of 8 and the pointers are 16-byte aligned.
+ *   Errors: KDA_ERR_NULL, _SHAPE, _ALIGN, _UNSUPPORTED, _CUDA.
+ */
+int kda_conv_fwd(const kda_bf16 *x, int64_t ldx, const kda_bf16 *weight, const kda_bf16 *bias,
+                 const int32_t *cu_seqlens, int n_seq, int64_t total_tokens, int D, int W,
+                 unsigned flags, const kda_bf16 *conv0, kda_bf16 *conv_final, kda_bf16 *o,
+                 int64_t ldo, kda_stream_t stream);
+
+/*
+ * kda_conv_tokens - the same convolution for n single tokens (cu_seqlens NULL,
+ * total_tokens = n) or short runs on a pool of held inputs: run b uses and,
+ * with commit, advances slot slots[b] (NULL: slot b) of conv_pool
+ * [n_slots, W - 1, D] bf16.
+ *   Errors: KDA_ERR_NULL, _SHAPE, _ALIGN, _UNSUPPORTED, _CUDA.
+ */
+int kda_conv_tokens(const kda_bf16 *x, int64_t ldx, const kda_bf16 *weight, const kda_bf16 *bias,
+                    const int32_t *cu_seqlens, int n, int64_t total_tokens, int D, int W,
+                    unsigned flags, kda_bf16 *conv_pool, int n_slots, const int32_t *slots,
+                    const int32_t *used, int commit, kda_bf16 *o, int64_t ldo,
+                    kda_stream_t stream);
+
+/*
+ * kda_ssm_fwd - selective state space scan over packed prompts.  Per sequence
+ * and head h, in group g = h / (H / G), with an N x P fp32 state S:
+ *   dt_t = softplus(dt[t, h] + dt_bias[h])        (or without softplus)
+ *   S_t  = exp(dt_t A[h]) S_{t-1} + dt_t B_t[g] x_t^T
+ *   o_t  = (S_t^T C_t[g] + D[h] x_t) * silu(z_t)
+ *   x, z, o     [total, H, P] bf16 (z NULL: no gate)
+ *   B, C        [total, G, N] bf16; G divides H
+ *   dt          [total, H] bf16; A, D, dt_bias [H] fp32 (D, dt_bias may be NULL)
+ *   S0, S_final [n_seq, H, N, P] fp32 or NULL (zeros / not wanted).  They must
+ *               not overlap (the same pointer is KDA_ERR_SHAPE).
+ * N, P in {64, 128}.  A <= 0 and dt >= 0 are expected (decays in (0, 1]).  A
+ * non-finite input makes the outputs of its own sequence undefined from up to
+ * 127 tokens before it on; other sequences are not touched by it.
+ * Rows of x, B, C, z and o start on 16-byte boundaries (pointers 16-byte
+ * aligned, strides multiples of 8); dt has no alignment beyond its type's.
+ *   workspace   device scratch, 16-byte aligned, of workspace_bytes bytes
+ *               (kda_ssm_fwd_workspace_bytes); not to be shared by calls that
+ *               overlap on the GPU.
+ *   Errors: KDA_ERR_NULL, _SHAPE, _ALIGN, _UNSUPPORTED, _WORKSPACE, _CUDA.
+ */
+int kda_ssm_fwd(const kda_bf16 *x, int64_t ldx, const kda_bf16 *dt, int64_t lddt, const float *A,
+                const kda_bf16 *B, int64_t ldb, const kda_bf16 *C, int64_t ldc, const float *D,
+                const kda_bf16 *z, int64_t ldz, const float *dt_bias, unsigned flags,
+                const int32_t *cu_seqlens, int n_seq, int64_t total_tokens, int H, int P, int G,
+                int N, const float *S0, kda_bf16 *o, int64_t ldo, float *S_final, void *workspace,
+                size_t workspace_bytes, kda_stream_t stream);
+
+/* Workspace bytes of kda_ssm_fwd (0: none needed, or unsupported sizes). */
+size_t kda_ssm_fwd_workspace_bytes(int n_seq, int64_t total_tokens, int H, int P, int G, int N);
+
+/*
+ * kda_ssm_tokens - the same recurrence for n single tokens (cu_seqlens NULL,
+ * total_tokens = n) or short runs on resident states: run b starts from slot
+ * slots[b] (NULL: slot b) of state_pool [n_slots, H, N, P] fp32 and, with
+ * commit, leaves its last state there.  A state is read once and written once,
+ * the tokens are applied one after another on chip.
+ *   Errors: KDA_ERR_NULL, _SHAPE, _ALIGN, _UNSUPPORTED, _CUDA.
+ */
+int kda_ssm_tokens(const kda_bf16 *x, int64_t ldx, const kda_bf16 *dt, int64_t lddt,
+                   const float *A, const kda_bf16 *B, int64_t ldb, const kda_bf16 *C, int64_t ldc,
+                   const float *D, const kda_bf16 *z, int64_t ldz, const float *dt_bias,
+                   unsigned flags, const int32_t *cu_seqlens, int n, int64_t total_tokens, int H,
+                   int P, int G, int N, float *state_pool, int n_slots, const int32_t *slots,
+                   const int32_t *used, int commit, kda_bf16 *o, int64_t ldo,
+                   kda_stream_t stream);
+
+/*
+ * kda_verify_draft - how much of each drafted run the target model accepts,
+ * and the token that follows, from given uniform random numbers.
+ * Run b is rows [cu_seqlens[b], cu_seqlens[b + 1]) of `tokens`: the last
+ * accepted token and then k drafted ones (k >= 0; an empty run is malformed).
+ *   target      [total, V] probabilities; row j of a run is the target's
+ *               distribution of the token after the run's token j.
+ *   draft       [total - n, V] probabilities the drafted tokens were drawn
+ *               from, k rows for each run (those of run b from row
+ *               cu_seqlens[b] - b on), or NULL: the drafts are certain (q = 1
+ *               at the drafted token).
+ *   prob_bytes  4 (fp32) or 2 (bf16) for both.
+ *   u           [total] fp32 in [0, 1): u[cu[b] + j] decides on draft j, the
+ *               run's last one draws the token after the accepted ones.
+ * Draft j (token x) is accepted while u_j q_j(x) < p_j(x).  The token after
+ * the accepted ones is the smallest i with w_0 + ... + w_i > u sum(w), where w
+ * is max(p - q, 0) of the first refused row (p where that is zero everywhere;
+ * without `draft`, p with the refused token taken out) or, with none refused,
+ * the run's last row of the target.  The sums carry at least 48 bits.  NaN and
+ * negative weights count as zero.
+ *   out_tokens  int32 [total]: the accepted tokens, the drawn one, then -1.
+ *   n_out       int32 [n]: how many there are, accepted + 1.  It is also how
+ *               many of the run's tokens belong in the recurrent states: the
+ *               `used` of kda_conv_tokens and kda_ssm_tokens.
+ * A drafted token outside [0, V) is refused and recorded as KDA_ERR_SHAPE; a
+ * malformed run gives n_out = 0 and KDA_ERR_SHAPE; a row without any finite
+ * positive weight sum gives the token -1, not counted in n_out, and
+ * KDA_ERR_RANGE.  V <= 2^22.
+ *   Errors: KDA_ERR_NULL, _SHAPE, _ALIGN, _UNSUPPORTED, _CUDA.
+ */
+int kda_verify_draft(const void *target, const void *draft, int prob_bytes, int V,
+                     const int32_t *tokens, const float *u, const int32_t *cu_seqlens, int n,
+                     int64_t total_tokens, int32_t *out_tokens, int32_t *n_out,
+                     kda_stream_t stream);
+
+/*
  * kda_device_status - read (and with reset != 0, clear) the library's
  * device-side status word on the current device.  Kernels record there what
  * only the GPU can see: KDA_ERR_TIMEOUT (a bounded wait gave up instead of

@@ -46,7 +46,9 @@ KDA_ERR_RANGE = 8
 EXPORTED = ("kda_status_string", "kda_version", "kda_chunk_fwd_workspace_bytes",
             "kda_chunk_fwd", "kda_decode_step", "kda_state_snapshot", "kda_device_status",
             "kda_chunk_fwd_noalloc", "kda_decode_tokens", "kda_chunk_fwd_ex",
-            "kda_decode_step_ex", "kda_stream_status_bind", "kda_stream_status")
+            "kda_decode_step_ex", "kda_stream_status_bind", "kda_stream_status",
+            "kda_conv_fwd", "kda_conv_tokens", "kda_ssm_fwd", "kda_ssm_fwd_workspace_bytes",
+            "kda_ssm_tokens", "kda_verify_draft")
 
 _lib = None
 
@@ -99,6 +101,19 @@ def lib():
         L.kda_stream_status_bind.argtypes = [P, P]
         L.kda_stream_status.restype = I
         L.kda_stream_status.argtypes = [P, I]
+        L.kda_conv_fwd.restype = I
+        L.kda_conv_fwd.argtypes = [P, I64, P, P, P, I, I64, I, I, U, P, P, P, I64, P]
+        L.kda_conv_tokens.restype = I
+        L.kda_conv_tokens.argtypes = [P, I64, P, P, P, I, I64, I, I, U, P, I, P, P, I, P, I64, P]
+        ssm = [P, I64, P, I64, P, P, I64, P, I64, P, P, I64, P, U, P, I, I64, I, I, I, I]
+        L.kda_ssm_fwd.restype = I
+        L.kda_ssm_fwd.argtypes = ssm + [P, P, I64, P, P, SZ, P]
+        L.kda_ssm_fwd_workspace_bytes.restype = SZ
+        L.kda_ssm_fwd_workspace_bytes.argtypes = [I, I64, I, I, I, I]
+        L.kda_ssm_tokens.restype = I
+        L.kda_ssm_tokens.argtypes = ssm + [P, I, P, P, I, P, I64, P]
+        L.kda_verify_draft.restype = I
+        L.kda_verify_draft.argtypes = [P, P, I, I, P, P, P, I, I64, P, P, P]
         _lib = L
     return _lib
 
@@ -307,3 +322,8 @@ def stream_status(stream=None, reset=True):
     if st == KDA_ERR_NULL:
         raise KDAError("kda_stream_status", st)
     return st
+
+
+# The state space layer's operators and draft verification.
+from .serving import (conv_fwd, conv_tokens, ssm_fwd, ssm_tokens,  # noqa: E402,F401
+                      ssm_workspace_bytes, verify_draft)

@@ -167,15 +167,6 @@ int *bound_status_word(cudaStream_t st) {
   return nullptr;
 }
 
-// The word the kernels of a call on stream st record into.
-int *status_word(cudaStream_t st) {
-  if (int *w = bound_status_word(st)) return w;
-  void *p = nullptr;
-  return cudaGetSymbolAddress(&p, g_status) == cudaSuccess ? static_cast<int *>(p) : nullptr;
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 bool dim_ok(int d) { return d == 64 || d == 128; }
 
 // gmin must keep exp(-16 gmin) (the largest sub-tile rescaling factor) well
@@ -192,6 +183,15 @@ constexpr unsigned kPassFlags = KDA_PASS_PREPARE | KDA_PASS_STATE;
 constexpr int64_t kDecodeTokensRun = 16;
 
 }  // namespace
+
+// The word the kernels of a call on stream st record into.
+int *status_word(cudaStream_t st) {
+  if (int *w = bound_status_word(st)) return w;
+  void *p = nullptr;
+  return cudaGetSymbolAddress(&p, g_status) == cudaSuccess ? static_cast<int *>(p) : nullptr;
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // The one rule for whether a kda_chunk_fwd call takes the segment-parallel
 // scan (shared with kda_chunk_fwd_noalloc): equal-length sequences given
@@ -230,7 +230,7 @@ const char *kda_status_string(int status) {
   }
 }
 
-int kda_version(void) { return 200; }
+int kda_version(void) { return 210; }
 
 size_t kda_chunk_fwd_workspace_bytes(int n_seq, int64_t total_tokens, int H, int dk, int dv,
                                      int chunk) {

@@ -1,0 +1,100 @@
+// Arguments that the kernels of the state space layer (short convolution, selective scan) and of
+// draft verification take by value, and the small device functions that they share.
+#pragma once
+
+#include "kda_common.cuh"
+
+namespace kda {
+
+// A batch of token runs: rows [cu[b], cu[b + 1]) of packed tensors, or fixed_len tokens each
+// where cu is NULL.  `used` (NULL: all) cuts every run to its first used[b] tokens.
+struct Runs {
+  const int32_t *cu;
+  const int32_t *used;
+  int n;
+  int64_t total, fixed_len;
+};
+
+// Token range [b, b + len) of run s, and how many of them are used.  false for a malformed entry
+// (an empty run; the caller records KDA_ERR_SHAPE).
+__device__ __forceinline__ bool run_range(const Runs &r, int s, int64_t &begin, int64_t &len,
+                                          int64_t &used) {
+  int64_t end;
+  bool ok = true;
+  if (r.cu) {
+    ok = seq_range(r.cu, s, r.total, begin, end);
+  } else {
+    begin = static_cast<int64_t>(s) * r.fixed_len;
+    end = begin + r.fixed_len;
+  }
+  used = len = end - begin;
+  if (r.used && ok) {
+    const int64_t u = r.used[s];
+    if (u < 0 || u > len) {
+      begin = len = used = 0;
+      return false;
+    }
+    used = u;
+  }
+  return ok;
+}
+
+// x / (1 + exp(-x)).  exp overflows to +inf for x < -88 and gives -0, x = -inf gives NaN as the
+// formula does.
+__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+
+// log(1 + exp(x)); beyond 20 the difference to x is under half a unit in the last place.
+__device__ __forceinline__ float softplus(float x) { return x > 20.f ? x : log1pf(expf(x)); }
+
+struct ConvArgs {
+  const kda_bf16 *x, *weight, *bias, *state_in;
+  kda_bf16 *state_out, *o;
+  int64_t ldx, ldo;
+  int D, act;
+  Runs runs;
+  const int32_t *slots;
+  int n_slots;
+  int *status;
+};
+
+struct SsmArgs {
+  const kda_bf16 *x, *dt, *B, *C, *z;
+  const float *A, *D, *dt_bias;
+  int64_t ldx, lddt, ldb, ldc, ldz, ldo;
+  int H, G, softplus;
+  Runs runs;
+  const float *S_in;
+  float *S_out;
+  const int32_t *slots;
+  int n_slots;
+  kda_bf16 *o;
+  int *status;
+};
+
+struct VerifyArgs {
+  const void *target, *draft;
+  const int32_t *tokens;
+  const float *u;
+  const int32_t *cu;
+  int n, V;
+  int64_t total;
+  int32_t *out_tokens, *n_out;
+  int *status;
+};
+
+// The step of one token: dt after bias and softplus.
+__device__ __forceinline__ float ssm_dt(const SsmArgs &a, int64_t t, int h) {
+  float d = bf2f(a.dt[t * a.lddt + h]);
+  if (a.dt_bias) d += a.dt_bias[h];
+  return a.softplus ? softplus(d) : d;
+}
+
+int *status_word(cudaStream_t st);
+bool aligned16(const void *p);
+
+cudaError_t conv_fwd_launch(const ConvArgs &a, int W, cudaStream_t st);
+cudaError_t conv_tokens_launch(const ConvArgs &a, int W, cudaStream_t st);
+cudaError_t ssm_tokens_launch(const SsmArgs &a, int P, int N, bool single, cudaStream_t st);
+cudaError_t verify_launch(const VerifyArgs &a, bool half, cudaStream_t st);
+
+}  // namespace kda

@@ -1,0 +1,291 @@
+// Verification of drafted tokens against the target's probabilities, from given random numbers.
+//
+// Run b is the last accepted token and k drafted ones; row j of the target judges token j + 1.
+// Draft j is accepted while u_j q_j(x) < p_j(x).  At the first refusal the next token comes from
+// max(p - q, 0) (from p where that is zero everywhere), after k acceptances from the target's last
+// row, by the inverse distribution: the smallest i with w_0 + ... + w_i > u (sum of w).
+//
+// Bound by memory: one row of p (and of q) per run is read.  A cluster of CTAs shares a run's row.
+// Which token a sum lands on must not depend on the order of the additions, so sums carry 48 bits:
+// a lane adds its elements in pairs of fp32 (the value and what its rounding lost; double-precision
+// adds run at 2 per SM and cycle here, below the rate at which elements arrive), everything above a
+// lane is in double precision.  The row is cut into segments of kSeg elements whose sums stay in
+// shared memory; the segment that the target falls into is read a second time, from L2.
+#include "kda_serving.cuh"
+
+namespace kda {
+
+namespace {
+
+constexpr int kVThreads = 512;
+constexpr int kVWarps = kVThreads / 32;
+constexpr int kSeg = 1024;
+
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ unsigned cluster_size() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// A double in the shared memory of CTA `rank` of this cluster, at this CTA's address `p`.
+__device__ __forceinline__ double peer_load(const double *p, unsigned rank) {
+  uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(p)), there;
+  double v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(there) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float prob(const float *p, int64_t i) { return p[i]; }
+__device__ __forceinline__ float prob(const kda_bf16 *p, int64_t i) { return bf2f(p[i]); }
+
+// The row's weights: max(p - q, 0), p without one token, or p.  NaN counts as 0.
+template <typename T>
+struct Weights {
+  const T *p, *q;
+  int without;  // -1: none
+
+  // w = hi + lo: the rounded difference, and what its rounding lost
+  __device__ __forceinline__ void at(float pv, float qv, int i, float &hi, float &lo) const {
+    hi = fmaxf(pv - qv, 0.f);
+    lo = hi > 0.f ? (pv - hi) - qv : 0.f;
+    if (i == without || !(pv >= 0.f)) hi = lo = 0.f;
+  }
+  __device__ __forceinline__ double one(int i) const {
+    float hi, lo;
+    at(prob(p, i), q ? prob(q, i) : 0.f, i, hi, lo);
+    return static_cast<double>(hi) + static_cast<double>(lo);
+  }
+};
+
+struct Sum {  // hi + lo
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float x, float xl) {
+    const float s = hi + x, r = s - hi;
+    lo += (hi - (s - r)) + (x - r) + xl;
+    hi = s;
+  }
+  __device__ __forceinline__ double value() const {
+    return static_cast<double>(hi) + static_cast<double>(lo);
+  }
+};
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// inclusive prefix sums over the lanes
+__device__ __forceinline__ double warp_scan(double v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double w = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += w;
+  }
+  return v;
+}
+
+// One lane's elements of segment [i0, i1): vectors of 16 bytes, the lanes side by side.
+template <typename T, bool VECTOR>
+__device__ __forceinline__ double segment_sum(const Weights<T> &w, int i0, int i1, int lane) {
+  Sum s;
+  if constexpr (VECTOR) {
+    constexpr int E = 16 / sizeof(T);
+#pragma unroll
+    for (int k = 0; k < kSeg / (32 * E); ++k) {
+      const int i = i0 + (k * 32 + lane) * E;
+      if (i < i1) {
+        T pv[E], qv[E] = {};
+        *reinterpret_cast<uint4 *>(pv) = __ldg(reinterpret_cast<const uint4 *>(w.p + i));
+        if (w.q) *reinterpret_cast<uint4 *>(qv) = __ldg(reinterpret_cast<const uint4 *>(w.q + i));
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          float hi, lo;
+          w.at(prob(pv, e), prob(qv, e), i + e, hi, lo);
+          s.add(hi, lo);
+        }
+      }
+    }
+  } else {
+#pragma unroll 8
+    for (int k = 0; k < kSeg / 32; ++k) {
+      const int i = i0 + k * 32 + lane;
+      if (i < i1) {
+        float hi, lo;
+        w.at(prob(w.p, i), w.q ? prob(w.q, i) : 0.f, i, hi, lo);
+        s.add(hi, lo);
+      }
+    }
+  }
+  return s.value();
+}
+
+template <typename T, bool VECTOR>
+__global__ void __launch_bounds__(kVThreads) verify_kernel(const VerifyArgs a) {
+  extern __shared__ double s_seg[];  // sums of this CTA's segments
+  __shared__ double s_total;
+  __shared__ int s_got;
+  const unsigned rank = cluster_rank(), ranks = cluster_size();
+  const int b = blockIdx.x / ranks;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const T *target = static_cast<const T *>(a.target), *draft = static_cast<const T *>(a.draft);
+  int64_t t0, t1;
+  // every run has its last accepted token; the whole cluster takes the same way out
+  if (!seq_range(a.cu, b, a.total, t0, t1) || t1 == t0 || t0 < b ||
+      t1 - b - 1 > a.total - a.n) {
+    if (rank == 0 && tid == 0) {
+      atomicOr(a.status, KDA_ERR_SHAPE);
+      a.n_out[b] = 0;
+    }
+    return;
+  }
+  const int k = static_cast<int>(t1 - t0) - 1;
+  if (warp == 0) {
+    int got = k;
+    for (int j0 = 0; j0 < k && got == k; j0 += 32) {
+      const int j = j0 + lane;
+      bool refused = false;
+      if (j < k) {
+        const int x = a.tokens[t0 + j + 1];
+        refused = true;
+        if (x >= 0 && x < a.V) {
+          const double p = prob(target, (t0 + j) * a.V + x);
+          const double q = draft ? prob(draft, (t0 - b + j) * a.V + x) : 1.0;
+          refused = !(static_cast<double>(a.u[t0 + j]) * q < p);
+        } else if (rank == 0) {
+          atomicOr(a.status, KDA_ERR_SHAPE);
+        }
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, refused);
+      if (m) got = j0 + __ffs(m) - 1;
+    }
+    if (lane == 0) s_got = got;
+  }
+  __syncthreads();
+  const int got = s_got;
+  const bool cut = got < k;
+  if (rank == 0)
+    for (int j = tid; j <= k; j += kVThreads)
+      if (j != got) a.out_tokens[t0 + j] = j < got ? a.tokens[t0 + j + 1] : -1;
+
+  Weights<T> w{target + (t0 + got) * a.V, cut && draft ? draft + (t0 - b + got) * a.V : nullptr,
+               cut && !draft ? a.tokens[t0 + got + 1] : -1};
+  const int segs = (a.V + kSeg - 1) / kSeg;
+  const int seg0 = static_cast<int>(static_cast<int64_t>(segs) * rank / ranks);
+  const int seg1 = static_cast<int>(static_cast<int64_t>(segs) * (rank + 1) / ranks);
+  double total = 0.0, before = 0.0;
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int s = seg0 + warp; s < seg1; s += kVWarps) {
+      const int i0 = s * kSeg, i1 = i0 + kSeg < a.V ? i0 + kSeg : a.V;
+      const double v = warp_sum(segment_sum<T, VECTOR>(w, i0, i1, lane));
+      if (lane == 0) s_seg[s - seg0] = v;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      double sum = 0.0;
+      for (int s = 0; s < seg1 - seg0; s += 32)
+        sum += __shfl_sync(0xffffffffu,
+                           warp_scan(s + lane < seg1 - seg0 ? s_seg[s + lane] : 0.0, lane), 31);
+      if (lane == 0) s_total = sum;
+    }
+    cluster_sync();
+    total = before = 0.0;
+    for (unsigned r = 0; r < ranks; ++r) {
+      if (r == rank) before = total;
+      total += peer_load(&s_total, r);
+    }
+    cluster_sync();
+    if (total > 0.0 || (!w.q && w.without < 0)) break;
+    w.q = nullptr;  // nothing is left of the row: the target's own weights
+    w.without = -1;
+  }
+  if (!(total > 0.0 && total < 1e300)) {
+    if (rank == 0 && tid == 0) {
+      atomicOr(a.status, KDA_ERR_RANGE);
+      a.out_tokens[t0 + got] = -1;
+      a.n_out[b] = got;
+    }
+    return;
+  }
+  if (warp != 0) return;
+  const float u = a.u[t1 - 1];
+  const double want = static_cast<double>(u >= 0.f ? fminf(u, 0x1.fffffep-1f) : 0.f) * total;
+  // the CTA whose part of the row holds it
+  if (!(want >= before && want < before + s_total)) return;
+  double sum = before;
+  int seg = -1;
+  for (int s = 0; s < seg1 - seg0 && seg < 0; s += 32) {
+    const double c = warp_scan(s + lane < seg1 - seg0 ? s_seg[s + lane] : 0.0, lane);
+    const unsigned m = __ballot_sync(0xffffffffu, sum + c > want);
+    if (m) {
+      seg = s + __ffs(m) - 1;
+      const double prev = __shfl_sync(0xffffffffu, c, (__ffs(m) + 30) & 31);
+      if (__ffs(m) > 1) sum += prev;
+    } else {
+      sum += __shfl_sync(0xffffffffu, c, 31);
+    }
+  }
+  if (seg < 0) seg = seg1 - seg0 - 1;  // rounding of the sums alone
+  // inside the segment: 32 neighbouring elements per lane
+  const int i0 = (seg0 + seg) * kSeg + lane * 32;
+  double mine = 0.0;
+  for (int i = i0; i < i0 + 32 && i < a.V; ++i) mine += w.one(i);
+  const double c = warp_scan(mine, lane);
+  int token = -1;
+  double run = sum + (c - mine);
+  for (int i = i0; i < i0 + 32 && i < a.V; ++i) {
+    const double v = w.one(i);
+    run += v;
+    if (v > 0.0) {
+      token = i;
+      if (run > want) break;
+    }
+  }
+  // the first lane that passes `want`; else the last element with any weight
+  const unsigned over = __ballot_sync(0xffffffffu, token >= 0 && sum + c > want);
+  const unsigned any = __ballot_sync(0xffffffffu, token >= 0);
+  const int from = over ? __ffs(over) - 1 : 31 - __clz(any);
+  if (lane == from) {
+    a.out_tokens[t0 + got] = token;
+    a.n_out[b] = got + 1;
+  }
+}
+
+template <typename T, bool VECTOR>
+cudaError_t run(const VerifyArgs &a, cudaStream_t st) {
+  const int segs = (a.V + kSeg - 1) / kSeg;
+  int ranks = 1;
+  while (ranks < 8 && a.n * ranks < 2 * 152 && ranks * kVWarps < segs) ranks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.n) * ranks);
+  cfg.blockDim = dim3(kVThreads);
+  cfg.dynamicSmemBytes = ((segs + ranks - 1) / ranks) * sizeof(double);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, verify_kernel<T, VECTOR>, a);
+}
+
+}  // namespace
+
+cudaError_t verify_launch(const VerifyArgs &a, bool half, cudaStream_t st) {
+  const size_t size = half ? 2 : 4;
+  // 16-byte loads where every row starts on a 16-byte boundary
+  const bool v = a.V * size % 16 == 0 && aligned16(a.target) && aligned16(a.draft);
+  if (half) return v ? run<kda_bf16, true>(a, st) : run<kda_bf16, false>(a, st);
+  return v ? run<float, true>(a, st) : run<float, false>(a, st);
+}
+
+}  // namespace kda

@@ -95,6 +95,9 @@ bool aligned16(const void *p);
 cudaError_t conv_fwd_launch(const ConvArgs &a, int W, cudaStream_t st);
 cudaError_t conv_tokens_launch(const ConvArgs &a, int W, cudaStream_t st);
 cudaError_t ssm_tokens_launch(const SsmArgs &a, int P, int N, bool single, cudaStream_t st);
+size_t ssm_chunk_workspace(int n_seq, int64_t total, int H, int P, int G, int N);
+cudaError_t ssm_chunk_launch(const SsmArgs &a, int P, int G, int N, void *workspace, size_t bytes,
+                             cudaStream_t st);
 cudaError_t verify_launch(const VerifyArgs &a, bool half, cudaStream_t st);
 
 }  // namespace kda

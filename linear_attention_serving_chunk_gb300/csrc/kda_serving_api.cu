@@ -124,10 +124,15 @@ int kda_ssm_fwd(const kda_bf16 *x, int64_t ldx, const kda_bf16 *dt, int64_t lddt
   if (total_tokens == 0 && !S_final) return KDA_OK;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (!(a.status = status_word(st))) return KDA_ERR_CUDA;
-  return launched(ssm_tokens_launch(a, P, N, false, st));
+  return launched(ssm_chunk_launch(a, P, G, N, workspace, workspace_bytes, st));
 }
 
-size_t kda_ssm_fwd_workspace_bytes(int, int64_t, int, int, int, int) { return 0; }
+size_t kda_ssm_fwd_workspace_bytes(int n_seq, int64_t total_tokens, int H, int P, int G, int N) {
+  if (n_seq <= 0 || total_tokens <= 0 || H <= 0 || G <= 0 || H % G != 0 || !size_ok(P) ||
+      !size_ok(N))
+    return 0;
+  return ssm_chunk_workspace(n_seq, total_tokens, H, P, G, N);
+}
 
 int kda_ssm_tokens(const kda_bf16 *x, int64_t ldx, const kda_bf16 *dt, int64_t lddt,
                    const float *A, const kda_bf16 *B, int64_t ldb, const kda_bf16 *C, int64_t ldc,

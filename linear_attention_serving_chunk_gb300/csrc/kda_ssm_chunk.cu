@@ -14,7 +14,7 @@
 //
 // Roundings.  x, B and C are bf16 and enter exactly.  X' is split into three bf16 planes that hold
 // all 24 bits of its fp32 value, and the state itself lives in registers in fp32 (S^T: one thread
-// per column and half of n), so S and S_final carry fp32 accuracy.  For the output, S enters as two
+// per column and quarter of n), so S and S_final carry fp32 accuracy.  For the output, S enters as two
 // planes (16 bits) and M as one (8 bits): the in-chunk weights are rounded once to the type of the
 // result, which adds an error of the size of the result's own rounding.
 //
@@ -28,11 +28,11 @@
 // a of the whole segment; the second pass starts each segment from a_{j-1} (... (a_0 S0 + N_0) ...)
 // + N_{j-1}.
 //
-// Roles: warps 0-7 (two warpgroups) do the element-wise work, warp 8 issues the TMA loads, warp 9
-// the MMAs, warps 10 and 11 compute the decays of the chunks ahead (one head each) and clear the
-// rows behind a sequence's end, so that nothing of the next sequence is multiplied, not even by
-// zero.  X, C and B rotate through three buffers: the next X goes where C was (free first), the
-// next C where B was, the next B where X was.
+// Roles: warps 0-15 (four warpgroups, the workers) do the element-wise work, warp 16 issues the TMA
+// loads, warp 17 the MMAs, warps 18 and 19 compute the decays of the chunks ahead (one head each)
+// and clear the rows behind a sequence's end, so that nothing of the next sequence is multiplied,
+// not even by zero.  X, C and B rotate through three buffers: the next X goes where C was (free
+// first), the next C where B was, the next B where X was.
 #include <string.h>
 
 #include "kda_serving.cuh"
@@ -45,7 +45,9 @@ namespace {
 using namespace tcx;
 
 constexpr int kQ = 128;          // tokens of a chunk
-constexpr int kThreads = 384;
+constexpr int kWorkerWarps = 16;
+constexpr int kThreads = 32 * (kWorkerWarps + 4);
+constexpr int kLoadWarp = kWorkerWarps, kMmaWarp = kWorkerWarps + 1, kDecayWarp = kWorkerWarps + 2;
 
 // shared memory
 constexpr uint32_t SM_BUF = 0;              // X, C, B: three buffers of [128 rows][2 regions of 64]
@@ -71,7 +73,7 @@ constexpr uint32_t DC_T = 2560;      // log2 decays of the four blocks; then the
 
 // mbarriers, two of each kind: of chunk c the one of its parity, in phase c / 2 (for the two halves
 // of X' the one of the half, in phase c)
-enum Bar : int { FX, FC, FB, PREP, DFREE, DG, DCS, DXP, DDS, DY, AXP, AM, AS, AY, NBAR };
+enum Bar : int { FX, FC, FB, PREP, DFREE, DG, DCS, DXP, DDS, DY, AXP, AM, AS, AY, AO, NBAR };
 
 // TMEM columns
 constexpr uint32_t TM_G = 0, TM_Y = 128, TM_DS = 256, TM_M = 384;
@@ -115,6 +117,30 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ bool elect() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
+// K-step k of a K-major operand: 32 bytes inside a 128-byte row, then the next 64-column region.
+__device__ __forceinline__ constexpr uint32_t k_step(int k) {
+  return (static_cast<uint32_t>(k >> 2) * REG128 + static_cast<uint32_t>(k & 3) * 32u) >> 4;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // The upper halves of two fp32 values: two truncated bf16.
@@ -177,7 +203,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                  const __grid_constant__ CUtensorMap tm_c, const ChunkArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int HEADS = 128 / P;        // heads of a column block
-  constexpr int NT = N / 2;             // state entries of a worker thread
+  constexpr int NT = N / 4;             // state entries of a worker thread
   constexpr uint32_t BC_BYTES = 128 * N * 2;
   const SsmArgs &a = p.a;
   const uint32_t sb = smem_u32(smem);
@@ -204,13 +230,13 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
   if (tid == 0) {
     *s_abort = 0;
     for (int k = 0; k < NBAR; ++k) {
-      const uint32_t count = k == PREP ? 2u : k >= AXP || k == DFREE ? 8u : 1u;
+      const uint32_t count = k == PREP ? 2u : k >= AXP || k == DFREE ? kWorkerWarps : 1u;
       mbar_init(bar(k, 0), count);
       mbar_init(bar(k, 1), count);
     }
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tmem_alloc(sb + SM_MISC, 512);
     tmem_relinquish();
   }
@@ -246,7 +272,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     return STATE_ONLY ? ((c & 1) ? sb + SM_SP : sb + SM_BUF + 2 * BUF_BYTES) : buf(c + 2);
   };
 
-  if (warp == 8) {
+  if (warp == kLoadWarp) {
     if (lane == 0) {
       bool ok = true;
       int c = 0;
@@ -287,65 +313,81 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
       }
     }
     __syncwarp();
-  } else if (warp == 9) {
-    if (lane == 0) {
-      constexpr uint32_t ID_KK = idesc_mma(128, 128, kFmtBF16, kFmtBF16, 0, 0);
-      constexpr uint32_t ID_MX = idesc_mma(128, P, kFmtBF16, kFmtBF16, 0, 1);
-      constexpr uint32_t ID_DS = idesc_mma(128, N, kFmtBF16, kFmtBF16, 1, 1);
-      bool ok = true;
-      for (int c = 0; c < n_chunks && ok; ++c) {
-        if constexpr (!STATE_ONLY) {
-          ok = ok && wait_c(FC, c) && wait_c(FB, c) && wait_c(PREP, c);
-          if (!ok) break;
-          tc_fence_after();
-          issue_mma(tmem + TM_G, buf_c(c), false, REG128, buf_b(c), false, REG128, N / 16, ID_KK, 0);
-          mma_commit(bar(DG, c));
-          ok = wait_c(AS, c) && (c == 0 || wait_c(AY, c - 1));
-          if (!ok) break;
-          tc_fence_after();
-          for (int k = 0; k < 2; ++k)
-            issue_mma(tmem + TM_Y, buf_c(c), false, REG128, sb + SM_SP + k * SP_PLANE, false, REG128,
-                      N / 16, ID_KK, k);
-          mma_commit(bar(DCS, c));
-        } else {
-          ok = wait_c(FB, c) && wait_c(PREP, c) && wait_c(AS, c);
-          if (!ok) break;
-        }
-        for (int half = 0; half < 2; ++half) {
-          ok = wait(bar(AXP, half), c);
-          if (!ok) break;
-          tc_fence_after();
-          for (int k = 0; k < 3; ++k)
-            issue_mma(tmem + TM_DS, sb + SM_XP + k * XP_PLANE, true, REG64, buf_b(c) + half * REG64,
-                      true, REG128, 4, ID_DS, half + k);
-          if (half == 0)
-            mma_commit(bar(DXP, 0));
-          else
-            mma_commit(bar(DDS, c));
-        }
+  } else if (warp == kMmaWarp) {
+    // The whole warp goes through the loop (so that addresses and descriptors stay in uniform
+    // registers); one lane issues.
+    constexpr uint32_t ID_KK = idesc_mma(128, 128, kFmtBF16, kFmtBF16, 0, 0);
+    constexpr uint32_t ID_MX = idesc_mma(128, P, kFmtBF16, kFmtBF16, 0, 1);
+    constexpr uint32_t ID_DS = idesc_mma(128, N, kFmtBF16, kFmtBF16, 1, 1);
+    const bool one = elect();
+    bool ok = true;
+    for (int c = 0; c < n_chunks; ++c) {
+      const uint64_t b_k = sw128_desc(buf_b(c), 16u, 1024u);  // B by rows of n, and by rows of tokens
+      const uint64_t b_mn = sw128_desc(buf_b(c), REG128, 1024u);
+      if constexpr (!STATE_ONLY) {
+        const uint64_t c_k = sw128_desc(buf_c(c), 16u, 1024u);
+        const uint64_t s_k = sw128_desc(sb + SM_SP, 16u, 1024u);
+        ok = warp_wait_c(FC, c) && warp_wait_c(FB, c) && warp_wait_c(PREP, c);
         if (!ok) break;
-        if constexpr (!STATE_ONLY) {
-          ok = wait_c(FX, c) && wait_c(AM, c);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t x_desc = sw128_desc(buf_x(c), REG128, 1024u);
-          for (int h = 0; h < HEADS; ++h)
+        tc_fence_after();
+        if (one) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_f16_ta(tmem + TM_Y + 64 * h, tmem + TM_M + 64 * h + 8 * k,
-                         x_desc + ((h * REG128 + k * 2048u) >> 4), ID_MX, 1);
+          for (int k = 0; k < N / 16; ++k)
+            mma_f16(tmem + TM_G, c_k + k_step(k), b_k + k_step(k), ID_KK, k > 0);
+          mma_commit(bar(DG, c));
+        }
+        ok = warp_wait_c(AS, c) && (c == 0 || warp_wait_c(AY, c - 1));
+        if (!ok) break;
+        tc_fence_after();
+        if (one) {
+#pragma unroll
+          for (int k = 0; k < 2 * (N / 16); ++k)
+            mma_f16(tmem + TM_Y, c_k + k_step(k % (N / 16)),
+                    s_k + k_step(k % (N / 16)) + (k / (N / 16)) * (SP_PLANE >> 4), ID_KK, k > 0);
+          mma_commit(bar(DCS, c));
+        }
+      } else {
+        ok = warp_wait_c(FB, c) && warp_wait_c(PREP, c) && warp_wait_c(AS, c);
+        if (!ok) break;
+      }
+      const uint64_t xp_mn = sw128_desc(sb + SM_XP, REG64, 1024u);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        ok = ok && warp_wait(bar(AXP, half), c);
+        if (ok) {
+          tc_fence_after();
+          if (one) {
+#pragma unroll
+            for (int k = 0; k < 12; ++k)
+              mma_f16(tmem + TM_DS, xp_mn + (((k / 4) * XP_PLANE + (k % 4) * 2048u) >> 4),
+                      b_mn + ((half * REG64 + (k % 4) * 2048u) >> 4), ID_DS, half + k > 0);
+            mma_commit(half == 0 ? bar(DXP, 0) : bar(DDS, c));
+          }
+        }
+      }
+      if (!ok) break;
+      if constexpr (!STATE_ONLY) {
+        ok = warp_wait_c(FX, c) && warp_wait_c(AM, c);
+        if (!ok) break;
+        tc_fence_after();
+        if (one) {
+          const uint64_t x_mn = sw128_desc(buf_x(c), REG128, 1024u);
+#pragma unroll
+          for (int k = 0; k < 8 * HEADS; ++k)
+            mma_f16_ta(tmem + TM_Y + 64 * (k / 8), tmem + TM_M + 64 * (k / 8) + 8 * (k % 8),
+                       x_mn + (((k / 8) * REG128 + (k % 8) * 2048u) >> 4), ID_MX, 1);
           mma_commit(bar(DY, c));
         }
       }
-      if (!ok) {  // MMAs in flight finish before TMEM goes
-        mma_commit(bar(DXP, 1));
-        mbar_wait_bounded(bar(DXP, 1), 0, 1u << 16);
-      }
+    }
+    if (!ok && one) {  // MMAs in flight finish before TMEM goes
+      mma_commit(bar(DXP, 1));
+      mbar_wait_bounded(bar(DXP, 1), 0, 1u << 16);
     }
     __syncwarp();
-  } else if (warp >= 10) {
+  } else if (warp >= kDecayWarp) {
     // decays: lane i has tokens 4 i .. 4 i + 3, eight lanes a block
-    const int hh = warp - 10;
+    const int hh = warp - kDecayWarp;
     const bool mine = hh < heads;
     const float A2 = mine ? a.A[h0 + hh] * 1.44269504088896340736f : 0.f;
     for (int c = 0; c < n_chunks; ++c) {
@@ -413,7 +455,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
       if (len < kQ) {  // clear what lies behind the sequence's end
         if (!warp_wait_c(FX, c) || !warp_wait_c(FB, c)) break;
         const int rows = kQ - len;
-        for (int i = (warp - 10) * 32 + lane; i < rows * 8; i += 64) {
+        for (int i = hh * 32 + lane; i < rows * 8; i += 64) {
           const uint32_t off = static_cast<uint32_t>(len) * 128u + 16u * i;
           for (int r = 0; r < 2; ++r) S.u128(buf_x(c) + r * REG128 + off) = make_uint4(0, 0, 0, 0);
           for (int r = 0; r < N / 64; ++r)
@@ -425,12 +467,12 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
       if (lane == 0) mbar_arrive(bar(PREP, c));
     }
   } else {
-    // ---- the two warpgroups ---------------------------------------------------------------
+    // ---- the workers ----------------------------------------------------------------------
     const int wg = warp >> 2, quad = warp & 3;
     const int row = quad * 32 + lane;  // TMEM lane: token of G, M, Y; column of dS^T
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const int hcol = HEADS == 2 ? quad >> 1 : 0;   // head of this thread's state column
-    const int hout = HEADS == 2 ? wg : 0;          // head of its output columns
+    const int hout = HEADS == 2 ? wg >> 1 : 0;     // head of its output columns [32 wg, 32 wg + 32)
     const bool col_in = hcol < heads, out_in = hout < heads;
     const int n0 = wg * NT;
     const size_t col_at = static_cast<size_t>(h0 + hcol) * N * P + static_cast<size_t>(n0) * P +
@@ -458,7 +500,6 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     }
     // S^T as two bf16 planes, columns as rows of n
     auto put_state = [&]() {
-      constexpr int REGION_N = 64;
 #pragma unroll
       for (int j = 0; j < NT / 8; ++j) {
         uint32_t hi[4], lo[4];
@@ -470,14 +511,23 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
           lo[e] = pack_bf16x2(u - f.x, v - f.y);
         }
         const int n = n0 + 8 * j;
-        const uint32_t at = sb + SM_SP + (n / REGION_N) * REG128 + row * 128u +
-                            (static_cast<uint32_t>(((n % REGION_N) / 8) ^ (row & 7)) << 4);
+        const uint32_t at = sb + SM_SP + (n / 64) * REG128 + row * 128u +
+                            (static_cast<uint32_t>(((n % 64) / 8) ^ (row & 7)) << 4);
         S.u128(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         S.u128(at + SP_PLANE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
       fence_proxy_async();
     };
-    if (!STATE_ONLY) put_state();
+    if constexpr (!STATE_ONLY) {
+      put_state();
+      // weights of later blocks of tokens: zero, once and for all
+      float none[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) none[i] = 0.f;
+      for (int b = quad + 1; b < 4; ++b)
+        if (HEADS == 2 ? (wg & 1) == 0 : wg == 0) tmem_st16(lanes + TM_M + 64 * hout + 16 * b, none);
+      tmem_wait_st();
+    }
     arrive(bar(AS, 0));
     float decay = 1.f;
     const float skip = !STATE_ONLY && a.D && out_in ? a.D[h0 + hout] : 0.f;
@@ -485,119 +535,117 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     for (int c = 0; c < n_chunks; ++c) {
       const int64_t t0 = seg.begin + static_cast<int64_t>(c) * kQ;
       const uint32_t dec = sb + SM_DEC + (c & 1) * 2 * DEC_BYTES;
-      // X' of tokens [64 half, 64 half + 64): a thread takes 8 columns of four rows
-      auto put_weighted = [&](int half) {
-        const int j = tid & 7;
+      if (!warp_wait_c(PREP, c) || !warp_wait_c(FX, c)) break;
+      // X' overwrites what other warps staged of the last output
+      if (!STATE_ONLY && c > 0 && !warp_wait_c(AO, c - 1)) break;
+      bool ok = true;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        if (half == 1 && !(ok = warp_wait(bar(DXP, 0), c))) break;
+        // X' of tokens [64 half, 64 half + 64): a thread takes 8 columns of each region of a row
+        const int j = tid & 7, tok = tid >> 3;
+        const uint32_t off = tok * 128u + (static_cast<uint32_t>(j ^ (tok & 7)) << 4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int region = i & 1, tok = (tid >> 3) + 32 * (i >> 1);
-          const uint32_t off = (static_cast<uint32_t>(j ^ (tok & 7)) << 4);
+        for (int region = 0; region < 2; ++region) {
           const float w = S.f32(dec + (HEADS == 2 ? region : 0) * DEC_BYTES + DC_W +
                                 4 * (64 * half + tok));
-          const uint4 raw = S.u128(buf_x(c) + region * REG128 + (64 * half + tok) * 128u + off);
+          const uint4 raw = S.u128(buf_x(c) + region * REG128 + half * REG64 + off);
           const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+          const float2 w2 = make_float2(w, w);
           uint32_t out[3][4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float2 f = unpack_bf16x2(in[e]);
-            f.x *= w;
-            f.y *= w;
+            float2 f = __fmul2_rn(unpack_bf16x2(in[e]), w2);
             out[0][e] = upper(f.x, f.y);
-            f.x -= truncated(f.x);
-            f.y -= truncated(f.y);
+            f = __fadd2_rn(f, make_float2(-truncated(f.x), -truncated(f.y)));
             out[1][e] = upper(f.x, f.y);
-            f.x -= truncated(f.x);
-            f.y -= truncated(f.y);
+            f = __fadd2_rn(f, make_float2(-truncated(f.x), -truncated(f.y)));
             out[2][e] = upper(f.x, f.y);
           }
-          const uint32_t to = sb + SM_XP + region * REG64 + tok * 128u + off;
+          const uint32_t to = sb + SM_XP + region * REG64 + off;
 #pragma unroll
           for (int k = 0; k < 3; ++k)
             S.u128(to + k * XP_PLANE) = make_uint4(out[k][0], out[k][1], out[k][2], out[k][3]);
         }
         fence_proxy_async();
         arrive(bar(AXP, half));
-      };
 
-      if (!warp_wait_c(PREP, c) || !warp_wait_c(FX, c)) break;
-      put_weighted(0);
-
-      if constexpr (!STATE_ONLY) {
-        if (!warp_wait_c(DG, c)) break;
-        tc_fence_after();
-        // M: causal weights of the tokens, 32 at a time
-        const uint32_t d = dec + hout * DEC_BYTES;
-        const float lt = S.f32(d + DC_L + 4 * row);
-        constexpr int BLOCKS = HEADS == 2 ? 4 : 2;
-#pragma unroll
-        for (int k = 0; k < BLOCKS; ++k) {
-          const int b = HEADS == 2 ? k : 2 * wg + k;  // block of s
-          float m[32];
-          if (b > quad) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) m[i] = 0.f;
-          } else {
+        if constexpr (!STATE_ONLY) {
+          if (half == 1) break;
+          if (!(ok = warp_wait_c(DG, c))) break;
+          tc_fence_after();
+          // M: causal weights of the tokens, 32 at a time
+          const uint32_t d = dec + hout * DEC_BYTES;
+          const float lt = S.f32(d + DC_L + 4 * row);
+#pragma unroll 1
+          for (int k = 0; k < (HEADS == 2 ? 2 : 1); ++k) {
+            const int b = HEADS == 1 ? wg : k == 0 ? wg & 1 : 3 - (wg & 1);  // block of s
+            if (b > quad) continue;
+            float m[32];
             tmem_ld32(lanes + TM_G + 32 * b, m);
             tmem_wait_ld();
+            uint32_t packed[16];
             if (b < quad) {
               float l = lt;  // from the block's end to t
               for (int q = b + 1; q < quad; ++q) l += S.f32(d + DC_T + 4 * q);
               const float e = ex2(l);
+              const float2 e2 = make_float2(e, e);
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
                 const float4 f = *reinterpret_cast<const float4 *>(S.ptr(d + DC_F + 4 * (32 * b + i)));
-                m[i] *= f.x * e;
-                m[i + 1] *= f.y * e;
-                m[i + 2] *= f.z * e;
-                m[i + 3] *= f.w * e;
+                const float2 u = __fmul2_rn(make_float2(m[i], m[i + 1]),
+                                            __fmul2_rn(make_float2(f.x, f.y), e2));
+                const float2 v = __fmul2_rn(make_float2(m[i + 2], m[i + 3]),
+                                            __fmul2_rn(make_float2(f.z, f.w), e2));
+                packed[i / 2] = pack_bf16x2(u.x, u.y);
+                packed[i / 2 + 1] = pack_bf16x2(v.x, v.y);
               }
             } else {
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
                 const float4 l = *reinterpret_cast<const float4 *>(S.ptr(d + DC_L + 4 * (32 * b + i)));
                 const float4 w = *reinterpret_cast<const float4 *>(S.ptr(d + DC_DT + 4 * (32 * b + i)));
-                m[i] = i <= lane ? m[i] * (ex2(lt - l.x) * w.x) : 0.f;
-                m[i + 1] = i + 1 <= lane ? m[i + 1] * (ex2(lt - l.y) * w.y) : 0.f;
-                m[i + 2] = i + 2 <= lane ? m[i + 2] * (ex2(lt - l.z) * w.z) : 0.f;
-                m[i + 3] = i + 3 <= lane ? m[i + 3] * (ex2(lt - l.w) * w.w) : 0.f;
+                const float u0 = i <= lane ? m[i] * (ex2(lt - l.x) * w.x) : 0.f;
+                const float u1 = i + 1 <= lane ? m[i + 1] * (ex2(lt - l.y) * w.y) : 0.f;
+                const float u2 = i + 2 <= lane ? m[i + 2] * (ex2(lt - l.z) * w.z) : 0.f;
+                const float u3 = i + 3 <= lane ? m[i + 3] * (ex2(lt - l.w) * w.w) : 0.f;
+                packed[i / 2] = pack_bf16x2(u0, u1);
+                packed[i / 2 + 1] = pack_bf16x2(u2, u3);
               }
             }
-          }
-          float packed[16];
+            float words[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            packed[i] = __uint_as_float(pack_bf16x2(m[2 * i], m[2 * i + 1]));
-          tmem_st16(lanes + TM_M + 64 * hout + 16 * b, packed);
+            for (int i = 0; i < 16; ++i) words[i] = __uint_as_float(packed[i]);
+            tmem_st16(lanes + TM_M + 64 * hout + 16 * b, words);
+          }
         }
       }
-
-      if (!warp_wait(bar(DXP, 0), c)) break;
-      put_weighted(1);
+      if (!ok) break;
 
       if constexpr (!STATE_ONLY) {
         if (!warp_wait_c(DCS, c)) break;
         tc_fence_after();
         // C S, scaled to each token, and D x
         const float e = S.f32(dec + hout * DEC_BYTES + DC_E + 4 * row);
+        const float2 e2 = make_float2(e, e), skip2 = make_float2(skip, skip);
+        float y[32];
+        tmem_ld32(lanes + TM_Y + 32 * wg, y);
+        tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float y[32];
-          tmem_ld32(lanes + TM_Y + 64 * wg + 32 * k, y);
-          tmem_wait_ld();
+        for (int j = 0; j < 4; ++j) {
+          const uint4 raw = S.u128(buf_x(c) + (wg >> 1) * REG128 + row * 128u +
+                                   (static_cast<uint32_t>((4 * (wg & 1) + j) ^ (row & 7)) << 4));
+          const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 raw = S.u128(buf_x(c) + wg * REG128 + row * 128u +
-                                     (static_cast<uint32_t>((4 * k + j) ^ (row & 7)) << 4));
-            const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float2 f = unpack_bf16x2(in[q]);
-              y[8 * j + 2 * q] = fmaf(e, y[8 * j + 2 * q], skip * f.x);
-              y[8 * j + 2 * q + 1] = fmaf(e, y[8 * j + 2 * q + 1], skip * f.y);
-            }
+          for (int q = 0; q < 4; ++q) {
+            const int i = 8 * j + 2 * q;
+            const float2 f = __ffma2_rn(e2, make_float2(y[i], y[i + 1]),
+                                        __fmul2_rn(skip2, unpack_bf16x2(in[q])));
+            y[i] = f.x;
+            y[i + 1] = f.y;
           }
-          tmem_st32(lanes + TM_Y + 64 * wg + 32 * k, y);
         }
+        tmem_st32(lanes + TM_Y + 32 * wg, y);
         tmem_wait_st();
         tc_fence_before();
         arrive(bar(AM, c));
@@ -606,15 +654,30 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
       // the state behind this chunk
       if (!warp_wait_c(DDS, c)) break;
       tc_fence_after();
+      // X' is free from here on: each warp stages 32 rows of 64 bytes of z, then of o, there
+      const uint32_t stage = sb + SM_XP + warp * 2048u;
+      const int64_t rows_left = seg.len - static_cast<int64_t>(c) * kQ - quad * 32;
+      const int64_t first = t0 + quad * 32, cols = static_cast<int64_t>(h0) * P + 32 * wg;
+      if (!STATE_ONLY && a.z && out_in) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * i + (lane >> 2), j = lane & 3;
+          if (r < rows_left)
+            cp_async16(stage + r * 64u + ((j ^ ((r >> 1) & 3)) << 4),
+                       a.z + (first + r) * a.ldz + cols + 8 * j);
+        }
+      }
       const float keep = S.f32(dec + hcol * DEC_BYTES + DC_T + 16);
       decay *= keep;
-#pragma unroll
-      for (int k = 0; k < NT / 32; ++k) {
-        float v[32];
-        tmem_ld32(lanes + TM_DS + n0 + 32 * k, v);
+      {
+        float v[NT];
+        if constexpr (NT == 32)
+          tmem_ld32(lanes + TM_DS + n0, v);
+        else
+          tmem_ld16(lanes + TM_DS + n0, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s[32 * k + i] = fmaf(keep, s[32 * k + i], v[i]);
+        for (int i = 0; i < NT; ++i) s[i] = fmaf(keep, s[i], v[i]);
       }
       tc_fence_before();
       if (!STATE_ONLY && c + 1 < n_chunks) put_state();
@@ -622,43 +685,45 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
       if (lane == 0) mbar_arrive(bar(DFREE, c));
 
       if constexpr (!STATE_ONLY) {
-        const bool live = out_in && static_cast<int64_t>(c) * kQ + row < seg.len;
-        const int64_t cols = static_cast<int64_t>(h0) * P + 64 * wg;
-        uint4 z[8];
-        if (a.z && live) {
-          const uint4 *from = reinterpret_cast<const uint4 *>(a.z + (t0 + row) * a.ldz + cols);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) z[j] = from[j];
+        if (a.z) {
+          cp_async_wait_all();
+          __syncwarp();
         }
         if (!warp_wait_c(DY, c)) break;
         tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float y[32];
-          tmem_ld32(lanes + TM_Y + 64 * wg + 32 * k, y);
-          tmem_wait_ld();
-          if (live) {
-            uint4 *to = reinterpret_cast<uint4 *>(a.o + (t0 + row) * a.ldo + cols);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (a.z) {
-                const uint4 zz = z[4 * k + j];
-                const uint32_t in[4] = {zz.x, zz.y, zz.z, zz.w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const float2 f = unpack_bf16x2(in[q]);
-                  y[8 * j + 2 * q] *= silu(f.x);
-                  y[8 * j + 2 * q + 1] *= silu(f.y);
-                }
-              }
-              to[4 * k + j] = make_uint4(
-                  pack_bf16x2(y[8 * j], y[8 * j + 1]), pack_bf16x2(y[8 * j + 2], y[8 * j + 3]),
-                  pack_bf16x2(y[8 * j + 4], y[8 * j + 5]), pack_bf16x2(y[8 * j + 6], y[8 * j + 7]));
-            }
-          }
-        }
+        float y[32];
+        tmem_ld32(lanes + TM_Y + 32 * wg, y);
+        tmem_wait_ld();
         tc_fence_before();
         arrive(bar(AY, c));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t at = stage + lane * 64u + ((j ^ ((lane >> 1) & 3)) << 4);
+          if (a.z) {
+            const uint4 raw = S.u128(at);
+            const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float2 f = unpack_bf16x2(in[q]);
+              y[8 * j + 2 * q] *= f.x * rcp(1.f + ex2(-1.44269504088896340736f * f.x));
+              y[8 * j + 2 * q + 1] *= f.y * rcp(1.f + ex2(-1.44269504088896340736f * f.y));
+            }
+          }
+          S.u128(at) = make_uint4(
+              pack_bf16x2(y[8 * j], y[8 * j + 1]), pack_bf16x2(y[8 * j + 2], y[8 * j + 3]),
+              pack_bf16x2(y[8 * j + 4], y[8 * j + 5]), pack_bf16x2(y[8 * j + 6], y[8 * j + 7]));
+        }
+        __syncwarp();
+        if (out_in) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2), j = lane & 3;
+            if (r < rows_left)
+              *reinterpret_cast<uint4 *>(a.o + (first + r) * a.ldo + cols + 8 * j) =
+                  S.u128(stage + r * 64u + ((j ^ ((r >> 1) & 3)) << 4));
+          }
+        }
+        arrive(bar(AO, c));
       }
     }
     if (!*s_abort && col_in) {
@@ -676,7 +741,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

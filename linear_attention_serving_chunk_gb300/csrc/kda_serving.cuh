@@ -83,10 +83,12 @@ struct VerifyArgs {
 };
 
 // The step of one token: dt after bias and softplus.
+__device__ __forceinline__ float ssm_step(const SsmArgs &a, float raw, int h) {
+  if (a.dt_bias) raw += a.dt_bias[h];
+  return a.softplus ? softplus(raw) : raw;
+}
 __device__ __forceinline__ float ssm_dt(const SsmArgs &a, int64_t t, int h) {
-  float d = bf2f(a.dt[t * a.lddt + h]);
-  if (a.dt_bias) d += a.dt_bias[h];
-  return a.softplus ? softplus(d) : d;
+  return ssm_step(a, bf2f(a.dt[t * a.lddt + h]), h);
 }
 
 int *status_word(cudaStream_t st);

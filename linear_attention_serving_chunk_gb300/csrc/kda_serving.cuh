@@ -39,9 +39,22 @@ __device__ __forceinline__ bool run_range(const Runs &r, int s, int64_t &begin, 
   return ok;
 }
 
-// x / (1 + exp(-x)).  exp overflows to +inf for x < -88 and gives -0, x = -inf gives NaN as the
-// formula does.
-__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 1 / (1 + exp(-x)): two approximations of 2^-22 and 2^-23 relative; exp overflows to +inf for
+// x < -88, which gives 0.
+__device__ __forceinline__ float sigmoid(float x) {
+  return rcp(1.f + ex2(-1.44269504088896340736f * x));
+}
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 
 // log(1 + exp(x)); beyond 20 the difference to x is under half a unit in the last place.
 __device__ __forceinline__ float softplus(float x) { return x > 20.f ? x : log1pf(expf(x)); }

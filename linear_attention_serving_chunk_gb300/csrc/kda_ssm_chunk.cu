@@ -113,18 +113,6 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ bool elect() {
   uint32_t one;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
@@ -705,8 +693,8 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const float2 f = unpack_bf16x2(in[q]);
-              y[8 * j + 2 * q] *= f.x * rcp(1.f + ex2(-1.44269504088896340736f * f.x));
-              y[8 * j + 2 * q + 1] *= f.y * rcp(1.f + ex2(-1.44269504088896340736f * f.y));
+              y[8 * j + 2 * q] *= silu(f.x);
+              y[8 * j + 2 * q + 1] *= silu(f.y);
             }
           }
           S.u128(at) = make_uint4(

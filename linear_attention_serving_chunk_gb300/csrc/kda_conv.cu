@@ -6,16 +6,20 @@
 // with the W - 1 held rows (or zeros) in front of a sequence's first token.  Both kernels are bound
 // by memory: x is read once and o written once.  A thread owns VEC neighbouring channels (one
 // 16-byte vector where the layout allows it) and walks along the tokens with the last W - 1 rows in
-// registers.  It takes AHEAD tokens at a time (8 of a prompt, 4 of a run, 1 alone): their loads
-// are all in flight before the first is used, and each row is widened to fp32 once for the W outputs that it enters.  The arithmetic is
-// packed fp32x2 over channel pairs.
+// registers.  It takes AHEAD tokens at a time (4 of a prompt or a run, 1 alone); a prompt's next 4 rows
+// are in flight while the present ones are worked on (without that: 110 us instead of 98 at 32768 x
+// 4352), and each row is widened to fp32 once for the W outputs that it enters.  The arithmetic is
+// packed fp32x2 over channel pairs.  At that size the kernel moves 5.8 TB/s, 0.86 of a plain copy; the
+// exponential and the reciprocal of silu take 0.6 of its time on their pipe.
 #include "kda_serving.cuh"
 
 namespace kda {
 
 namespace {
 
-constexpr int kConvThreads = 128;
+// One warp to a CTA: 20 CTAs of 32 threads and 102 registers took 98 us for 32768 x 4352 tokens x
+// channels, 5 of 128 threads 105 us: the tiles of a long prompt end more evenly.
+constexpr int kConvThreads = 32;
 
 template <int VEC>
 struct Row {  // VEC bf16 channels of one row, two to a word (one alone: the lower half)
@@ -161,9 +165,9 @@ __device__ __forceinline__ int first_sequence(const Runs &r, int64_t t) {
 // Packed prompts.  Block = (tile, channels), channels fastest: `tile_tokens` tokens from
 // tile * tile_tokens on; the blocks behind the tiles write one sequence's final rows each.
 template <int W, int VEC>
-__global__ void __launch_bounds__(kConvThreads, 4)
+__global__ void __launch_bounds__(kConvThreads, 20)
 conv_fwd_kernel(const ConvArgs a, int c_blocks, int64_t tiles, int tile_tokens) {
-  constexpr int AHEAD = 8;
+  constexpr int AHEAD = 4;
   const int64_t tile = blockIdx.x / c_blocks;
   const int c = (static_cast<int>(blockIdx.x % c_blocks) * kConvThreads + threadIdx.x) * VEC;
   if (tile >= tiles) {
@@ -197,20 +201,27 @@ conv_fwd_kernel(const ConvArgs a, int c_blocks, int64_t tiles, int tile_tokens) 
       continue;
     }
     const int64_t end = begin + len < t_end ? begin + len : t_end;
-    Row<VEC> held[W - 1], x[AHEAD];
+    Row<VEC> held[W - 1], x[AHEAD], next[AHEAD];
 #pragma unroll
     for (int k = 0; k < W - 1; ++k)
       held[k] = earlier_row<W, VEC>(a, s, t, t - begin, W - 1 - k, c);
     const kda_bf16 *in = a.x + t * a.ldx + c;
     kda_bf16 *out = a.o + t * a.ldo + c;
-    for (; t < end; t += AHEAD, in += AHEAD * a.ldx, out += AHEAD * a.ldo) {
-      const int n = end - t < AHEAD ? static_cast<int>(end - t) : AHEAD;
+    int left = static_cast<int>(end - t);
+    auto load = [&](Row<VEC> (&to)[AHEAD], int n) {
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i) x[i] = i < n ? load_row<VEC>(in + i * a.ldx) : zero_row<VEC>();
+      for (int i = 0; i < AHEAD; ++i) to[i] = i < n ? load_row<VEC>(in + i * a.ldx) : zero_row<VEC>();
+      in += AHEAD * a.ldx;
+    };
+    load(x, left);
+    for (; left > 0; left -= AHEAD, out += AHEAD * a.ldo) {
+      load(next, left - AHEAD);
       taps.apply(held, x, a.act);  // (after a last, shorter step `held` is not used any more)
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i)
-        if (i < n) store_row<VEC>(out + i * a.ldo, x[i]);
+      for (int i = 0; i < AHEAD; ++i) {
+        if (i < left) store_row<VEC>(out + i * a.ldo, x[i]);
+        x[i] = next[i];
+      }
     }
     t = end;
     if (t < t_end) ++s;

@@ -10,14 +10,15 @@
 // a lane adds its elements in pairs of fp32 (the value and what its rounding lost; double-precision
 // adds run at 2 per SM and cycle here, below the rate at which elements arrive), everything above a
 // lane is in double precision.  The row is cut into segments of kSeg elements whose sums stay in
-// shared memory; the segment that the target falls into is read a second time, from L2.
+// shared memory; the segment that the target falls into is read a second time, from L2, 32
+// neighbouring elements a lane, and then the 32 of the lane that it falls into, one a lane.
 #include "kda_serving.cuh"
 
 namespace kda {
 
 namespace {
 
-constexpr int kVThreads = 512;
+constexpr int kVThreads = 256;
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kSeg = 1024;
 
@@ -31,9 +32,11 @@ __device__ __forceinline__ unsigned cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // A double in the shared memory of CTA `rank` of this cluster, at this CTA's address `p`.
 __device__ __forceinline__ double peer_load(const double *p, unsigned rank) {
@@ -54,15 +57,14 @@ struct Weights {
   int without;  // -1: none
 
   // w = hi + lo: the rounded difference, and what its rounding lost
-  __device__ __forceinline__ void at(float pv, float qv, int i, float &hi, float &lo) const {
+  static __device__ __forceinline__ void weight(float pv, float qv, float &hi, float &lo) {
     hi = fmaxf(pv - qv, 0.f);
     lo = hi > 0.f ? (pv - hi) - qv : 0.f;
-    if (i == without || !(pv >= 0.f)) hi = lo = 0.f;
   }
   __device__ __forceinline__ double one(int i) const {
     float hi, lo;
-    at(prob(p, i), q ? prob(q, i) : 0.f, i, hi, lo);
-    return static_cast<double>(hi) + static_cast<double>(lo);
+    weight(prob(p, i), q ? prob(q, i) : 0.f, hi, lo);
+    return i == without ? 0.0 : static_cast<double>(hi) + static_cast<double>(lo);
   }
 };
 
@@ -93,37 +95,51 @@ __device__ __forceinline__ double warp_scan(double v, int lane) {
   return v;
 }
 
-// One lane's elements of segment [i0, i1): vectors of 16 bytes, the lanes side by side.
-template <typename T, bool VECTOR>
-__device__ __forceinline__ double segment_sum(const Weights<T> &w, int i0, int i1, int lane) {
+// One lane's elements of segment [i0, i0 + kSeg) of the row: SPREAD, vectors of the 32 lanes side by
+// side; otherwise 32 neighbouring ones a lane.
+template <typename T, bool VECTOR, bool SPREAD>
+__device__ __forceinline__ double segment_sum(const Weights<T> &w, int i0, int V, int lane) {
   Sum s;
   if constexpr (VECTOR) {
-    constexpr int E = 16 / sizeof(T);
+    constexpr int E = 16 / sizeof(T), STEPS = kSeg / (32 * E), AHEAD = STEPS < 4 ? STEPS : 4;
+    const int first = i0 + lane * (SPREAD ? E : 32);
+    constexpr int STEP = SPREAD ? 32 * E : E;
 #pragma unroll
-    for (int k = 0; k < kSeg / (32 * E); ++k) {
-      const int i = i0 + (k * 32 + lane) * E;
-      if (i < i1) {
-        T pv[E], qv[E] = {};
-        *reinterpret_cast<uint4 *>(pv) = __ldg(reinterpret_cast<const uint4 *>(w.p + i));
-        if (w.q) *reinterpret_cast<uint4 *>(qv) = __ldg(reinterpret_cast<const uint4 *>(w.q + i));
+    for (int k0 = 0; k0 < STEPS; k0 += AHEAD) {
+      uint4 pv[AHEAD], qv[AHEAD];
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        const int i = first + (k0 + k) * STEP;
+        pv[k] = qv[k] = make_uint4(0, 0, 0, 0);
+        if (i < V) {
+          pv[k] = __ldg(reinterpret_cast<const uint4 *>(w.p + i));
+          if (w.q) qv[k] = __ldg(reinterpret_cast<const uint4 *>(w.q + i));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k)
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           float hi, lo;
-          w.at(prob(pv, e), prob(qv, e), i + e, hi, lo);
+          Weights<T>::weight(prob(reinterpret_cast<const T *>(&pv[k]), e),
+                             prob(reinterpret_cast<const T *>(&qv[k]), e), hi, lo);
           s.add(hi, lo);
         }
-      }
     }
   } else {
 #pragma unroll 8
     for (int k = 0; k < kSeg / 32; ++k) {
-      const int i = i0 + k * 32 + lane;
-      if (i < i1) {
-        float hi, lo;
-        w.at(prob(w.p, i), w.q ? prob(w.q, i) : 0.f, i, hi, lo);
-        s.add(hi, lo);
-      }
+      const int i = i0 + (SPREAD ? k * 32 + lane : lane * 32 + k);
+      float hi = 0.f, lo = 0.f;
+      if (i < V) Weights<T>::weight(prob(w.p, i), w.q ? prob(w.q, i) : 0.f, hi, lo);
+      s.add(hi, lo);
     }
+  }
+  // the token that is taken out, by the lane that added it
+  const int out = w.without - i0;
+  if (out >= 0 && out < kSeg) {
+    constexpr int E = VECTOR ? 16 / sizeof(T) : 1;
+    if (lane == (SPREAD ? out / E % 32 : out / 32)) s.add(-fmaxf(prob(w.p, w.without), 0.f), 0.f);
   }
   return s.value();
 }
@@ -184,10 +200,10 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(const VerifyArgs a) {
   double total = 0.0, before = 0.0;
   for (int pass = 0; pass < 2; ++pass) {
     for (int s = seg0 + warp; s < seg1; s += kVWarps) {
-      const int i0 = s * kSeg, i1 = i0 + kSeg < a.V ? i0 + kSeg : a.V;
-      const double v = warp_sum(segment_sum<T, VECTOR>(w, i0, i1, lane));
+      const double v = warp_sum(segment_sum<T, VECTOR, true>(w, s * kSeg, a.V, lane));
       if (lane == 0) s_seg[s - seg0] = v;
     }
+    if (pass > 0) cluster_wait();  // every CTA has read the first totals
     __syncthreads();
     if (warp == 0) {
       double sum = 0.0;
@@ -196,13 +212,15 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(const VerifyArgs a) {
                            warp_scan(s + lane < seg1 - seg0 ? s_seg[s + lane] : 0.0, lane), 31);
       if (lane == 0) s_total = sum;
     }
-    cluster_sync();
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
     total = before = 0.0;
     for (unsigned r = 0; r < ranks; ++r) {
       if (r == rank) before = total;
       total += peer_load(&s_total, r);
     }
-    cluster_sync();
+    cluster_arrive();  // waited for before s_total goes
     if (total > 0.0 || (!w.q && w.without < 0)) break;
     w.q = nullptr;  // nothing is left of the row: the target's own weights
     w.without = -1;
@@ -213,50 +231,42 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(const VerifyArgs a) {
       a.out_tokens[t0 + got] = -1;
       a.n_out[b] = got;
     }
-    return;
-  }
-  if (warp != 0) return;
-  const float u = a.u[t1 - 1];
-  const double want = static_cast<double>(u >= 0.f ? fminf(u, 0x1.fffffep-1f) : 0.f) * total;
-  // the CTA whose part of the row holds it
-  if (!(want >= before && want < before + s_total)) return;
-  double sum = before;
-  int seg = -1;
-  for (int s = 0; s < seg1 - seg0 && seg < 0; s += 32) {
-    const double c = warp_scan(s + lane < seg1 - seg0 ? s_seg[s + lane] : 0.0, lane);
-    const unsigned m = __ballot_sync(0xffffffffu, sum + c > want);
-    if (m) {
-      seg = s + __ffs(m) - 1;
-      const double prev = __shfl_sync(0xffffffffu, c, (__ffs(m) + 30) & 31);
-      if (__ffs(m) > 1) sum += prev;
-    } else {
-      sum += __shfl_sync(0xffffffffu, c, 31);
+  } else if (warp == 0) {
+    const float u = a.u[t1 - 1];
+    const double want = static_cast<double>(u >= 0.f ? fminf(u, 0x1.fffffep-1f) : 0.f) * total;
+    // the CTA whose part of the row holds it
+    if (want >= before && want < before + s_total) {
+      double sum = before;
+      int seg = -1;
+      for (int s = 0; s < seg1 - seg0 && seg < 0; s += 32) {
+        const double c = warp_scan(s + lane < seg1 - seg0 ? s_seg[s + lane] : 0.0, lane);
+        const unsigned m = __ballot_sync(0xffffffffu, sum + c > want);
+        const int at = m ? __ffs(m) - 1 : 32;  // lanes in front of it count in full
+        const double front = __shfl_sync(0xffffffffu, c, (at + 31) & 31);
+        if (m) seg = s + at;
+        if (at > 0) sum += front;
+      }
+      if (seg < 0) seg = seg1 - seg0 - 1;  // rounding of the sums alone
+      const int i0 = (seg0 + seg) * kSeg;
+      double mine = segment_sum<T, VECTOR, false>(w, i0, a.V, lane);
+      double c = warp_scan(mine, lane);
+      unsigned over = __ballot_sync(0xffffffffu, mine > 0.0 && sum + c > want);
+      unsigned some = __ballot_sync(0xffffffffu, mine > 0.0);
+      const int from = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : 0;
+      sum += __shfl_sync(0xffffffffu, c - mine, from);
+      const int i = i0 + from * 32 + lane;
+      mine = i < a.V ? w.one(i) : 0.0;
+      c = warp_scan(mine, lane);
+      over = __ballot_sync(0xffffffffu, mine > 0.0 && sum + c > want);
+      some = __ballot_sync(0xffffffffu, mine > 0.0);
+      if (lane == (over ? __ffs(over) - 1 : some ? 31 - __clz(some) : 0)) {
+        a.out_tokens[t0 + got] = i;
+        a.n_out[b] = got + 1;
+      }
     }
   }
-  if (seg < 0) seg = seg1 - seg0 - 1;  // rounding of the sums alone
-  // inside the segment: 32 neighbouring elements per lane
-  const int i0 = (seg0 + seg) * kSeg + lane * 32;
-  double mine = 0.0;
-  for (int i = i0; i < i0 + 32 && i < a.V; ++i) mine += w.one(i);
-  const double c = warp_scan(mine, lane);
-  int token = -1;
-  double run = sum + (c - mine);
-  for (int i = i0; i < i0 + 32 && i < a.V; ++i) {
-    const double v = w.one(i);
-    run += v;
-    if (v > 0.0) {
-      token = i;
-      if (run > want) break;
-    }
-  }
-  // the first lane that passes `want`; else the last element with any weight
-  const unsigned over = __ballot_sync(0xffffffffu, token >= 0 && sum + c > want);
-  const unsigned any = __ballot_sync(0xffffffffu, token >= 0);
-  const int from = over ? __ffs(over) - 1 : 31 - __clz(any);
-  if (lane == from) {
-    a.out_tokens[t0 + got] = token;
-    a.n_out[b] = got + 1;
-  }
+  __syncwarp();
+  cluster_wait();
 }
 
 template <typename T, bool VECTOR>

@@ -7,9 +7,9 @@
 // Bound by memory for short runs: a state is read once and, with commit, written once.  One
 // 256-thread CTA owns one state; TPR = P / 4 threads lie along a row (4 columns each) and 256 / TPR
 // row groups along N, as in the KDA decode step.  The tokens of a run are staged TB at a time (B, C
-// and dt x in fp32), a thread then takes its block of the state through all of them and leaves its
-// part of S^T C per token in shared memory: two barriers per TB tokens.  The arithmetic is packed
-// fp32x2 over column pairs.
+// and x in fp32), a thread then takes its block of the state through all of them and leaves its part
+// of S^T C per token in shared memory: two barriers per TB tokens.  The arithmetic is packed fp32x2
+// over column pairs.
 //
 // A decay near 1 is applied as S + ((a - 1) S + B dt x) with a - 1 from expm1: rounded to fp32, a itself
 // is off by up to 2^-24 the same way at every token, which over the hundreds of tokens that such a
@@ -24,15 +24,15 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
 template <int N, int P, int TB>
-__global__ void __launch_bounds__(kThreads) ssm_tokens_kernel(const SsmArgs a) {
+__global__ void __launch_bounds__(kThreads, N * P <= 8192 ? 4 : 2) ssm_tokens_kernel(const SsmArgs a) {
   constexpr int TPR = P / 4;           // threads along a row
   constexpr int RG = kThreads / TPR;   // row groups
   constexpr int RPT = N / RG;          // rows per thread
   constexpr int RGW = 32 / TPR;        // row groups of one warp
   static_assert(RPT * RG == N && TPR * RG == kThreads, "state tiling");
   __shared__ float2 s_bc[TB][N];       // (B, C)
-  __shared__ float4 s_x[TB][TPR];      // dt x
-  __shared__ float2 s_a[TB];           // S <- k S + (m S + B dt x): (k, m) = (1, a - 1) or (0, a)
+  __shared__ float4 s_x[TB][TPR];
+  __shared__ float4 s_a[TB];           // S <- k S + (m S + B dt x): (k, m) = (1, a - 1) or (0, a); dt
   __shared__ float4 s_part[TB][kWarps][TPR];
 
   const int b = blockIdx.x / a.H, h = blockIdx.x % a.H, g = h / (a.H / a.G);
@@ -60,26 +60,33 @@ __global__ void __launch_bounds__(kThreads) ssm_tokens_kernel(const SsmArgs a) {
     const int nt = used - t0 < TB ? static_cast<int>(used - t0) : TB;
     const int64_t row0 = begin + t0;
     if (t0 > 0) __syncthreads();
-    for (int i = tid; i < nt * N; i += kThreads) {
-      const int t = i / N, n = i % N;
-      s_bc[t][n] = make_float2(bf2f(a.B[(row0 + t) * a.ldb + g * N + n]),
-                               bf2f(a.C[(row0 + t) * a.ldc + g * N + n]));
+    const int mine = tid - kThreads / 2;  // (the ends of the block stage the rows of one token)
+    if (mine >= 0 && mine < nt) {
+      const float dt = ssm_dt(a, row0 + mine, h), m = expm1f(dt * A);
+      s_a[mine] = m > -0.5f ? make_float4(1.f, m, dt, 0.f) : make_float4(0.f, expf(dt * A), dt, 0.f);
     }
-    for (int i = tid; i < nt * P; i += kThreads) {
-      const int t = i / P, p = i % P;
-      const float dt = ssm_dt(a, row0 + t, h);
-      reinterpret_cast<float *>(s_x[t])[p] = dt * bf2f(a.x[(row0 + t) * a.ldx + h * P + p]);
-      if (p == 0) {
-        const float m = expm1f(dt * A);
-        s_a[t] = m > -0.5f ? make_float2(1.f, m) : make_float2(0.f, expf(dt * A));
-      }
+    for (int i = tid; i < nt * (N / 2); i += kThreads) {
+      const int t = i / (N / 2), n = 2 * (i % (N / 2));
+      const uint32_t B = *reinterpret_cast<const uint32_t *>(a.B + (row0 + t) * a.ldb + g * N + n);
+      const uint32_t C = *reinterpret_cast<const uint32_t *>(a.C + (row0 + t) * a.ldc + g * N + n);
+      const float b0 = __uint_as_float(B << 16), b1 = __uint_as_float(B & 0xffff0000u);
+      const float c0 = __uint_as_float(C << 16), c1 = __uint_as_float(C & 0xffff0000u);
+      *reinterpret_cast<float4 *>(&s_bc[t][n]) = make_float4(b0, c0, b1, c1);
+    }
+    for (int i = kThreads - 1 - tid; i < nt * (P / 2); i += kThreads) {
+      const int t = i / (P / 2), p = i % (P / 2);
+      const uint32_t x =
+          reinterpret_cast<const uint32_t *>(a.x + (row0 + t) * a.ldx + h * P)[p];
+      reinterpret_cast<float2 *>(s_x[t])[p] =
+          make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
     }
     __syncthreads();
     for (int t = 0; t < nt; ++t) {
-      const float2 km = s_a[t];
-      const float2 k2 = make_float2(km.x, km.x), m2 = make_float2(km.y, km.y);
-      const float4 x = s_x[t][cg];
-      const float2 x0 = make_float2(x.x, x.y), x1 = make_float2(x.z, x.w);
+      const float4 km = s_a[t], x = s_x[t][cg];
+      const float2 k2 = make_float2(km.x, km.x), m2 = make_float2(km.y, km.y),
+                   dt2 = make_float2(km.z, km.z);
+      const float2 x0 = __fmul2_rn(dt2, make_float2(x.x, x.y)),
+                   x1 = __fmul2_rn(dt2, make_float2(x.z, x.w));
       float2 y0 = make_float2(0.f, 0.f), y1 = y0;
 #pragma unroll
       for (int r = 0; r < RPT; ++r) {
@@ -100,14 +107,22 @@ __global__ void __launch_bounds__(kThreads) ssm_tokens_kernel(const SsmArgs a) {
     }
     __syncthreads();
     if (a.o)
-      for (int i = tid; i < nt * P; i += kThreads) {
-        const int t = i / P, p = i % P;
-        float y = 0.f;
+      for (int i = tid; i < nt * (P / 2); i += kThreads) {
+        const int t = i / (P / 2), p = i % (P / 2);
+        const float2 x = reinterpret_cast<const float2 *>(s_x[t])[p];
+        float2 y = __fmul2_rn(make_float2(D, D), x);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) y += reinterpret_cast<const float *>(s_part[t][w])[p];
-        y = fmaf(D, bf2f(a.x[(row0 + t) * a.ldx + h * P + p]), y);
-        if (a.z) y *= silu(bf2f(a.z[(row0 + t) * a.ldz + h * P + p]));
-        a.o[(row0 + t) * a.ldo + h * P + p] = f2bf(y);
+        for (int w = 0; w < kWarps; ++w)
+          y = __fadd2_rn(y, reinterpret_cast<const float2 *>(s_part[t][w])[p]);
+        if (a.z) {
+          const uint32_t z =
+              reinterpret_cast<const uint32_t *>(a.z + (row0 + t) * a.ldz + h * P)[p];
+          y.x *= silu(__uint_as_float(z << 16));
+          y.y *= silu(__uint_as_float(z & 0xffff0000u));
+        }
+        const __nv_bfloat162 r = __floats2bfloat162_rn(y.x, y.y);
+        reinterpret_cast<uint32_t *>(a.o + (row0 + t) * a.ldo + h * P)[p] =
+            *reinterpret_cast<const uint32_t *>(&r);
       }
   }
   if (a.o)
@@ -126,7 +141,7 @@ cudaError_t run(const SsmArgs &a, bool single, cudaStream_t st) {
   if (single)
     ssm_tokens_kernel<N, P, 1><<<grid, kThreads, 0, st>>>(a);
   else
-    ssm_tokens_kernel<N, P, 8><<<grid, kThreads, 0, st>>>(a);
+    ssm_tokens_kernel<N, P, N * P <= 8192 ? 8 : 4><<<grid, kThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 

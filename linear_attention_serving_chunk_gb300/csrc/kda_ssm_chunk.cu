@@ -13,8 +13,8 @@
 //   dS^T[column x n]     = X'^T B                      X' = e^{l_end - l_s} dt_s x_s
 //
 // Roundings.  x, B and C are bf16 and enter exactly.  X' is split into three bf16 planes that hold
-// all 24 bits of its fp32 value, and the state itself lives in registers in fp32 (S^T: one thread
-// per column and quarter of n), so S and S_final carry fp32 accuracy.  For the output, S enters as two
+// all 24 bits of its fp32 value, and the state itself stays in fp32 registers (S^T: a thread has one
+// column and half of n), so S and S_final carry fp32 accuracy.  For the output, S enters as two
 // planes (16 bits) and M as one (8 bits): the in-chunk weights are rounded once to the type of the
 // result, which adds an error of the size of the result's own rounding.
 //
@@ -28,11 +28,17 @@
 // a of the whole segment; the second pass starts each segment from a_{j-1} (... (a_0 S0 + N_0) ...)
 // + N_{j-1}.
 //
-// Roles: warps 0-15 (four warpgroups, the workers) do the element-wise work, warp 16 issues the TMA
-// loads, warp 17 the MMAs, warps 18 and 19 compute the decays of the chunks ahead (one head each)
-// and clear the rows behind a sequence's end, so that nothing of the next sequence is multiplied,
-// not even by zero.  X, C and B rotate through three buffers: the next X goes where C was (free
-// first), the next C where B was, the next B where X was.
+// Roles, each at its own pace and with its own registers, joined by mbarriers:
+//   state    (8 warps)  X', 32 tokens at a time; the state and its planes for the next chunk
+//   token    (8 warps)  M; Y = e^{l_t} C S + D x before M X is added
+//   output   (8 warps)  gate and store
+//   one warp each       TMA loads; the MMAs of Y; the other MMAs; the decays of the chunks ahead, and
+//                       the rows behind a sequence's end cleared, so that nothing of the next
+//                       sequence is multiplied, not even by zero
+// X has two buffers, C and B have one.  G has two places in TMEM, so that the next chunk's G is there
+// when its M is built; M takes the columns of its G, 32 tokens at a time.  The gate and the result
+// pass through the chunk's X tile once nothing reads it any more.  In the first pass the token warps
+// build X' too, and the output warps keep the state.
 #include <string.h>
 
 #include "kda_serving.cuh"
@@ -45,23 +51,35 @@ namespace {
 using namespace tcx;
 
 constexpr int kQ = 128;          // tokens of a chunk
-constexpr int kWorkerWarps = 16;
-constexpr int kThreads = 32 * (kWorkerWarps + 4);
-constexpr int kLoadWarp = kWorkerWarps, kMmaWarp = kWorkerWarps + 1, kDecayWarp = kWorkerWarps + 2;
+// warps of the roles: whole warpgroups, since a warp reaches the 32 TMEM lanes of its number mod 4
+constexpr int kStateWarps = 8, kTokenWarps = 8, kOutWarps = 8;
+constexpr int kTokenWarp = kStateWarps, kOutWarp = kTokenWarp + kTokenWarps;
+constexpr int kLoadWarp = kOutWarp + kOutWarps, kTokenMma = kLoadWarp + 1, kStateMma = kLoadWarp + 2;
+constexpr int kOthers = 4;  // (the fourth: decays)
+constexpr int kThreads = 32 * (kLoadWarp + kOthers);
+// registers a thread: 72 at launch, then in the second pass
+constexpr int kLaunchRegs = 72, kStateRegs = 96, kTokenRegs = 64, kOutRegs = 64, kOtherRegs = 56;
+static_assert(32 * (kStateWarps * kStateRegs + kTokenWarps * kTokenRegs + kOutWarps * kOutRegs +
+                    kOthers * kOtherRegs) <= kThreads * kLaunchRegs,
+              "a warpgroup would wait for registers that the block does not have");
 
-// shared memory
-constexpr uint32_t SM_BUF = 0;              // X, C, B: three buffers of [128 rows][2 regions of 64]
-constexpr uint32_t BUF_BYTES = 32 * KiB;
-constexpr uint32_t SM_XP = 96 * KiB;        // X': three planes of [64 tokens][2 regions of 64]
-constexpr uint32_t XP_PLANE = 16 * KiB;
-constexpr uint32_t SM_SP = 144 * KiB;       // S^T: two planes of [128 columns][N / 64 regions]
+// shared memory: tiles of [128 rows][2 regions of 64 columns], 128-byte swizzle
+constexpr uint32_t TILE = 32 * KiB;
+constexpr uint32_t SM_X = 0;                // X, two chunks
+constexpr uint32_t SM_B = 2 * TILE;         // (first pass: two chunks)
+constexpr uint32_t SM_C = 3 * TILE;
+constexpr uint32_t SM_XP = 4 * TILE;        // X': [3 planes][2 regions][32 tokens] (first pass: thrice)
+constexpr uint32_t XP_REGION = 4 * KiB, XP_PLANE = 2 * XP_REGION, XP_BYTES = 3 * XP_PLANE;
+constexpr uint32_t SM_SP = SM_XP + XP_BYTES;  // S^T: two planes of [128 columns][N / 64 regions]
 constexpr uint32_t SP_PLANE = 32 * KiB;
-constexpr uint32_t SM_DEC = 208 * KiB;      // decays: [2 chunks][2 heads] of struct Decays
+constexpr uint32_t SM_DEC = SM_SP + 2 * SP_PLANE;  // decays: [2 chunks][2 heads]
 constexpr uint32_t DEC_BYTES = 5 * 512 + 32;
 constexpr uint32_t SM_BAR = SM_DEC + 4 * DEC_BYTES;
-constexpr uint32_t SM_MISC = SM_BAR + 256;
+constexpr uint32_t SM_MISC = SM_BAR + 288;
 constexpr uint32_t SM_BYTES = SM_MISC + 64;
 static_assert(SM_BYTES <= 232448, "shared memory budget");
+static_assert(SM_XP + 3 * XP_BYTES <= SM_DEC, "three X' buffers of the first pass");
+constexpr int kRounds = kQ / 32;            // X' buffers filled for a chunk
 
 // Decays of one (chunk, head): offsets in bytes
 constexpr uint32_t DC_L = 0;         // log2 decay from the 32-token block's start, token included
@@ -71,12 +89,19 @@ constexpr uint32_t DC_E = 1536;      // decay from the chunk's start
 constexpr uint32_t DC_W = 2048;      // decay to the chunk's end, times dt
 constexpr uint32_t DC_T = 2560;      // log2 decays of the four blocks; then the chunk's decay
 
-// mbarriers, two of each kind: of chunk c the one of its parity, in phase c / 2 (for the two halves
-// of X' the one of the half, in phase c)
-enum Bar : int { FX, FC, FB, PREP, DFREE, DG, DCS, DXP, DDS, DY, AXP, AM, AS, AY, AO, NBAR };
+// mbarriers.  Two of each kind: of chunk c the one of its parity, in phase c / 2.  F: a tile has come;
+// D: an MMA is done; A: warps have arrived.  FIN is for a wait that has given up.
+enum Bar : int { FX, FC, FB, PREP, DFREE, DG, DCS, DDS, DY, AM, AS, AY, AO, FIN, NBAR };
+// One for each X' buffer: filled, and read.
+constexpr uint32_t BAR_AXP = SM_BAR + 16 * NBAR, BAR_DXP = BAR_AXP + 24;
+static_assert(BAR_DXP + 24 <= SM_MISC, "barriers");
 
-// TMEM columns
-constexpr uint32_t TM_G = 0, TM_Y = 128, TM_DS = 256, TM_M = 384;
+// TMEM columns: two of G, Y, dS (the first pass: two of dS, and S)
+constexpr uint32_t TM_Y = 256, TM_DS = 384, TM_S = 256;
+// M of head h in the columns of its G: tokens [16 k, 16 k + 16) in 8 of the 32 that held their G
+__device__ __forceinline__ constexpr uint32_t tm_m(int h, int k) {
+  return 32 * (k >> 1) + 16 * h + 8 * (k & 1);
+}
 
 constexpr uint32_t kPolls = 1u << 24;
 
@@ -124,11 +149,14 @@ __device__ __forceinline__ constexpr uint32_t k_step(int k) {
   return (static_cast<uint32_t>(k >> 2) * REG128 + static_cast<uint32_t>(k & 3) * 32u) >> 4;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
+template <int REGS, bool MORE, bool ON>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (!ON)
+    return;
+  else if constexpr (MORE)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
 // The upper halves of two fp32 values: two truncated bf16.
@@ -191,8 +219,9 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                  const __grid_constant__ CUtensorMap tm_c, const ChunkArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int HEADS = 128 / P;        // heads of a column block
-  constexpr int NT = N / 4;             // state entries of a worker thread
   constexpr uint32_t BC_BYTES = 128 * N * 2;
+  constexpr int XP_BUFS = STATE_ONLY ? 3 : 1;
+  constexpr int DECAY_WARPS = STATE_ONLY ? HEADS : 1;  // (the first pass has no MMAs of Y)
   const SsmArgs &a = p.a;
   const uint32_t sb = smem_u32(smem);
   const Smem S{smem, sb};
@@ -213,18 +242,27 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
   const int heads = per_group - first_in_group < HEADS ? 1 : HEADS;
   const int n_chunks = static_cast<int>((seg.len + kQ - 1) / kQ);
 
-  volatile int *s_abort = reinterpret_cast<volatile int *>(smem + SM_MISC + 8);
   auto bar = [&](int kind, int c) { return sb + SM_BAR + 16u * kind + 8u * (c & 1); };
+  auto xp_full = [&](int i) { return sb + BAR_AXP + 8u * (i % XP_BUFS); };
+  auto xp_read = [&](int i) { return sb + BAR_DXP + 8u * (i % XP_BUFS); };
   if (tid == 0) {
-    *s_abort = 0;
     for (int k = 0; k < NBAR; ++k) {
-      const uint32_t count = k == PREP ? 2u : k >= AXP || k == DFREE ? kWorkerWarps : 1u;
+      uint32_t count = 1;
+      if (k == PREP) count = DECAY_WARPS;
+      if (k == DFREE) count = kStateWarps + kTokenWarps + (STATE_ONLY ? kOutWarps : 0);
+      if (k == AM) count = kTokenWarps;
+      if (k == AS) count = kStateWarps;
+      if (k == AY || k == AO) count = kOutWarps;
       mbar_init(bar(k, 0), count);
       mbar_init(bar(k, 1), count);
     }
+    for (int k = 0; k < XP_BUFS; ++k) {
+      mbar_init(xp_full(k), kStateWarps);
+      mbar_init(xp_read(k), 1);
+    }
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kStateMma) {
     tmem_alloc(sb + SM_MISC, 512);
     tmem_relinquish();
   }
@@ -233,15 +271,18 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + SM_MISC);
 
-  // Every wait is bounded; one that gives up ends them all.
+  // Every wait is bounded.  A role whose wait gives up leaves its loop, so those that wait for it give
+  // up too; the loop around a wait stays short, for the roles' code shares the instruction cache.
+  bool gave_up = false;
   auto wait = [&](uint32_t b, uint32_t phase) -> bool {
-    for (uint32_t i = 0; i < kPolls; ++i) {
-      if (mbar_try_wait(b, phase & 1u)) return true;
-      if (*s_abort) return false;
-    }
-    *s_abort = 1;
-    atomicOr(a.status, KDA_ERR_TIMEOUT);
-    return false;
+    uint32_t left = kPolls;
+#pragma unroll 1
+    while (!mbar_try_wait(b, phase & 1u))
+      if (--left == 0) {
+        gave_up = true;
+        return false;
+      }
+    return true;
   };
   auto wait_c = [&](int kind, int c) { return wait(bar(kind, c), static_cast<uint32_t>(c) >> 1); };
   // the same for a whole warp, which goes on or stops as one
@@ -252,327 +293,368 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     return warp_wait(bar(kind, c), static_cast<uint32_t>(c) >> 1);
   };
 
-  // buffers of chunk c
-  auto buf = [&](int i) { return sb + SM_BUF + static_cast<uint32_t>(i % 3) * BUF_BYTES; };
-  auto buf_x = [&](int c) { return STATE_ONLY ? sb + SM_BUF + (c & 1) * BUF_BYTES : buf(c); };
-  auto buf_c = [&](int c) { return buf(c + 1); };
-  auto buf_b = [&](int c) {
-    return STATE_ONLY ? ((c & 1) ? sb + SM_SP : sb + SM_BUF + 2 * BUF_BYTES) : buf(c + 2);
+  // tiles of chunk c
+  auto tile_x = [&](int c) { return sb + SM_X + (c & 1) * TILE; };
+  auto tile_b = [&](int c) { return sb + SM_B + (STATE_ONLY ? (c & 1) * TILE : 0u); };
+  const uint32_t tile_c = sb + SM_C;
+
+  auto arrive = [&](uint32_t b) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b);
   };
 
-  if (warp == kLoadWarp) {
-    if (lane == 0) {
-      bool ok = true;
-      int c = 0;
-      for (; c < n_chunks && ok; ++c) {
-        const int t = static_cast<int>(seg.begin + static_cast<int64_t>(c) * kQ);
-        auto load_x = [&]() {
-          mbar_expect_tx(bar(FX, c), BUF_BYTES);
+  if (warp >= kLoadWarp) {
+    set_registers<kOtherRegs, false, !STATE_ONLY>();
+    if (warp == kLoadWarp) {
+      if (lane == 0) {
+        bool ok = true;
+        int c = 0;
+        for (; c < n_chunks; ++c) {
+          const int t = static_cast<int>(seg.begin + static_cast<int64_t>(c) * kQ);
+          auto load_bc = [&](const CUtensorMap *map, uint32_t to, uint32_t b) {
+            mbar_expect_tx(b, BC_BYTES);
+            for (int r = 0; r < N / 64; ++r)
+              tma_load_2d(to + r * REG128, map, g * N + 64 * r, t, b);
+          };
+          if (c >= 2 && !(ok = wait_c(STATE_ONLY ? DDS : AO, c - 2))) break;
+          mbar_expect_tx(bar(FX, c), TILE);
           for (int r = 0; r < 2; ++r)
-            tma_load_2d(buf_x(c) + r * REG128, &tm_x, h0 * P + 64 * r, t, bar(FX, c));
-        };
-        auto load_bc = [&](const CUtensorMap *map, uint32_t to, uint32_t b) {
-          mbar_expect_tx(b, BC_BYTES);
-          for (int r = 0; r < N / 64; ++r) tma_load_2d(to + r * REG128, map, g * N + 64 * r, t, b);
-        };
-        if constexpr (STATE_ONLY) {
-          if (c >= 2) ok = wait_c(DDS, c - 2);
-          if (!ok) break;
-          load_x();
-          load_bc(&tm_b, buf_b(c), bar(FB, c));
-        } else {
-          if (c > 0) ok = wait_c(DCS, c - 1);
-          if (!ok) break;
-          load_x();
-          if (c > 0) ok = wait_c(DDS, c - 1);
-          if (!ok) break;
-          load_bc(&tm_c, buf_c(c), bar(FC, c));
-          if (c > 0) ok = wait_c(DY, c - 1);
-          if (!ok) break;
-          load_bc(&tm_b, buf_b(c), bar(FB, c));
+            tma_load_2d(tile_x(c) + r * REG128, &tm_x, h0 * P + 64 * r, t, bar(FX, c));
+          if (!STATE_ONLY && c > 0 && !(ok = wait_c(DDS, c - 1))) break;
+          load_bc(&tm_b, tile_b(c), bar(FB, c));
+          if constexpr (!STATE_ONLY) {
+            if (c > 0 && !(ok = wait_c(DCS, c - 1) && wait_c(DG, c - 1))) break;
+            load_bc(&tm_c, tile_c, bar(FC, c));
+          }
+        }
+        if (!ok) {  // what is in flight lands before the shared memory goes
+          for (int k = c > 1 ? c - 2 : 0; k <= c && k < n_chunks; ++k) {
+            mbar_wait_bounded(bar(FX, k), (k >> 1) & 1, 1u << 16);
+            mbar_wait_bounded(bar(FB, k), (k >> 1) & 1, 1u << 16);
+            if (!STATE_ONLY) mbar_wait_bounded(bar(FC, k), (k >> 1) & 1, 1u << 16);
+          }
         }
       }
-      if (!ok) {  // what is in flight lands before the shared memory goes
-        for (int k = c > 1 ? c - 2 : 0; k <= c && k < n_chunks; ++k) {
-          mbar_wait_bounded(bar(FX, k), (k >> 1) & 1, 1u << 16);
-          mbar_wait_bounded(bar(FB, k), (k >> 1) & 1, 1u << 16);
-          if (!STATE_ONLY) mbar_wait_bounded(bar(FC, k), (k >> 1) & 1, 1u << 16);
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // The whole warp goes through the loop (so that addresses and descriptors stay in uniform
-    // registers); one lane issues.
-    constexpr uint32_t ID_KK = idesc_mma(128, 128, kFmtBF16, kFmtBF16, 0, 0);
-    constexpr uint32_t ID_MX = idesc_mma(128, P, kFmtBF16, kFmtBF16, 0, 1);
-    constexpr uint32_t ID_DS = idesc_mma(128, N, kFmtBF16, kFmtBF16, 1, 1);
-    const bool one = elect();
-    bool ok = true;
-    for (int c = 0; c < n_chunks; ++c) {
-      const uint64_t b_k = sw128_desc(buf_b(c), 16u, 1024u);  // B by rows of n, and by rows of tokens
-      const uint64_t b_mn = sw128_desc(buf_b(c), REG128, 1024u);
-      if constexpr (!STATE_ONLY) {
-        const uint64_t c_k = sw128_desc(buf_c(c), 16u, 1024u);
-        const uint64_t s_k = sw128_desc(sb + SM_SP, 16u, 1024u);
-        ok = warp_wait_c(FC, c) && warp_wait_c(FB, c) && warp_wait_c(PREP, c);
-        if (!ok) break;
-        tc_fence_after();
-        if (one) {
-#pragma unroll
-          for (int k = 0; k < N / 16; ++k)
-            mma_f16(tmem + TM_G, c_k + k_step(k), b_k + k_step(k), ID_KK, k > 0);
-          mma_commit(bar(DG, c));
-        }
-        ok = warp_wait_c(AS, c) && (c == 0 || warp_wait_c(AY, c - 1));
+    } else if (warp == kTokenMma && !STATE_ONLY) {
+      // A whole warp goes through an MMA loop (so that addresses and descriptors stay in uniform
+      // registers); one lane issues.
+      constexpr uint32_t ID_CS = idesc_mma(128, 128, kFmtBF16, kFmtBF16, 0, 0);
+      constexpr uint32_t ID_MX = idesc_mma(128, P, kFmtBF16, kFmtBF16, 0, 1);
+      const uint64_t c_k = sw128_desc(tile_c, 16u, 1024u), s_k = sw128_desc(sb + SM_SP, 16u, 1024u);
+      const bool one = elect();
+      bool ok = true;
+      for (int c = 0; c < n_chunks; ++c) {
+        const uint64_t x_mn = sw128_desc(tile_x(c), REG128, 1024u);
+        ok = warp_wait_c(FC, c) && warp_wait_c(AS, c) && (c == 0 || warp_wait_c(AY, c - 1));
         if (!ok) break;
         tc_fence_after();
         if (one) {
 #pragma unroll
           for (int k = 0; k < 2 * (N / 16); ++k)
             mma_f16(tmem + TM_Y, c_k + k_step(k % (N / 16)),
-                    s_k + k_step(k % (N / 16)) + (k / (N / 16)) * (SP_PLANE >> 4), ID_KK, k > 0);
+                    s_k + k_step(k % (N / 16)) + (k / (N / 16)) * (SP_PLANE >> 4), ID_CS, k > 0);
           mma_commit(bar(DCS, c));
         }
-      } else {
-        ok = warp_wait_c(FB, c) && warp_wait_c(PREP, c) && warp_wait_c(AS, c);
-        if (!ok) break;
-      }
-      const uint64_t xp_mn = sw128_desc(sb + SM_XP, REG64, 1024u);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        ok = ok && warp_wait(bar(AXP, half), c);
-        if (ok) {
-          tc_fence_after();
-          if (one) {
-#pragma unroll
-            for (int k = 0; k < 12; ++k)
-              mma_f16(tmem + TM_DS, xp_mn + (((k / 4) * XP_PLANE + (k % 4) * 2048u) >> 4),
-                      b_mn + ((half * REG64 + (k % 4) * 2048u) >> 4), ID_DS, half + k > 0);
-            mma_commit(half == 0 ? bar(DXP, 0) : bar(DDS, c));
-          }
-        }
-      }
-      if (!ok) break;
-      if constexpr (!STATE_ONLY) {
         ok = warp_wait_c(FX, c) && warp_wait_c(AM, c);
         if (!ok) break;
         tc_fence_after();
         if (one) {
-          const uint64_t x_mn = sw128_desc(buf_x(c), REG128, 1024u);
 #pragma unroll
           for (int k = 0; k < 8 * HEADS; ++k)
-            mma_f16_ta(tmem + TM_Y + 64 * (k / 8), tmem + TM_M + 64 * (k / 8) + 8 * (k % 8),
+            mma_f16_ta(tmem + TM_Y + 64 * (k / 8), tmem + 128 * (c & 1) + tm_m(k / 8, k % 8),
                        x_mn + (((k / 8) * REG128 + (k % 8) * 2048u) >> 4), ID_MX, 1);
           mma_commit(bar(DY, c));
         }
       }
-    }
-    if (!ok && one) {  // MMAs in flight finish before TMEM goes
-      mma_commit(bar(DXP, 1));
-      mbar_wait_bounded(bar(DXP, 1), 0, 1u << 16);
+      if (!ok && one) {  // MMAs in flight finish before TMEM goes
+        mma_commit(bar(FIN, 0));
+        mbar_wait_bounded(bar(FIN, 0), 0, 1u << 16);
+      }
+    } else if (warp == kStateMma) {
+      constexpr uint32_t ID_G = idesc_mma(128, 128, kFmtBF16, kFmtBF16, 0, 0);
+      constexpr uint32_t ID_DS = idesc_mma(128, N, kFmtBF16, kFmtBF16, 1, 1);
+      const bool one = elect();
+      bool ok = true;
+      for (int c = 0; c < n_chunks && ok; ++c) {
+        ok = warp_wait_c(FB, c) && warp_wait_c(PREP, c);
+        if constexpr (!STATE_ONLY) {
+          ok = ok && warp_wait_c(FC, c) && (c < 2 || warp_wait_c(DY, c - 2));
+          if (!ok) break;
+          tc_fence_after();
+          if (one) {
+            const uint64_t c_k = sw128_desc(tile_c, 16u, 1024u);
+            const uint64_t b_k = sw128_desc(tile_b(c), 16u, 1024u);
+#pragma unroll
+            for (int k = 0; k < N / 16; ++k)
+              mma_f16(tmem + 128 * (c & 1), c_k + k_step(k), b_k + k_step(k), ID_G, k > 0);
+            mma_commit(bar(DG, c));
+          }
+        } else {
+          ok = ok && (c < 2 || warp_wait_c(AY, c - 2));
+        }
+        const uint64_t b_mn = sw128_desc(tile_b(c), REG128, 1024u);
+        const uint32_t to = tmem + (STATE_ONLY ? 128u * (c & 1) : TM_DS);
+#pragma unroll 1
+        for (int r = 0; r < kRounds && ok; ++r) {
+          const int i = kRounds * c + r;
+          ok = warp_wait(xp_full(i), i / XP_BUFS);
+          if (!ok) break;
+          tc_fence_after();
+          if (one) {
+            const uint64_t xp = sw128_desc(sb + SM_XP + (i % XP_BUFS) * XP_BYTES, XP_REGION, 1024u);
+#pragma unroll
+            for (int k = 0; k < 6; ++k)
+              mma_f16(to, xp + (((k / 2) * XP_PLANE + (k % 2) * 2048u) >> 4),
+                      b_mn + ((r * 4096u + (k % 2) * 2048u) >> 4), ID_DS, r + k > 0);
+            mma_commit(xp_read(i));
+            if (r == kRounds - 1) mma_commit(bar(DDS, c));
+          }
+        }
+      }
+      if (!ok && one) {
+        mma_commit(bar(FIN, 1));
+        mbar_wait_bounded(bar(FIN, 1), 0, 1u << 16);
+      }
+    } else if (warp == kLoadWarp + 3 || DECAY_WARPS == 2) {
+      const int first_head = warp == kLoadWarp + 3 ? 0 : 1;
+      // lane i has tokens 4 i .. 4 i + 3, eight lanes a block of 32
+      for (int c = 0; c < n_chunks; ++c) {
+        const int64_t t0 = seg.begin + static_cast<int64_t>(c) * kQ;
+        const int len = seg.len - static_cast<int64_t>(c) * kQ < kQ
+                            ? static_cast<int>(seg.len - static_cast<int64_t>(c) * kQ)
+                            : kQ;
+        float raw[HEADS / DECAY_WARPS][4];
+#pragma unroll
+        for (int k = 0; k < HEADS / DECAY_WARPS; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            raw[k][i] = first_head + k < heads && 4 * lane + i < len
+                            ? bf2f(a.dt[(t0 + 4 * lane + i) * a.lddt + h0 + first_head + k])
+                            : 0.f;
+        if (c >= 2 && !warp_wait(bar(DFREE, c), (c >> 1) - 1)) break;
+#pragma unroll 1
+        for (int k = 0; k < HEADS / DECAY_WARPS; ++k) {
+          const int hh = first_head + k;
+          const bool mine = hh < heads;
+          const float A2 = mine ? a.A[h0 + hh] * 1.44269504088896340736f : 0.f;
+          float dt[4], pre[4], suf[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dt[i] = mine && 4 * lane + i < len ? ssm_step(a, k == 0 ? raw[0][i] : raw[HEADS / DECAY_WARPS - 1][i], h0 + hh) : 0.f;
+          pre[0] = dt[0] * A2;
+#pragma unroll
+          for (int i = 1; i < 4; ++i) pre[i] = pre[i - 1] + dt[i] * A2;
+          suf[3] = 0.f;
+#pragma unroll
+          for (int i = 2; i >= 0; --i) suf[i] = suf[i + 1] + dt[i + 1] * A2;
+          const float four = suf[0] + dt[0] * A2;
+          float up = four, down = four;
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) {
+            const float u = __shfl_up_sync(0xffffffffu, up, o, 8);
+            const float d = __shfl_down_sync(0xffffffffu, down, o, 8);
+            if ((lane & 7) >= o) up += u;
+            if ((lane & 7) + o < 8) down += d;
+          }
+          const float whole = __shfl_sync(0xffffffffu, up, 7, 8);
+          // sums of the lanes before and after, without this one's
+          float up_ex = __shfl_up_sync(0xffffffffu, up, 1, 8);
+          float down_ex = __shfl_down_sync(0xffffffffu, down, 1, 8);
+          if ((lane & 7) == 0) up_ex = 0.f;
+          if ((lane & 7) == 7) down_ex = 0.f;
+          float blocks[4], front = 0.f, behind = 0.f;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) blocks[b] = __shfl_sync(0xffffffffu, whole, 8 * b);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            if (b < lane / 8) front += blocks[b];
+            if (3 - b > lane / 8) behind += blocks[3 - b];
+          }
+          const uint32_t at = sb + SM_DEC + ((c & 1) * 2 + hh) * DEC_BYTES;
+          float4 v;
+          float *vp = &v.x;
+          auto put = [&](uint32_t off) {
+            *reinterpret_cast<float4 *>(S.ptr(at + off + 16 * lane)) = v;
+          };
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vp[i] = up_ex + pre[i];
+          put(DC_L);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vp[i] = dt[i];
+          put(DC_DT);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vp[i] = exp2f(suf[i] + down_ex) * dt[i];
+          put(DC_F);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vp[i] = exp2f(front + (up_ex + pre[i]));
+          put(DC_E);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vp[i] = exp2f(behind + (suf[i] + down_ex)) * dt[i];
+          put(DC_W);
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            if (lane == b) S.f32(at + DC_T + 4 * b) = blocks[b];
+          if (lane == 4)
+            S.f32(at + DC_T + 16) = exp2f((blocks[0] + blocks[1]) + (blocks[2] + blocks[3]));
+        }
+        if (len < kQ) {  // clear what lies behind the sequence's end
+          if (!warp_wait_c(FX, c) || !warp_wait_c(FB, c)) break;
+          for (int i = lane + 32 * first_head; i < (kQ - len) * 8; i += 32 * DECAY_WARPS) {
+            const uint32_t off = static_cast<uint32_t>(len) * 128u + 16u * i;
+            for (int r = 0; r < 2; ++r)
+              S.u128(tile_x(c) + r * REG128 + off) = make_uint4(0, 0, 0, 0);
+            for (int r = 0; r < N / 64; ++r)
+              S.u128(tile_b(c) + r * REG128 + off) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+        }
+        arrive(bar(PREP, c));
+      }
     }
     __syncwarp();
-  } else if (warp >= kDecayWarp) {
-    // decays: lane i has tokens 4 i .. 4 i + 3, eight lanes a block
-    const int hh = warp - kDecayWarp;
-    const bool mine = hh < heads;
-    const float A2 = mine ? a.A[h0 + hh] * 1.44269504088896340736f : 0.f;
-    for (int c = 0; c < n_chunks; ++c) {
-      const int64_t t0 = seg.begin + static_cast<int64_t>(c) * kQ;
-      const int len = seg.len - static_cast<int64_t>(c) * kQ < kQ
-                          ? static_cast<int>(seg.len - static_cast<int64_t>(c) * kQ)
-                          : kQ;
-      float dt[4], pre[4], suf[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        dt[i] = mine && 4 * lane + i < len ? ssm_dt(a, t0 + 4 * lane + i, h0 + hh) : 0.f;
-      pre[0] = dt[0] * A2;
-#pragma unroll
-      for (int i = 1; i < 4; ++i) pre[i] = pre[i - 1] + dt[i] * A2;
-      suf[3] = 0.f;
-#pragma unroll
-      for (int i = 2; i >= 0; --i) suf[i] = suf[i + 1] + dt[i + 1] * A2;
-      const float four = suf[0] + dt[0] * A2;
-      float up = four, down = four;
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) {
-        const float u = __shfl_up_sync(0xffffffffu, up, o, 8);
-        const float d = __shfl_down_sync(0xffffffffu, down, o, 8);
-        if ((lane & 7) >= o) up += u;
-        if ((lane & 7) + o < 8) down += d;
-      }
-      const float whole = __shfl_sync(0xffffffffu, up, 7, 8);
-      // sums of the lanes before and after, without this one's
-      float up_ex = __shfl_up_sync(0xffffffffu, up, 1, 8);
-      float down_ex = __shfl_down_sync(0xffffffffu, down, 1, 8);
-      if ((lane & 7) == 0) up_ex = 0.f;
-      if ((lane & 7) == 7) down_ex = 0.f;
-      float blocks[4], front = 0.f, behind = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) blocks[k] = __shfl_sync(0xffffffffu, whole, 8 * k);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (k < lane / 8) front += blocks[k];
-        if (3 - k > lane / 8) behind += blocks[3 - k];
-      }
-      if (c >= 2 && !warp_wait(bar(DFREE, c), (c >> 1) - 1)) break;
-      const uint32_t at = sb + SM_DEC + ((c & 1) * 2 + hh) * DEC_BYTES;
-      float4 v;
-      float *vp = &v.x;
-      auto put = [&](uint32_t off) { *reinterpret_cast<float4 *>(S.ptr(at + off + 16 * lane)) = v; };
-#pragma unroll
-      for (int i = 0; i < 4; ++i) vp[i] = up_ex + pre[i];
-      put(DC_L);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) vp[i] = dt[i];
-      put(DC_DT);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) vp[i] = exp2f(suf[i] + down_ex) * dt[i];
-      put(DC_F);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) vp[i] = exp2f(front + (up_ex + pre[i]));
-      put(DC_E);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) vp[i] = exp2f(behind + (suf[i] + down_ex)) * dt[i];
-      put(DC_W);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (lane == k) S.f32(at + DC_T + 4 * k) = blocks[k];
-      if (lane == 4) S.f32(at + DC_T + 16) = exp2f((blocks[0] + blocks[1]) + (blocks[2] + blocks[3]));
-      if (len < kQ) {  // clear what lies behind the sequence's end
-        if (!warp_wait_c(FX, c) || !warp_wait_c(FB, c)) break;
-        const int rows = kQ - len;
-        for (int i = hh * 32 + lane; i < rows * 8; i += 64) {
-          const uint32_t off = static_cast<uint32_t>(len) * 128u + 16u * i;
-          for (int r = 0; r < 2; ++r) S.u128(buf_x(c) + r * REG128 + off) = make_uint4(0, 0, 0, 0);
-          for (int r = 0; r < N / 64; ++r)
-            S.u128(buf_b(c) + r * REG128 + off) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(PREP, c));
-    }
-  } else {
-    // ---- the workers ----------------------------------------------------------------------
-    const int wg = warp >> 2, quad = warp & 3;
-    const int row = quad * 32 + lane;  // TMEM lane: token of G, M, Y; column of dS^T
+  } else if (warp >= kOutWarp) {
+    set_registers<kOutRegs, false, !STATE_ONLY>();
+    const int quad = warp & 3, half = (warp - kOutWarp) >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const int hcol = HEADS == 2 ? quad >> 1 : 0;   // head of this thread's state column
-    const int hout = HEADS == 2 ? wg >> 1 : 0;     // head of its output columns [32 wg, 32 wg + 32)
-    const bool col_in = hcol < heads, out_in = hout < heads;
-    const int n0 = wg * NT;
-    const size_t col_at = static_cast<size_t>(h0 + hcol) * N * P + static_cast<size_t>(n0) * P +
-                          row % P;
-    const size_t state = static_cast<size_t>(a.H) * N * P;
-    auto arrive = [&](uint32_t b) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b);
-    };
-    float s[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) s[i] = 0.f;
-    if (!STATE_ONLY && col_in) {
-      if (a.S_in) {
-        const float *from = a.S_in + seg.seq * state + col_at;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) s[i] = from[static_cast<size_t>(i) * P];
-      }
-      for (int j = 0; j < seg.index; ++j) {
-        const float *from = p.part + (seg.id0 + j) * state + col_at;
-        const float d = p.part_decay[static_cast<size_t>(seg.id0 + j) * a.H + h0 + hcol];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) s[i] = fmaf(d, s[i], from[static_cast<size_t>(i) * P]);
-      }
-    }
-    // S^T as two bf16 planes, columns as rows of n
-    auto put_state = [&]() {
-#pragma unroll
-      for (int j = 0; j < NT / 8; ++j) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float u = s[8 * j + 2 * e], v = s[8 * j + 2 * e + 1];
-          hi[e] = pack_bf16x2(u, v);
-          const float2 f = unpack_bf16x2(hi[e]);
-          lo[e] = pack_bf16x2(u - f.x, v - f.y);
-        }
-        const int n = n0 + 8 * j;
-        const uint32_t at = sb + SM_SP + (n / 64) * REG128 + row * 128u +
-                            (static_cast<uint32_t>(((n % 64) / 8) ^ (row & 7)) << 4);
-        S.u128(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        S.u128(at + SP_PLANE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
-      fence_proxy_async();
-    };
     if constexpr (!STATE_ONLY) {
-      put_state();
-      // weights of later blocks of tokens: zero, once and for all
-      float none[16];
+      // columns [64 half, 64 half + 64): 32 rows of 128 bytes a warp.  In global memory 4 rows in one
+      // instruction, in TMEM a row for each lane.
+      const bool in = HEADS == 1 || half < heads;
+      const int64_t cols = static_cast<int64_t>(h0) * P + 64 * half;
+      const int r0 = lane >> 3, piece = lane & 7;
+      const bool gate = a.z && in;
+      for (int c = 0; c < n_chunks; ++c) {
+        const int64_t left = seg.len - static_cast<int64_t>(c) * kQ - quad * 32;
+        const int64_t first = seg.begin + static_cast<int64_t>(c) * kQ + quad * 32;
+        const uint32_t stage = tile_x(c) + half * REG128 + quad * 4096u;
+        uint4 z[8];
+        if (gate) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) none[i] = 0.f;
-      for (int b = quad + 1; b < 4; ++b)
-        if (HEADS == 2 ? (wg & 1) == 0 : wg == 0) tmem_st16(lanes + TM_M + 64 * hout + 16 * b, none);
-      tmem_wait_st();
-    }
-    arrive(bar(AS, 0));
-    float decay = 1.f;
-    const float skip = !STATE_ONLY && a.D && out_in ? a.D[h0 + hout] : 0.f;
-
-    for (int c = 0; c < n_chunks; ++c) {
-      const int64_t t0 = seg.begin + static_cast<int64_t>(c) * kQ;
-      const uint32_t dec = sb + SM_DEC + (c & 1) * 2 * DEC_BYTES;
-      if (!warp_wait_c(PREP, c) || !warp_wait_c(FX, c)) break;
-      // X' overwrites what other warps staged of the last output
-      if (!STATE_ONLY && c > 0 && !warp_wait_c(AO, c - 1)) break;
-      bool ok = true;
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        if (half == 1 && !(ok = warp_wait(bar(DXP, 0), c))) break;
-        // X' of tokens [64 half, 64 half + 64): a thread takes 8 columns of each region of a row
-        const int j = tid & 7, tok = tid >> 3;
-        const uint32_t off = tok * 128u + (static_cast<uint32_t>(j ^ (tok & 7)) << 4);
-#pragma unroll
-        for (int region = 0; region < 2; ++region) {
-          const float w = S.f32(dec + (HEADS == 2 ? region : 0) * DEC_BYTES + DC_W +
-                                4 * (64 * half + tok));
-          const uint4 raw = S.u128(buf_x(c) + region * REG128 + half * REG64 + off);
-          const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-          const float2 w2 = make_float2(w, w);
-          uint32_t out[3][4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float2 f = __fmul2_rn(unpack_bf16x2(in[e]), w2);
-            out[0][e] = upper(f.x, f.y);
-            f = __fadd2_rn(f, make_float2(-truncated(f.x), -truncated(f.y)));
-            out[1][e] = upper(f.x, f.y);
-            f = __fadd2_rn(f, make_float2(-truncated(f.x), -truncated(f.y)));
-            out[2][e] = upper(f.x, f.y);
-          }
-          const uint32_t to = sb + SM_XP + region * REG64 + off;
-#pragma unroll
-          for (int k = 0; k < 3; ++k)
-            S.u128(to + k * XP_PLANE) = make_uint4(out[k][0], out[k][1], out[k][2], out[k][3]);
+          for (int i = 0; i < 8; ++i)
+            if (4 * i + r0 < left)
+              z[i] = *reinterpret_cast<const uint4 *>(a.z + (first + 4 * i + r0) * a.ldz + cols +
+                                                      8 * piece);
         }
-        fence_proxy_async();
-        arrive(bar(AXP, half));
-
-        if constexpr (!STATE_ONLY) {
-          if (half == 1) break;
-          if (!(ok = warp_wait_c(DG, c))) break;
-          tc_fence_after();
-          // M: causal weights of the tokens, 32 at a time
-          const uint32_t d = dec + hout * DEC_BYTES;
-          const float lt = S.f32(d + DC_L + 4 * row);
+        // X is read by the state's warps until dS is done, by the others until Y is
+        if (!warp_wait_c(DDS, c) || !warp_wait_c(DY, c)) break;
+        tc_fence_after();
+        if (gate) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + r0;
+            S.u128(stage + r * 128u + ((piece ^ (r & 7)) << 4)) = z[i];
+          }
+          __syncwarp();
+        }
 #pragma unroll 1
-          for (int k = 0; k < (HEADS == 2 ? 2 : 1); ++k) {
-            const int b = HEADS == 1 ? wg : k == 0 ? wg & 1 : 3 - (wg & 1);  // block of s
-            if (b > quad) continue;
-            float m[32];
-            tmem_ld32(lanes + TM_G + 32 * b, m);
-            tmem_wait_ld();
-            uint32_t packed[16];
+        for (int k = 0; k < 2; ++k) {
+          float y[32];
+          tmem_ld32(lanes + TM_Y + 64 * half + 32 * k, y);
+          tmem_wait_ld();
+          if (k == 1) {
+            tc_fence_before();
+            arrive(bar(AY, c));
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t at = stage + lane * 128u + (((4 * k + j) ^ (lane & 7)) << 4);
+            if (gate) {
+              const uint4 raw = S.u128(at);
+              const uint32_t in4[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int i = 8 * j + 2 * q;
+                const float2 f = unpack_bf16x2(in4[q]);
+                const float2 v = __fmul2_rn(make_float2(y[i], y[i + 1]), f);
+                y[i] = v.x * sigmoid(f.x);
+                y[i + 1] = v.y * sigmoid(f.y);
+              }
+            }
+            const int i = 8 * j;
+            S.u128(at) =
+                make_uint4(pack_bf16x2(y[i], y[i + 1]), pack_bf16x2(y[i + 2], y[i + 3]),
+                           pack_bf16x2(y[i + 4], y[i + 5]), pack_bf16x2(y[i + 6], y[i + 7]));
+          }
+        }
+        __syncwarp();
+        if (in) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + r0;
+            if (r < left)
+              *reinterpret_cast<uint4 *>(a.o + (first + r) * a.ldo + cols + 8 * piece) =
+                  S.u128(stage + r * 128u + ((piece ^ (r & 7)) << 4));
+          }
+        }
+        fence_proxy_async();  // the tile goes back to the TMA
+        arrive(bar(AO, c));
+      }
+    } else {
+      // the state of the first pass: S^T in TMEM, a column for each lane and half of n a warp
+      const int row = quad * 32 + lane, n0 = half * (N / 2);
+      const int hcol = HEADS == 2 ? quad >> 1 : 0;
+      const size_t at0 = (static_cast<size_t>(id) * a.H + h0 + hcol) * N * P +
+                         static_cast<size_t>(n0) * P + row % P;
+      float decay = 1.f;
+      for (int c = 0; c < n_chunks; ++c) {
+        if (!warp_wait_c(PREP, c)) break;
+        const float keep = S.f32(sb + SM_DEC + ((c & 1) * 2 + hcol) * DEC_BYTES + DC_T + 16);
+        decay *= keep;
+        if (!warp_wait_c(DDS, c)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int k = 0; k < N / 2; k += 16) {
+          float s[16], v[16];
+          if (c > 0) tmem_ld16(lanes + TM_S + n0 + k, s);
+          tmem_ld16(lanes + 128 * (c & 1) + n0 + k, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[i] = c > 0 ? fmaf(keep, s[i], v[i]) : v[i];
+          if (c + 1 < n_chunks) {
+            tmem_st16(lanes + TM_S + n0 + k, s);
+          } else if (hcol < heads) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) p.part[at0 + static_cast<size_t>(k + i) * P] = s[i];
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(bar(AY, c));
+        if (lane == 0) mbar_arrive(bar(DFREE, c));
+      }
+      if (n0 == 0 && row % P == 0 && hcol < heads)
+        p.part_decay[static_cast<size_t>(id) * a.H + h0 + hcol] = decay;
+    }
+  } else if (warp >= kTokenWarp && !STATE_ONLY) {
+    set_registers<kTokenRegs, false, !STATE_ONLY>();
+      const int half = (warp - kTokenWarp) >> 2;  // of the columns of Y; of the blocks of M
+      const int quad = warp & 3, row = quad * 32 + lane;  // token of G, M and Y
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+      const int hout = HEADS == 2 ? half : 0;
+      const float skip = a.D && hout < heads ? a.D[h0 + hout] : 0.f;
+      for (int c = 0; c < n_chunks; ++c) {
+        const uint32_t dec = sb + SM_DEC + (c & 1) * 2 * DEC_BYTES;
+        if (!warp_wait_c(PREP, c) || !warp_wait_c(FX, c) || !warp_wait_c(DG, c)) break;
+        tc_fence_after();
+        // M, 32 tokens s at a time: blocks 0 and 3, or 1 and 2
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          const int b = k == 0 ? half : 3 - half;
+          const uint32_t block = lanes + 128 * (c & 1) + tm_m(0, 2 * b);
+          float m[32];
+          if (b > quad) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) m[i] = 0.f;
+            tmem_st32(block, m);
+            continue;
+          }
+          tmem_ld32(block, m);
+          tmem_wait_ld();
+#pragma unroll 1
+          for (int h = 0; h < HEADS; ++h) {
+            const uint32_t d = dec + h * DEC_BYTES;
+            const float lt = S.f32(d + DC_L + 4 * row);
+            float words[16];
             if (b < quad) {
               float l = lt;  // from the block's end to t
               for (int q = b + 1; q < quad; ++q) l += S.f32(d + DC_T + 4 * q);
@@ -585,8 +667,8 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                                             __fmul2_rn(make_float2(f.x, f.y), e2));
                 const float2 v = __fmul2_rn(make_float2(m[i + 2], m[i + 3]),
                                             __fmul2_rn(make_float2(f.z, f.w), e2));
-                packed[i / 2] = pack_bf16x2(u.x, u.y);
-                packed[i / 2 + 1] = pack_bf16x2(v.x, v.y);
+                words[i / 2] = __uint_as_float(pack_bf16x2(u.x, u.y));
+                words[i / 2 + 1] = __uint_as_float(pack_bf16x2(v.x, v.y));
               }
             } else {
 #pragma unroll
@@ -597,139 +679,172 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 const float u1 = i + 1 <= lane ? m[i + 1] * (ex2(lt - l.y) * w.y) : 0.f;
                 const float u2 = i + 2 <= lane ? m[i + 2] * (ex2(lt - l.z) * w.z) : 0.f;
                 const float u3 = i + 3 <= lane ? m[i + 3] * (ex2(lt - l.w) * w.w) : 0.f;
-                packed[i / 2] = pack_bf16x2(u0, u1);
-                packed[i / 2 + 1] = pack_bf16x2(u2, u3);
+                words[i / 2] = __uint_as_float(pack_bf16x2(u0, u1));
+                words[i / 2 + 1] = __uint_as_float(pack_bf16x2(u2, u3));
               }
             }
-            float words[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) words[i] = __uint_as_float(packed[i]);
-            tmem_st16(lanes + TM_M + 64 * hout + 16 * b, words);
+            tmem_st16(block + 16 * h, words);
           }
         }
-      }
-      if (!ok) break;
-
-      if constexpr (!STATE_ONLY) {
         if (!warp_wait_c(DCS, c)) break;
         tc_fence_after();
         // C S, scaled to each token, and D x
         const float e = S.f32(dec + hout * DEC_BYTES + DC_E + 4 * row);
         const float2 e2 = make_float2(e, e), skip2 = make_float2(skip, skip);
-        float y[32];
-        tmem_ld32(lanes + TM_Y + 32 * wg, y);
-        tmem_wait_ld();
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          float y[32];
+          tmem_ld32(lanes + TM_Y + 64 * half + 32 * k, y);
+          tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 raw = S.u128(buf_x(c) + (wg >> 1) * REG128 + row * 128u +
-                                   (static_cast<uint32_t>((4 * (wg & 1) + j) ^ (row & 7)) << 4));
-          const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int i = 8 * j + 2 * q;
-            const float2 f = __ffma2_rn(e2, make_float2(y[i], y[i + 1]),
-                                        __fmul2_rn(skip2, unpack_bf16x2(in[q])));
-            y[i] = f.x;
-            y[i + 1] = f.y;
-          }
-        }
-        tmem_st32(lanes + TM_Y + 32 * wg, y);
-        tmem_wait_st();
-        tc_fence_before();
-        arrive(bar(AM, c));
-      }
-
-      // the state behind this chunk
-      if (!warp_wait_c(DDS, c)) break;
-      tc_fence_after();
-      // X' is free from here on: each warp stages 32 rows of 64 bytes of z, then of o, there
-      const uint32_t stage = sb + SM_XP + warp * 2048u;
-      const int64_t rows_left = seg.len - static_cast<int64_t>(c) * kQ - quad * 32;
-      const int64_t first = t0 + quad * 32, cols = static_cast<int64_t>(h0) * P + 32 * wg;
-      if (!STATE_ONLY && a.z && out_in) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 8 * i + (lane >> 2), j = lane & 3;
-          if (r < rows_left)
-            cp_async16(stage + r * 64u + ((j ^ ((r >> 1) & 3)) << 4),
-                       a.z + (first + r) * a.ldz + cols + 8 * j);
-        }
-      }
-      const float keep = S.f32(dec + hcol * DEC_BYTES + DC_T + 16);
-      decay *= keep;
-      {
-        float v[NT];
-        if constexpr (NT == 32)
-          tmem_ld32(lanes + TM_DS + n0, v);
-        else
-          tmem_ld16(lanes + TM_DS + n0, v);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < NT; ++i) s[i] = fmaf(keep, s[i], v[i]);
-      }
-      tc_fence_before();
-      if (!STATE_ONLY && c + 1 < n_chunks) put_state();
-      arrive(bar(AS, c + 1));
-      if (lane == 0) mbar_arrive(bar(DFREE, c));
-
-      if constexpr (!STATE_ONLY) {
-        if (a.z) {
-          cp_async_wait_all();
-          __syncwarp();
-        }
-        if (!warp_wait_c(DY, c)) break;
-        tc_fence_after();
-        float y[32];
-        tmem_ld32(lanes + TM_Y + 32 * wg, y);
-        tmem_wait_ld();
-        tc_fence_before();
-        arrive(bar(AY, c));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t at = stage + lane * 64u + ((j ^ ((lane >> 1) & 3)) << 4);
-          if (a.z) {
-            const uint4 raw = S.u128(at);
+          for (int j = 0; j < 4; ++j) {
+            const uint4 raw = S.u128(tile_x(c) + half * REG128 + row * 128u +
+                                     (static_cast<uint32_t>((4 * k + j) ^ (row & 7)) << 4));
             const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const float2 f = unpack_bf16x2(in[q]);
-              y[8 * j + 2 * q] *= silu(f.x);
-              y[8 * j + 2 * q + 1] *= silu(f.y);
+              const int i = 8 * j + 2 * q;
+              const float2 f = __ffma2_rn(e2, make_float2(y[i], y[i + 1]),
+                                          __fmul2_rn(skip2, unpack_bf16x2(in[q])));
+              y[i] = f.x;
+              y[i + 1] = f.y;
             }
           }
-          S.u128(at) = make_uint4(
-              pack_bf16x2(y[8 * j], y[8 * j + 1]), pack_bf16x2(y[8 * j + 2], y[8 * j + 3]),
-              pack_bf16x2(y[8 * j + 4], y[8 * j + 5]), pack_bf16x2(y[8 * j + 6], y[8 * j + 7]));
+          tmem_st32(lanes + TM_Y + 64 * half + 32 * k, y);
         }
-        __syncwarp();
-        if (out_in) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + (lane >> 2), j = lane & 3;
-            if (r < rows_left)
-              *reinterpret_cast<uint4 *>(a.o + (first + r) * a.ldo + cols + 8 * j) =
-                  S.u128(stage + r * 64u + ((j ^ ((r >> 1) & 3)) << 4));
-          }
-        }
-        arrive(bar(AO, c));
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(bar(AM, c));
+        if (lane == 0) mbar_arrive(bar(DFREE, c));
       }
-    }
-    if (!*s_abort && col_in) {
-      float *to = nullptr;
-      if (STATE_ONLY)
-        to = p.part + static_cast<size_t>(id) * state + col_at;
-      else if (seg.last && a.S_out)
-        to = a.S_out + seg.seq * state + col_at;
-      if (to)
+  } else {
+    // the state's warps; in the first pass the token's beside them, every other round each
+    set_registers<kStateRegs, true, !STATE_ONLY>();
+    // X' of tokens [32 r, 32 r + 32) of chunk c: a thread takes 8 columns of both regions of a row
+    auto put_weighted = [&](int c, int r) -> bool {
+      const int i = kRounds * c + r;
+      if (i >= XP_BUFS && !warp_wait(xp_read(i), i / XP_BUFS - 1)) return false;
+      const int j = tid & 7, row = (tid >> 3) & 31, tok = 32 * r + row;
+      const uint32_t flip = static_cast<uint32_t>(j ^ (row & 7)) << 4;
+      const uint32_t dec = sb + SM_DEC + (c & 1) * 2 * DEC_BYTES + DC_W + 4 * tok;
+#pragma unroll
+      for (int region = 0; region < 2; ++region) {
+        const float w = S.f32(dec + (HEADS == 2 ? region : 0) * DEC_BYTES);
+        const uint4 raw = S.u128(tile_x(c) + region * REG128 + tok * 128u + flip);
+        const uint32_t in4[4] = {raw.x, raw.y, raw.z, raw.w};
+        const float2 w2 = make_float2(w, w);
+        uint32_t out[3][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float2 f = __fmul2_rn(unpack_bf16x2(in4[e]), w2);
+          out[0][e] = upper(f.x, f.y);
+          f = __fadd2_rn(f, make_float2(-truncated(f.x), -truncated(f.y)));
+          out[1][e] = upper(f.x, f.y);
+          f = __fadd2_rn(f, make_float2(-truncated(f.x), -truncated(f.y)));
+          out[2][e] = upper(f.x, f.y);
+        }
+        const uint32_t to = sb + SM_XP + (i % XP_BUFS) * XP_BYTES + region * XP_REGION + row * 128u + flip;
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          S.u128(to + k * XP_PLANE) = make_uint4(out[k][0], out[k][1], out[k][2], out[k][3]);
+      }
+      fence_proxy_async();
+      arrive(xp_full(i));
+      return true;
+    };
+    if constexpr (STATE_ONLY) {
+      for (int c = 0; c < n_chunks; ++c) {
+        if (!warp_wait_c(PREP, c) || !warp_wait_c(FX, c)) break;
+        bool ok = true;
+#pragma unroll 1
+        for (int r = warp / kTokenWarp; r < kRounds && ok; r += 2) ok = put_weighted(c, r);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(bar(DFREE, c));
+      }
+    } else {
+      constexpr int NT = N / 2;                      // state entries of a thread
+      const int n0 = (warp >> 2) * NT, quad = warp & 3;
+      const int row = quad * 32 + lane;              // column of the state: TMEM lane of dS^T
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+      const int hcol = HEADS == 2 ? quad >> 1 : 0;   // its head
+      const bool in = hcol < heads;
+      const size_t at0 =
+          static_cast<size_t>(h0 + hcol) * N * P + static_cast<size_t>(n0) * P + row % P;
+      const size_t state = static_cast<size_t>(a.H) * N * P;
+      float s[NT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) s[i] = 0.f;
+      if (in) {
+        if (a.S_in) {
+          const float *from = a.S_in + seg.seq * state + at0;
+#pragma unroll
+          for (int i = 0; i < NT; ++i) s[i] = from[static_cast<size_t>(i) * P];
+        }
+        for (int j = 0; j < seg.index; ++j) {
+          const float *from = p.part + (seg.id0 + j) * state + at0;
+          const float d = p.part_decay[static_cast<size_t>(seg.id0 + j) * a.H + h0 + hcol];
+#pragma unroll
+          for (int i = 0; i < NT; ++i) s[i] = fmaf(d, s[i], from[static_cast<size_t>(i) * P]);
+        }
+      }
+      // S^T as two bf16 planes, columns as rows of n
+      auto put_state = [&](int c) {
+#pragma unroll
+        for (int j = 0; j < NT / 8; ++j) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 u = make_float2(s[8 * j + 2 * e], s[8 * j + 2 * e + 1]);
+            hi[e] = pack_bf16x2(u.x, u.y);
+            const float2 f = unpack_bf16x2(hi[e]);
+            const float2 r = __fadd2_rn(u, make_float2(-f.x, -f.y));
+            lo[e] = pack_bf16x2(r.x, r.y);
+          }
+          const int n = n0 + 8 * j;
+          const uint32_t at = sb + SM_SP + (n / 64) * REG128 + row * 128u +
+                              (static_cast<uint32_t>(((n % 64) / 8) ^ (row & 7)) << 4);
+          S.u128(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          S.u128(at + SP_PLANE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_proxy_async();
+        arrive(bar(AS, c));
+      };
+      put_state(0);
+      bool ok = true;
+      for (int c = 0; c < n_chunks; ++c) {
+        ok = warp_wait_c(PREP, c) && warp_wait_c(FX, c);
+#pragma unroll 1
+        for (int r = 0; r < kRounds && ok; ++r) ok = put_weighted(c, r);
+        ok = ok && warp_wait_c(DDS, c);
+        if (!ok) break;
+        tc_fence_after();
+        const float keep = S.f32(sb + SM_DEC + ((c & 1) * 2 + hcol) * DEC_BYTES + DC_T + 16);
+#pragma unroll
+        for (int k = 0; k < NT; k += 16) {
+          float v[16];
+          tmem_ld16(lanes + TM_DS + n0 + k, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[k + i] = fmaf(keep, s[k + i], v[i]);
+        }
+        tc_fence_before();
+        arrive(bar(DFREE, c));
+        if (c + 1 < n_chunks) {
+          if (!(ok = warp_wait_c(DCS, c))) break;  // the planes are read until then
+          put_state(c + 1);
+        }
+      }
+      if (ok && in && seg.last && a.S_out) {
+        float *to = a.S_out + seg.seq * state + at0;
 #pragma unroll
         for (int i = 0; i < NT; ++i) to[static_cast<size_t>(i) * P] = s[i];
-      if (STATE_ONLY && wg == 0 && row % P == 0)
-        p.part_decay[static_cast<size_t>(id) * a.H + h0 + hcol] = decay;
+      }
     }
   }
+  if (gave_up) atomicOr(a.status, KDA_ERR_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kStateMma) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -56,8 +56,24 @@ __device__ __forceinline__ float sigmoid(float x) {
 }
 __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 
-// log(1 + exp(x)); beyond 20 the difference to x is under half a unit in the last place.
-__device__ __forceinline__ float softplus(float x) { return x > 20.f ? x : log1pf(expf(x)); }
+// log(1 + exp(x)) = max(x, 0) + log(1 + v), v = exp(-|x|), to a few 1e-7 relative everywhere.
+// log(1 + v) = 2 artanh(s) with s = v / (2 + v) <= 1/3, by its series in s^2 up to s^13 / 13 (the next
+// term is under 2e-8 of the first).  The product |x| log2(e) is kept in two parts, since its rounding
+// would come back as a relative error of v.
+__device__ __forceinline__ float softplus(float x) {
+  const float m = -fabsf(x), hi = m * 1.44269504f;
+  const float lo = fmaf(m, 1.44269504f, -hi) + m * 1.92596299e-8f;  // log2(e) - 1.44269504
+  float v = ex2(hi);
+  v = fmaf(v, 0.69314718f * lo, v);
+  const float s = v * rcp(2.f + v), s2 = s * s;
+  float q = fmaf(s2, 1.f / 13.f, 1.f / 11.f);
+  q = fmaf(q, s2, 1.f / 9.f);
+  q = fmaf(q, s2, 1.f / 7.f);
+  q = fmaf(q, s2, 1.f / 5.f);
+  q = fmaf(q, s2, 1.f / 3.f);
+  q = fmaf(q * s2, s, s);
+  return fmaxf(x, 0.f) + (q + q);
+}
 
 struct ConvArgs {
   const kda_bf16 *x, *weight, *bias, *state_in;

@@ -417,30 +417,41 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
       }
     } else if (warp == kLoadWarp + 3 || DECAY_WARPS == 2) {
       const int first_head = warp == kLoadWarp + 3 ? 0 : 1;
-      // lane i has tokens 4 i .. 4 i + 3, eight lanes a block of 32
+      // lane i has tokens 4 i .. 4 i + 3, eight lanes a block of 32; the next chunk's are on their way
+      constexpr int MINE = HEADS / DECAY_WARPS;
+      uint32_t raw[MINE][4], next[MINE][4];  // (widened only where they are used)
+      auto fetch = [&](uint32_t (&to)[MINE][4], int c) {
+        const int64_t t0 = seg.begin + static_cast<int64_t>(c) * kQ + 4 * lane;
+        const int64_t end = seg.begin + seg.len;
+#pragma unroll
+        for (int k = 0; k < MINE; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            to[k][i] = 0;
+            if (first_head + k < heads && t0 + i < end)
+              to[k][i] = a.dt[(t0 + i) * a.lddt + h0 + first_head + k];
+          }
+      };
+      fetch(next, 0);
       for (int c = 0; c < n_chunks; ++c) {
-        const int64_t t0 = seg.begin + static_cast<int64_t>(c) * kQ;
         const int len = seg.len - static_cast<int64_t>(c) * kQ < kQ
                             ? static_cast<int>(seg.len - static_cast<int64_t>(c) * kQ)
                             : kQ;
-        float raw[HEADS / DECAY_WARPS][4];
 #pragma unroll
-        for (int k = 0; k < HEADS / DECAY_WARPS; ++k)
+        for (int k = 0; k < MINE; ++k)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            raw[k][i] = first_head + k < heads && 4 * lane + i < len
-                            ? bf2f(a.dt[(t0 + 4 * lane + i) * a.lddt + h0 + first_head + k])
-                            : 0.f;
+          for (int i = 0; i < 4; ++i) raw[k][i] = next[k][i];
+        fetch(next, c + 1);
         if (c >= 2 && !warp_wait(bar(DFREE, c), (c >> 1) - 1)) break;
 #pragma unroll 1
-        for (int k = 0; k < HEADS / DECAY_WARPS; ++k) {
+        for (int k = 0; k < MINE; ++k) {
           const int hh = first_head + k;
           const bool mine = hh < heads;
           const float A2 = mine ? a.A[h0 + hh] * 1.44269504088896340736f : 0.f;
           float dt[4], pre[4], suf[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            dt[i] = mine && 4 * lane + i < len ? ssm_step(a, k == 0 ? raw[0][i] : raw[HEADS / DECAY_WARPS - 1][i], h0 + hh) : 0.f;
+            dt[i] = mine && 4 * lane + i < len ? ssm_step(a, __uint_as_float((k == 0 ? raw[0][i] : raw[MINE - 1][i]) << 16), h0 + hh) : 0.f;
           pre[0] = dt[0] * A2;
 #pragma unroll
           for (int i = 1; i < 4; ++i) pre[i] = pre[i - 1] + dt[i] * A2;
@@ -483,13 +494,13 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
           for (int i = 0; i < 4; ++i) vp[i] = dt[i];
           put(DC_DT);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) vp[i] = exp2f(suf[i] + down_ex) * dt[i];
+          for (int i = 0; i < 4; ++i) vp[i] = ex2(suf[i] + down_ex) * dt[i];
           put(DC_F);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) vp[i] = exp2f(front + (up_ex + pre[i]));
+          for (int i = 0; i < 4; ++i) vp[i] = ex2(front + (up_ex + pre[i]));
           put(DC_E);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) vp[i] = exp2f(behind + (suf[i] + down_ex)) * dt[i];
+          for (int i = 0; i < 4; ++i) vp[i] = ex2(behind + (suf[i] + down_ex)) * dt[i];
           put(DC_W);
 #pragma unroll
           for (int b = 0; b < 4; ++b)
@@ -535,6 +546,8 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
               z[i] = *reinterpret_cast<const uint4 *>(a.z + (first + 4 * i + r0) * a.ldz + cols +
                                                       8 * piece);
         }
+        if (gate && lane + kQ < left)  // the next chunk's gate, a line for each row
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(a.z + (first + kQ + lane) * a.ldz + cols));
         // X is read by the state's warps until dS is done, by the others until Y is
         if (!warp_wait_c(DDS, c) || !warp_wait_c(DY, c)) break;
         tc_fence_after();
@@ -565,9 +578,12 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
               for (int q = 0; q < 4; ++q) {
                 const int i = 8 * j + 2 * q;
                 const float2 f = unpack_bf16x2(in4[q]);
-                const float2 v = __fmul2_rn(make_float2(y[i], y[i + 1]), f);
-                y[i] = v.x * sigmoid(f.x);
-                y[i + 1] = v.y * sigmoid(f.y);
+                const float2 l = __fmul2_rn(f, make_float2(-1.44269504f, -1.44269504f));
+                const float2 d = __fadd2_rn(make_float2(ex2(l.x), ex2(l.y)), make_float2(1.f, 1.f));
+                const float2 v = __fmul2_rn(__fmul2_rn(make_float2(y[i], y[i + 1]), f),
+                                            make_float2(rcp(d.x), rcp(d.y)));
+                y[i] = v.x;
+                y[i + 1] = v.y;
               }
             }
             const int i = 8 * j;

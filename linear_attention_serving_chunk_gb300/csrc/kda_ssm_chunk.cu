@@ -534,20 +534,27 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
       const int64_t cols = static_cast<int64_t>(h0) * P + 64 * half;
       const int r0 = lane >> 3, piece = lane & 7;
       const bool gate = a.z && in;
-      for (int c = 0; c < n_chunks; ++c) {
-        const int64_t left = seg.len - static_cast<int64_t>(c) * kQ - quad * 32;
-        const int64_t first = seg.begin + static_cast<int64_t>(c) * kQ + quad * 32;
+      // row r0 of this warp's 32, in the gate and in the result
+      const int64_t row0 = (seg.begin + quad * 32 + r0);
+      const kda_bf16 *gate_at = a.z + row0 * a.ldz + cols + 8 * piece;
+      kda_bf16 *out_at = a.o + row0 * a.ldo + cols + 8 * piece;
+#pragma unroll 1
+      for (int c = 0; c < n_chunks; ++c, gate_at += kQ * a.ldz, out_at += kQ * a.ldo) {
+        const int64_t behind = seg.len - static_cast<int64_t>(c) * kQ - quad * 32;
+        const int left = behind < 32 ? static_cast<int>(behind) : 32;  // rows of this warp
         const uint32_t stage = tile_x(c) + half * REG128 + quad * 4096u;
         uint4 z[8];
         if (gate) {
+          const kda_bf16 *from = gate_at;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (4 * i + r0 < left)
-              z[i] = *reinterpret_cast<const uint4 *>(a.z + (first + 4 * i + r0) * a.ldz + cols +
-                                                      8 * piece);
+          for (int i = 0; i < 8; ++i, from += 4 * a.ldz)
+            if (4 * i + r0 < left) z[i] = *reinterpret_cast<const uint4 *>(from);
+          if (piece == 0 && behind > kQ) {  // the next chunk's lines
+            from = gate_at + kQ * a.ldz;
+            for (int i = r0; i < 32 && i + kQ < behind; i += 4, from += 4 * a.ldz)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(from));
+          }
         }
-        if (gate && lane + kQ < left)  // the next chunk's gate, a line for each row
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(a.z + (first + kQ + lane) * a.ldz + cols));
         // X is read by the state's warps until dS is done, by the others until Y is
         if (!warp_wait_c(DDS, c) || !warp_wait_c(DY, c)) break;
         tc_fence_after();
@@ -560,17 +567,17 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
           __syncwarp();
         }
 #pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
-          float y[32];
-          tmem_ld32(lanes + TM_Y + 64 * half + 32 * k, y);
+        for (int k = 0; k < 4; ++k) {
+          float y[16];
+          tmem_ld16(lanes + TM_Y + 64 * half + 16 * k, y);
           tmem_wait_ld();
-          if (k == 1) {
+          if (k == 3) {
             tc_fence_before();
             arrive(bar(AY, c));
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t at = stage + lane * 128u + (((4 * k + j) ^ (lane & 7)) << 4);
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t at = stage + lane * 128u + (((2 * k + j) ^ (lane & 7)) << 4);
             if (gate) {
               const uint4 raw = S.u128(at);
               const uint32_t in4[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -594,12 +601,12 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         }
         __syncwarp();
         if (in) {
+          kda_bf16 *to = out_at;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 8; ++i, to += 4 * a.ldo) {
             const int r = 4 * i + r0;
             if (r < left)
-              *reinterpret_cast<uint4 *>(a.o + (first + r) * a.ldo + cols + 8 * piece) =
-                  S.u128(stage + r * 128u + ((piece ^ (r & 7)) << 4));
+              *reinterpret_cast<uint4 *>(to) = S.u128(stage + r * 128u + ((piece ^ (r & 7)) << 4));
           }
         }
         fence_proxy_async();  // the tile goes back to the TMA

@@ -144,11 +144,6 @@ __device__ __forceinline__ bool elect() {
   return one != 0;
 }
 
-// K-step k of a K-major operand: 32 bytes inside a 128-byte row, then the next 64-column region.
-__device__ __forceinline__ constexpr uint32_t k_step(int k) {
-  return (static_cast<uint32_t>(k >> 2) * REG128 + static_cast<uint32_t>(k & 3) * 32u) >> 4;
-}
-
 template <int REGS, bool MORE, bool ON>
 __device__ __forceinline__ void set_registers() {
   if constexpr (!ON)
@@ -349,20 +344,28 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         if (!ok) break;
         tc_fence_after();
         if (one) {
+#pragma unroll 1
+          for (int r = 0; r < 2 * (N / 64); ++r) {  // (plane, 64 of n); 16 of n in a step of 32 bytes
+            const uint32_t at = (r % (N / 64)) * (REG128 >> 4);
+            const uint64_t cd = c_k + at, sd = s_k + at + (r / (N / 64)) * (SP_PLANE >> 4);
 #pragma unroll
-          for (int k = 0; k < 2 * (N / 16); ++k)
-            mma_f16(tmem + TM_Y, c_k + k_step(k % (N / 16)),
-                    s_k + k_step(k % (N / 16)) + (k / (N / 16)) * (SP_PLANE >> 4), ID_CS, k > 0);
+            for (int k = 0; k < 4; ++k) mma_f16(tmem + TM_Y, cd + 2 * k, sd + 2 * k, ID_CS, r + k > 0);
+          }
           mma_commit(bar(DCS, c));
         }
         ok = warp_wait_c(FX, c) && warp_wait_c(AM, c);
         if (!ok) break;
         tc_fence_after();
         if (one) {
+#pragma unroll 1
+          for (int r = 0; r < 2 * HEADS; ++r) {  // (head, 64 tokens); 16 tokens in a step
+            const int h = r / 2, k0 = 4 * (r % 2);
+            const uint32_t m = tmem + 128 * (c & 1) + tm_m(h, k0);
+            const uint64_t xd = x_mn + ((h * REG128 + k0 * 2048u) >> 4);
 #pragma unroll
-          for (int k = 0; k < 8 * HEADS; ++k)
-            mma_f16_ta(tmem + TM_Y + 64 * (k / 8), tmem + 128 * (c & 1) + tm_m(k / 8, k % 8),
-                       x_mn + (((k / 8) * REG128 + (k % 8) * 2048u) >> 4), ID_MX, 1);
+            for (int k = 0; k < 4; ++k)
+              mma_f16_ta(tmem + TM_Y + 64 * h, m + tm_m(0, k), xd + 128 * k, ID_MX, 1);
+          }
           mma_commit(bar(DY, c));
         }
       }
@@ -384,9 +387,12 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
           if (one) {
             const uint64_t c_k = sw128_desc(tile_c, 16u, 1024u);
             const uint64_t b_k = sw128_desc(tile_b(c), 16u, 1024u);
+#pragma unroll 1
+            for (int r = 0; r < N / 64; ++r)
 #pragma unroll
-            for (int k = 0; k < N / 16; ++k)
-              mma_f16(tmem + 128 * (c & 1), c_k + k_step(k), b_k + k_step(k), ID_G, k > 0);
+              for (int k = 0; k < 4; ++k)
+                mma_f16(tmem + 128 * (c & 1), c_k + r * (REG128 >> 4) + 2 * k,
+                        b_k + r * (REG128 >> 4) + 2 * k, ID_G, r + k > 0);
             mma_commit(bar(DG, c));
           }
         } else {
@@ -417,41 +423,40 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
       }
     } else if (warp == kLoadWarp + 3 || DECAY_WARPS == 2) {
       const int first_head = warp == kLoadWarp + 3 ? 0 : 1;
-      // lane i has tokens 4 i .. 4 i + 3, eight lanes a block of 32; the next chunk's are on their way
+      // lane i has tokens 4 i .. 4 i + 3, eight lanes a block of 32.  One (chunk, head) after another; the
+      // next one's steps are on their way (and widened only where they are used).
       constexpr int MINE = HEADS / DECAY_WARPS;
-      uint32_t raw[MINE][4], next[MINE][4];  // (widened only where they are used)
-      auto fetch = [&](uint32_t (&to)[MINE][4], int c) {
-        const int64_t t0 = seg.begin + static_cast<int64_t>(c) * kQ + 4 * lane;
-        const int64_t end = seg.begin + seg.len;
+      uint32_t next[4];
+      auto fetch = [&](int it) {
+        const int64_t at = seg.begin + static_cast<int64_t>(it / MINE) * kQ + 4 * lane;
+        const int left = static_cast<int>(seg.begin + seg.len - at < 4 ? seg.begin + seg.len - at : 4);
+        const int h = first_head + it % MINE;
+        const kda_bf16 *from = a.dt + at * a.lddt + h0 + h;
 #pragma unroll
-        for (int k = 0; k < MINE; ++k)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            to[k][i] = 0;
-            if (first_head + k < heads && t0 + i < end)
-              to[k][i] = a.dt[(t0 + i) * a.lddt + h0 + first_head + k];
-          }
+        for (int i = 0; i < 4; ++i, from += a.lddt) {
+          next[i] = 0;
+          if (h < heads && i < left) next[i] = *from;
+        }
       };
-      fetch(next, 0);
-      for (int c = 0; c < n_chunks; ++c) {
+      fetch(0);
+#pragma unroll 1
+      for (int it = 0; it < n_chunks * MINE; ++it) {
+        const int c = it / MINE, hh = first_head + it % MINE;
         const int len = seg.len - static_cast<int64_t>(c) * kQ < kQ
                             ? static_cast<int>(seg.len - static_cast<int64_t>(c) * kQ)
                             : kQ;
+        uint32_t raw[4];
 #pragma unroll
-        for (int k = 0; k < MINE; ++k)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) raw[k][i] = next[k][i];
-        fetch(next, c + 1);
-        if (c >= 2 && !warp_wait(bar(DFREE, c), (c >> 1) - 1)) break;
-#pragma unroll 1
-        for (int k = 0; k < MINE; ++k) {
-          const int hh = first_head + k;
+        for (int i = 0; i < 4; ++i) raw[i] = next[i];
+        fetch(it + 1);
+        if (it % MINE == 0 && c >= 2 && !warp_wait(bar(DFREE, c), (c >> 1) - 1)) break;
+        {
           const bool mine = hh < heads;
           const float A2 = mine ? a.A[h0 + hh] * 1.44269504088896340736f : 0.f;
           float dt[4], pre[4], suf[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            dt[i] = mine && 4 * lane + i < len ? ssm_step(a, __uint_as_float((k == 0 ? raw[0][i] : raw[MINE - 1][i]) << 16), h0 + hh) : 0.f;
+            dt[i] = mine && 4 * lane + i < len ? ssm_step(a, __uint_as_float(raw[i] << 16), h0 + hh) : 0.f;
           pre[0] = dt[0] * A2;
 #pragma unroll
           for (int i = 1; i < 4; ++i) pre[i] = pre[i - 1] + dt[i] * A2;
@@ -508,6 +513,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
           if (lane == 4)
             S.f32(at + DC_T + 16) = exp2f((blocks[0] + blocks[1]) + (blocks[2] + blocks[3]));
         }
+        if (it % MINE != MINE - 1) continue;
         if (len < kQ) {  // clear what lies behind the sequence's end
           if (!warp_wait_c(FX, c) || !warp_wait_c(FB, c)) break;
           for (int i = lane + 32 * first_head; i < (kQ - len) * 8; i += 32 * DECAY_WARPS) {

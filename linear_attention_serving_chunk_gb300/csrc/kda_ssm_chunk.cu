@@ -54,9 +54,12 @@ constexpr int kQ = 128;          // tokens of a chunk
 // warps of the roles: whole warpgroups, since a warp reaches the 32 TMEM lanes of its number mod 4
 constexpr int kStateWarps = 8, kTokenWarps = 8, kOutWarps = 8;
 constexpr int kTokenWarp = kStateWarps, kOutWarp = kTokenWarp + kTokenWarps;
-constexpr int kLoadWarp = kOutWarp + kOutWarps, kTokenMma = kLoadWarp + 1, kStateMma = kLoadWarp + 2;
-constexpr int kOthers = 4;  // (the fourth: decays)
-constexpr int kThreads = 32 * (kLoadWarp + kOthers);
+// (the token warps of the last 32 tokens have the most to do, and the loads the least: they share a
+// scheduler, and so do the first 32 tokens and the decays)
+constexpr int kDecayWarp = kOutWarp + kOutWarps, kTokenMma = kDecayWarp + 1, kStateMma = kDecayWarp + 2,
+              kLoadWarp = kDecayWarp + 3;
+constexpr int kOthers = 4;
+constexpr int kThreads = 32 * (kDecayWarp + kOthers);
 // registers a thread: 72 at launch, then in the second pass
 constexpr int kLaunchRegs = 72, kStateRegs = 96, kTokenRegs = 64, kOutRegs = 64, kOtherRegs = 56;
 static_assert(32 * (kStateWarps * kStateRegs + kTokenWarps * kTokenRegs + kOutWarps * kOutRegs +
@@ -68,18 +71,25 @@ constexpr uint32_t TILE = 32 * KiB;
 constexpr uint32_t SM_X = 0;                // X, two chunks
 constexpr uint32_t SM_B = 2 * TILE;         // (first pass: two chunks)
 constexpr uint32_t SM_C = 3 * TILE;
-constexpr uint32_t SM_XP = 4 * TILE;        // X': [3 planes][2 regions][32 tokens] (first pass: thrice)
-constexpr uint32_t XP_REGION = 4 * KiB, XP_PLANE = 2 * XP_REGION, XP_BYTES = 3 * XP_PLANE;
-constexpr uint32_t SM_SP = SM_XP + XP_BYTES;  // S^T: two planes of [128 columns][N / 64 regions]
+constexpr uint32_t SM_XP = 4 * TILE;        // X': 32 tokens (first pass: three buffers)
+constexpr uint32_t SM_SP = SM_XP + 24 * KiB;  // S^T: two planes of [128 columns][N / 64 regions]
 constexpr uint32_t SP_PLANE = 32 * KiB;
-constexpr uint32_t SM_DEC = SM_SP + 2 * SP_PLANE;  // decays: [2 chunks][2 heads]
+constexpr uint32_t SM_DEC = SM_SP + 2 * SP_PLANE;  // decays: [2 chunks][2 heads] (first pass: 2 more)
+constexpr uint32_t SM_DEC2 = SM_XP + 72 * KiB;
 constexpr uint32_t DEC_BYTES = 5 * 512 + 32;
 constexpr uint32_t SM_BAR = SM_DEC + 4 * DEC_BYTES;
-constexpr uint32_t SM_MISC = SM_BAR + 288;
+constexpr uint32_t SM_MISC = SM_BAR + 304;
 constexpr uint32_t SM_BYTES = SM_MISC + 64;
-static_assert(SM_BYTES <= 232448, "shared memory budget");
-static_assert(SM_XP + 3 * XP_BYTES <= SM_DEC, "three X' buffers of the first pass");
-constexpr int kRounds = kQ / 32;            // X' buffers filled for a chunk
+static_assert(SM_BYTES <= 232448 && SM_DEC2 + 4 * DEC_BYTES <= SM_DEC, "shared memory budget");
+
+// X' of a round: [3 planes][2 regions of 64 columns][TOKENS rows]
+template <bool STATE_ONLY>
+struct Weighted {
+  static constexpr int TOKENS = 32, BUFS = STATE_ONLY ? 3 : 1;
+  static constexpr int ROUNDS = kQ / TOKENS;
+  static constexpr uint32_t REGION = TOKENS * 128, PLANE = 2 * REGION, BYTES = 3 * PLANE;
+  static_assert(SM_XP + BUFS * BYTES <= (STATE_ONLY ? SM_DEC2 : SM_SP), "X' buffers");
+};
 
 // Decays of one (chunk, head): offsets in bytes
 constexpr uint32_t DC_L = 0;         // log2 decay from the 32-token block's start, token included
@@ -91,10 +101,12 @@ constexpr uint32_t DC_T = 2560;      // log2 decays of the four blocks; then the
 
 // mbarriers.  Two of each kind: of chunk c the one of its parity, in phase c / 2.  F: a tile has come;
 // D: an MMA is done; A: warps have arrived.  FIN is for a wait that has given up.
-enum Bar : int { FX, FC, FB, PREP, DFREE, DG, DCS, DDS, DY, AM, AS, AY, AO, FIN, NBAR };
+enum Bar : int { FX, FC, FB, DG, DCS, DDS, DY, AM, AS, AY, AO, FIN, NBAR };
 // One for each X' buffer: filled, and read.
 constexpr uint32_t BAR_AXP = SM_BAR + 16 * NBAR, BAR_DXP = BAR_AXP + 24;
-static_assert(BAR_DXP + 24 <= SM_MISC, "barriers");
+// One for each buffer of decays: written, and no longer needed.
+constexpr uint32_t BAR_PREP = BAR_DXP + 24, BAR_DFREE = BAR_PREP + 32;
+static_assert(BAR_DFREE + 32 <= SM_MISC, "barriers");
 
 // TMEM columns: two of G, Y, dS (the first pass: two of dS, and S)
 constexpr uint32_t TM_Y = 256, TM_DS = 384, TM_S = 256;
@@ -215,7 +227,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int HEADS = 128 / P;        // heads of a column block
   constexpr uint32_t BC_BYTES = 128 * N * 2;
-  constexpr int XP_BUFS = STATE_ONLY ? 3 : 1;
+  using XP = Weighted<STATE_ONLY>;
   constexpr int DECAY_WARPS = STATE_ONLY ? HEADS : 1;  // (the first pass has no MMAs of Y)
   const SsmArgs &a = p.a;
   const uint32_t sb = smem_u32(smem);
@@ -238,20 +250,29 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
   const int n_chunks = static_cast<int>((seg.len + kQ - 1) / kQ);
 
   auto bar = [&](int kind, int c) { return sb + SM_BAR + 16u * kind + 8u * (c & 1); };
-  auto xp_full = [&](int i) { return sb + BAR_AXP + 8u * (i % XP_BUFS); };
-  auto xp_read = [&](int i) { return sb + BAR_DXP + 8u * (i % XP_BUFS); };
+  constexpr int DECS = STATE_ONLY ? 4 : 2;  // buffers of decays
+  auto decays = [&](int c, int head) {
+    const int k = c % DECS;
+    return sb + (k < 2 ? SM_DEC : SM_DEC2) + ((k & 1) * 2 + head) * DEC_BYTES;
+  };
+  auto prepared = [&](int c) { return sb + BAR_PREP + 8u * (c % DECS); };
+  auto dec_free = [&](int c) { return sb + BAR_DFREE + 8u * (c % DECS); };
+  auto xp_full = [&](int i) { return sb + BAR_AXP + 8u * (i % XP::BUFS); };
+  auto xp_read = [&](int i) { return sb + BAR_DXP + 8u * (i % XP::BUFS); };
   if (tid == 0) {
     for (int k = 0; k < NBAR; ++k) {
       uint32_t count = 1;
-      if (k == PREP) count = DECAY_WARPS;
-      if (k == DFREE) count = kStateWarps + kTokenWarps + (STATE_ONLY ? kOutWarps : 0);
       if (k == AM) count = kTokenWarps;
       if (k == AS) count = kStateWarps;
       if (k == AY || k == AO) count = kOutWarps;
       mbar_init(bar(k, 0), count);
       mbar_init(bar(k, 1), count);
     }
-    for (int k = 0; k < XP_BUFS; ++k) {
+    for (int k = 0; k < DECS; ++k) {
+      mbar_init(prepared(k), DECAY_WARPS);
+      mbar_init(dec_free(k), kStateWarps + kTokenWarps + (STATE_ONLY ? kOutWarps : 0));
+    }
+    for (int k = 0; k < XP::BUFS; ++k) {
       mbar_init(xp_full(k), kStateWarps);
       mbar_init(xp_read(k), 1);
     }
@@ -298,7 +319,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     if (lane == 0) mbar_arrive(b);
   };
 
-  if (warp >= kLoadWarp) {
+  if (warp >= kDecayWarp) {
     set_registers<kOtherRegs, false, !STATE_ONLY>();
     if (warp == kLoadWarp) {
       if (lane == 0) {
@@ -379,7 +400,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
       const bool one = elect();
       bool ok = true;
       for (int c = 0; c < n_chunks && ok; ++c) {
-        ok = warp_wait_c(FB, c) && warp_wait_c(PREP, c);
+        ok = warp_wait_c(FB, c) && warp_wait(prepared(c), c / DECS);
         if constexpr (!STATE_ONLY) {
           ok = ok && warp_wait_c(FC, c) && (c < 2 || warp_wait_c(DY, c - 2));
           if (!ok) break;
@@ -401,19 +422,21 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         const uint64_t b_mn = sw128_desc(tile_b(c), REG128, 1024u);
         const uint32_t to = tmem + (STATE_ONLY ? 128u * (c & 1) : TM_DS);
 #pragma unroll 1
-        for (int r = 0; r < kRounds && ok; ++r) {
-          const int i = kRounds * c + r;
-          ok = warp_wait(xp_full(i), i / XP_BUFS);
+        for (int r = 0; r < XP::ROUNDS && ok; ++r) {
+          const int i = XP::ROUNDS * c + r;
+          ok = warp_wait(xp_full(i), i / XP::BUFS);
           if (!ok) break;
           tc_fence_after();
           if (one) {
-            const uint64_t xp = sw128_desc(sb + SM_XP + (i % XP_BUFS) * XP_BYTES, XP_REGION, 1024u);
+            const uint64_t xp =
+                sw128_desc(sb + SM_XP + (i % XP::BUFS) * XP::BYTES, XP::REGION, 1024u);
+            constexpr int STEPS = XP::TOKENS / 16;
 #pragma unroll
-            for (int k = 0; k < 6; ++k)
-              mma_f16(to, xp + (((k / 2) * XP_PLANE + (k % 2) * 2048u) >> 4),
-                      b_mn + ((r * 4096u + (k % 2) * 2048u) >> 4), ID_DS, r + k > 0);
+            for (int k = 0; k < 3 * STEPS; ++k)
+              mma_f16(to, xp + (((k / STEPS) * XP::PLANE + (k % STEPS) * 2048u) >> 4),
+                      b_mn + ((r * XP::TOKENS * 128u + (k % STEPS) * 2048u) >> 4), ID_DS, r + k > 0);
             mma_commit(xp_read(i));
-            if (r == kRounds - 1) mma_commit(bar(DDS, c));
+            if (r == XP::ROUNDS - 1) mma_commit(bar(DDS, c));
           }
         }
       }
@@ -421,8 +444,8 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         mma_commit(bar(FIN, 1));
         mbar_wait_bounded(bar(FIN, 1), 0, 1u << 16);
       }
-    } else if (warp == kLoadWarp + 3 || DECAY_WARPS == 2) {
-      const int first_head = warp == kLoadWarp + 3 ? 0 : 1;
+    } else if (warp == kDecayWarp || DECAY_WARPS == 2) {
+      const int first_head = warp == kDecayWarp ? 0 : 1;
       // lane i has tokens 4 i .. 4 i + 3, eight lanes a block of 32.  One (chunk, head) after another; the
       // next one's steps are on their way (and widened only where they are used).
       constexpr int MINE = HEADS / DECAY_WARPS;
@@ -449,7 +472,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
 #pragma unroll
         for (int i = 0; i < 4; ++i) raw[i] = next[i];
         fetch(it + 1);
-        if (it % MINE == 0 && c >= 2 && !warp_wait(bar(DFREE, c), (c >> 1) - 1)) break;
+        if (it % MINE == 0 && c >= DECS && !warp_wait(dec_free(c), c / DECS - 1)) break;
         {
           const bool mine = hh < heads;
           const float A2 = mine ? a.A[h0 + hh] * 1.44269504088896340736f : 0.f;
@@ -486,7 +509,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             if (b < lane / 8) front += blocks[b];
             if (3 - b > lane / 8) behind += blocks[3 - b];
           }
-          const uint32_t at = sb + SM_DEC + ((c & 1) * 2 + hh) * DEC_BYTES;
+          const uint32_t at = decays(c, hh);
           float4 v;
           float *vp = &v.x;
           auto put = [&](uint32_t off) {
@@ -525,7 +548,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
           }
           fence_proxy_async();
         }
-        arrive(bar(PREP, c));
+        arrive(prepared(c));
       }
     }
     __syncwarp();
@@ -626,8 +649,8 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                          static_cast<size_t>(n0) * P + row % P;
       float decay = 1.f;
       for (int c = 0; c < n_chunks; ++c) {
-        if (!warp_wait_c(PREP, c)) break;
-        const float keep = S.f32(sb + SM_DEC + ((c & 1) * 2 + hcol) * DEC_BYTES + DC_T + 16);
+        if (!warp_wait(prepared(c), c / DECS)) break;
+        const float keep = S.f32(decays(c, hcol) + DC_T + 16);
         decay *= keep;
         if (!warp_wait_c(DDS, c)) break;
         tc_fence_after();
@@ -649,7 +672,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         tmem_wait_st();
         tc_fence_before();
         arrive(bar(AY, c));
-        if (lane == 0) mbar_arrive(bar(DFREE, c));
+        if (lane == 0) mbar_arrive(dec_free(c));
       }
       if (n0 == 0 && row % P == 0 && hcol < heads)
         p.part_decay[static_cast<size_t>(id) * a.H + h0 + hcol] = decay;
@@ -662,8 +685,8 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
       const int hout = HEADS == 2 ? half : 0;
       const float skip = a.D && hout < heads ? a.D[h0 + hout] : 0.f;
       for (int c = 0; c < n_chunks; ++c) {
-        const uint32_t dec = sb + SM_DEC + (c & 1) * 2 * DEC_BYTES;
-        if (!warp_wait_c(PREP, c) || !warp_wait_c(FX, c) || !warp_wait_c(DG, c)) break;
+        const uint32_t dec = decays(c, 0);
+        if (!warp_wait(prepared(c), c / DECS) || !warp_wait_c(FX, c) || !warp_wait_c(DG, c)) break;
         tc_fence_after();
         // M, 32 tokens s at a time: blocks 0 and 3, or 1 and 2
 #pragma unroll 1
@@ -704,12 +727,19 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
               for (int i = 0; i < 32; i += 4) {
                 const float4 l = *reinterpret_cast<const float4 *>(S.ptr(d + DC_L + 4 * (32 * b + i)));
                 const float4 w = *reinterpret_cast<const float4 *>(S.ptr(d + DC_DT + 4 * (32 * b + i)));
-                const float u0 = i <= lane ? m[i] * (ex2(lt - l.x) * w.x) : 0.f;
-                const float u1 = i + 1 <= lane ? m[i + 1] * (ex2(lt - l.y) * w.y) : 0.f;
-                const float u2 = i + 2 <= lane ? m[i + 2] * (ex2(lt - l.z) * w.z) : 0.f;
-                const float u3 = i + 3 <= lane ? m[i + 3] * (ex2(lt - l.w) * w.w) : 0.f;
-                words[i / 2] = __uint_as_float(pack_bf16x2(u0, u1));
-                words[i / 2 + 1] = __uint_as_float(pack_bf16x2(u2, u3));
+                const float2 d0 = __fadd2_rn(make_float2(lt, lt), make_float2(-l.x, -l.y));
+                const float2 d1 = __fadd2_rn(make_float2(lt, lt), make_float2(-l.z, -l.w));
+                const float2 u = __fmul2_rn(make_float2(m[i], m[i + 1]),
+                                            __fmul2_rn(make_float2(ex2(d0.x), ex2(d0.y)),
+                                                       make_float2(w.x, w.y)));
+                const float2 v = __fmul2_rn(make_float2(m[i + 2], m[i + 3]),
+                                            __fmul2_rn(make_float2(ex2(d1.x), ex2(d1.y)),
+                                                       make_float2(w.z, w.w)));
+                // (a choice, not a product: what lies in the future may be infinite)
+                words[i / 2] = __uint_as_float(pack_bf16x2(i <= lane ? u.x : 0.f,
+                                                           i + 1 <= lane ? u.y : 0.f));
+                words[i / 2 + 1] = __uint_as_float(pack_bf16x2(i + 2 <= lane ? v.x : 0.f,
+                                                               i + 3 <= lane ? v.y : 0.f));
               }
             }
             tmem_st16(block + 16 * h, words);
@@ -744,20 +774,21 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         tmem_wait_st();
         tc_fence_before();
         arrive(bar(AM, c));
-        if (lane == 0) mbar_arrive(bar(DFREE, c));
+        if (lane == 0) mbar_arrive(dec_free(c));
       }
   } else {
     // the state's warps; in the first pass the token's beside them, every other round each
     set_registers<kStateRegs, true, !STATE_ONLY>();
-    // X' of tokens [32 r, 32 r + 32) of chunk c: a thread takes 8 columns of both regions of a row
+    // X' of the tokens of round r of chunk c: a thread takes 8 columns of a row, of one region or both
     auto put_weighted = [&](int c, int r) -> bool {
-      const int i = kRounds * c + r;
-      if (i >= XP_BUFS && !warp_wait(xp_read(i), i / XP_BUFS - 1)) return false;
-      const int j = tid & 7, row = (tid >> 3) & 31, tok = 32 * r + row;
+      const int i = XP::ROUNDS * c + r;
+      if (i >= XP::BUFS && !warp_wait(xp_read(i), i / XP::BUFS - 1)) return false;
+      const int j = tid & 7, row = (tid >> 3) % XP::TOKENS, tok = XP::TOKENS * r + row;
       const uint32_t flip = static_cast<uint32_t>(j ^ (row & 7)) << 4;
-      const uint32_t dec = sb + SM_DEC + (c & 1) * 2 * DEC_BYTES + DC_W + 4 * tok;
+      const uint32_t dec = decays(c, 0) + DC_W + 4 * tok;
 #pragma unroll
-      for (int region = 0; region < 2; ++region) {
+      for (int u = 0; u < XP::TOKENS / 16; ++u) {
+        const int region = XP::TOKENS == 16 ? (tid >> 7) & 1 : u;
         const float w = S.f32(dec + (HEADS == 2 ? region : 0) * DEC_BYTES);
         const uint4 raw = S.u128(tile_x(c) + region * REG128 + tok * 128u + flip);
         const uint32_t in4[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -772,10 +803,10 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
           f = __fadd2_rn(f, make_float2(-truncated(f.x), -truncated(f.y)));
           out[2][e] = upper(f.x, f.y);
         }
-        const uint32_t to = sb + SM_XP + (i % XP_BUFS) * XP_BYTES + region * XP_REGION + row * 128u + flip;
+        const uint32_t to = sb + SM_XP + (i % XP::BUFS) * XP::BYTES + region * XP::REGION + row * 128u + flip;
 #pragma unroll
         for (int k = 0; k < 3; ++k)
-          S.u128(to + k * XP_PLANE) = make_uint4(out[k][0], out[k][1], out[k][2], out[k][3]);
+          S.u128(to + k * XP::PLANE) = make_uint4(out[k][0], out[k][1], out[k][2], out[k][3]);
       }
       fence_proxy_async();
       arrive(xp_full(i));
@@ -783,12 +814,12 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     };
     if constexpr (STATE_ONLY) {
       for (int c = 0; c < n_chunks; ++c) {
-        if (!warp_wait_c(PREP, c) || !warp_wait_c(FX, c)) break;
+        if (!warp_wait(prepared(c), c / DECS) || !warp_wait_c(FX, c)) break;
         bool ok = true;
 #pragma unroll 1
-        for (int r = warp / kTokenWarp; r < kRounds && ok; r += 2) ok = put_weighted(c, r);
+        for (int r = warp / kTokenWarp; r < XP::ROUNDS && ok; r += 2) ok = put_weighted(c, r);
         if (!ok) break;
-        if (lane == 0) mbar_arrive(bar(DFREE, c));
+        if (lane == 0) mbar_arrive(dec_free(c));
       }
     } else {
       constexpr int NT = N / 2;                      // state entries of a thread
@@ -841,13 +872,13 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
       put_state(0);
       bool ok = true;
       for (int c = 0; c < n_chunks; ++c) {
-        ok = warp_wait_c(PREP, c) && warp_wait_c(FX, c);
+        ok = warp_wait(prepared(c), c / DECS) && warp_wait_c(FX, c);
 #pragma unroll 1
-        for (int r = 0; r < kRounds && ok; ++r) ok = put_weighted(c, r);
+        for (int r = 0; r < XP::ROUNDS && ok; ++r) ok = put_weighted(c, r);
         ok = ok && warp_wait_c(DDS, c);
         if (!ok) break;
         tc_fence_after();
-        const float keep = S.f32(sb + SM_DEC + ((c & 1) * 2 + hcol) * DEC_BYTES + DC_T + 16);
+        const float keep = S.f32(decays(c, hcol) + DC_T + 16);
 #pragma unroll
         for (int k = 0; k < NT; k += 16) {
           float v[16];
@@ -857,7 +888,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
           for (int i = 0; i < 16; ++i) s[k + i] = fmaf(keep, s[k + i], v[i]);
         }
         tc_fence_before();
-        arrive(bar(DFREE, c));
+        arrive(dec_free(c));
         if (c + 1 < n_chunks) {
           if (!(ok = warp_wait_c(DCS, c))) break;  // the planes are read until then
           put_state(c + 1);

@@ -228,7 +228,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
   constexpr int HEADS = 128 / P;        // heads of a column block
   constexpr uint32_t BC_BYTES = 128 * N * 2;
   using XP = Weighted<STATE_ONLY>;
-  constexpr int DECAY_WARPS = STATE_ONLY ? HEADS : 1;  // (the first pass has no MMAs of Y)
+  constexpr int DECAY_WARPS = STATE_ONLY ? 2 : 1;  // (the first pass has no MMAs of Y)
   const SsmArgs &a = p.a;
   const uint32_t sb = smem_u32(smem);
   const Smem S{smem, sb};
@@ -269,7 +269,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
       mbar_init(bar(k, 1), count);
     }
     for (int k = 0; k < DECS; ++k) {
-      mbar_init(prepared(k), DECAY_WARPS);
+      mbar_init(prepared(k), HEADS);
       mbar_init(dec_free(k), kStateWarps + kTokenWarps + (STATE_ONLY ? kOutWarps : 0));
     }
     for (int k = 0; k < XP::BUFS; ++k) {
@@ -444,35 +444,33 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         mma_commit(bar(FIN, 1));
         mbar_wait_bounded(bar(FIN, 1), 0, 1u << 16);
       }
-    } else if (warp == kDecayWarp || DECAY_WARPS == 2) {
-      const int first_head = warp == kDecayWarp ? 0 : 1;
+    } else {
       // lane i has tokens 4 i .. 4 i + 3, eight lanes a block of 32.  One (chunk, head) after another; the
       // next one's steps are on their way (and widened only where they are used).
-      constexpr int MINE = HEADS / DECAY_WARPS;
       uint32_t next[4];
       auto fetch = [&](int it) {
-        const int64_t at = seg.begin + static_cast<int64_t>(it / MINE) * kQ + 4 * lane;
+        const int64_t at = seg.begin + static_cast<int64_t>(it / HEADS) * kQ + 4 * lane;
         const int left = static_cast<int>(seg.begin + seg.len - at < 4 ? seg.begin + seg.len - at : 4);
-        const int h = first_head + it % MINE;
-        const kda_bf16 *from = a.dt + at * a.lddt + h0 + h;
+        const kda_bf16 *from = a.dt + at * a.lddt + h0 + it % HEADS;
 #pragma unroll
         for (int i = 0; i < 4; ++i, from += a.lddt) {
           next[i] = 0;
-          if (h < heads && i < left) next[i] = *from;
+          if (it % HEADS < heads && i < left) next[i] = *from;
         }
       };
-      fetch(0);
+      const int first = warp == kDecayWarp ? 0 : 1;
+      fetch(first);
 #pragma unroll 1
-      for (int it = 0; it < n_chunks * MINE; ++it) {
-        const int c = it / MINE, hh = first_head + it % MINE;
+      for (int it = first; it < n_chunks * HEADS; it += DECAY_WARPS) {
+        const int c = it / HEADS, hh = it % HEADS;
         const int len = seg.len - static_cast<int64_t>(c) * kQ < kQ
                             ? static_cast<int>(seg.len - static_cast<int64_t>(c) * kQ)
                             : kQ;
         uint32_t raw[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) raw[i] = next[i];
-        fetch(it + 1);
-        if (it % MINE == 0 && c >= DECS && !warp_wait(dec_free(c), c / DECS - 1)) break;
+        fetch(it + DECAY_WARPS);
+        if (c >= DECS && !warp_wait(dec_free(c), c / DECS - 1)) break;
         {
           const bool mine = hh < heads;
           const float A2 = mine ? a.A[h0 + hh] * 1.44269504088896340736f : 0.f;
@@ -536,10 +534,9 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
           if (lane == 4)
             S.f32(at + DC_T + 16) = exp2f((blocks[0] + blocks[1]) + (blocks[2] + blocks[3]));
         }
-        if (it % MINE != MINE - 1) continue;
-        if (len < kQ) {  // clear what lies behind the sequence's end
+        if (len < kQ && hh == 0) {  // clear what lies behind the sequence's end
           if (!warp_wait_c(FX, c) || !warp_wait_c(FB, c)) break;
-          for (int i = lane + 32 * first_head; i < (kQ - len) * 8; i += 32 * DECAY_WARPS) {
+          for (int i = lane; i < (kQ - len) * 8; i += 32) {
             const uint32_t off = static_cast<uint32_t>(len) * 128u + 16u * i;
             for (int r = 0; r < 2; ++r)
               S.u128(tile_x(c) + r * REG128 + off) = make_uint4(0, 0, 0, 0);

@@ -41,6 +41,7 @@
 // build X' too, and the output warps keep the state.
 #include <string.h>
 
+#include "kda_pdl.cuh"
 #include "kda_serving.cuh"
 #include "kda_tc_common.cuh"
 
@@ -61,7 +62,7 @@ constexpr int kDecayWarp = kOutWarp + kOutWarps, kTokenMma = kDecayWarp + 1, kSt
 constexpr int kOthers = 4;
 constexpr int kThreads = 32 * (kDecayWarp + kOthers);
 // registers a thread: 72 at launch, then in the second pass
-constexpr int kLaunchRegs = 72, kStateRegs = 96, kTokenRegs = 64, kOutRegs = 64, kOtherRegs = 56;
+constexpr int kLaunchRegs = 72, kStateRegs = 88, kTokenRegs = 64, kOutRegs = 72, kOtherRegs = 56;
 static_assert(32 * (kStateWarps * kStateRegs + kTokenWarps * kTokenRegs + kOutWarps * kOutRegs +
                     kOthers * kOtherRegs) <= kThreads * kLaunchRegs,
               "a warpgroup would wait for registers that the block does not have");
@@ -123,7 +124,8 @@ struct ChunkArgs {
   int blocks;        // column blocks: of a group, times G
   float *part;       // [segments, H, N, P]: what the first pass leaves
   float *part_decay; // [segments, H]
-  int single;        // no sequence is cut (one segment for each sequence)
+  int uncut;         // one segment for each sequence
+  int parts;         // segments that `part` has room for
 };
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y,
@@ -176,26 +178,31 @@ __device__ __forceinline__ float truncated(float x) {
 
 struct Segment {
   int seq, index;    // sequence, and the segment's number in it
-  int id0;           // id of the sequence's first segment
-  int64_t begin;     // first token
-  int64_t len;
-  bool last, bad;
+  int id0;           // id of the sequence's first segment (of the first ones, if it has several)
+  int begin, len;    // tokens
+  int last, bad;
 };
 
-// Segment `id` of the batch: sequence after sequence, ceil(length / seg_len) of each and one for an
-// empty one.  Called by a whole warp; false beyond the last.
-__device__ __forceinline__ bool find_segment(const Runs &r, int64_t seg_len, int id, Segment &g) {
+// Segment `id` of the batch.  The segments in front of a sequence's last one are all seg_len long and
+// come first, sequence after sequence; then come the last ones, one for each sequence.  So the full
+// ones start first, and the shorter ones fill the end.  Called by a whole warp, which looks at 128
+// sequences at a time; false beyond the last.
+__device__ __forceinline__ bool find_segment(const Runs &r, int64_t seg_len, int id, bool uncut,
+                                             Segment &g) {
   const int lane = threadIdx.x & 31;
-  auto count = [&](int s) -> int {
+  auto front = [&](int s) -> int {  // segments in front of the last one
     int64_t b, n, u;
     if (s >= r.n) return 0;
     run_range(r, s, b, n, u);
-    return n <= seg_len ? 1 : static_cast<int>((n + seg_len - 1) / seg_len);
+    return n <= seg_len ? 0 : static_cast<int>((n - 1) / seg_len);
   };
   int before = 0;
-  for (int base = 0; base < r.n; base += 32) {
-    const int c = count(base + lane);
-    int x = c;
+  g.seq = -1;
+  for (int base = 0; base < r.n && !uncut; base += 128) {
+    int c[4], mine = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mine += c[k] = front(base + 4 * lane + k);
+    int x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -204,19 +211,42 @@ __device__ __forceinline__ bool find_segment(const Runs &r, int64_t seg_len, int
     const unsigned m = __ballot_sync(0xffffffffu, before + x > id);
     if (m) {
       const int l = __ffs(m) - 1;
-      g.seq = base + l;
-      g.id0 = before + __shfl_sync(0xffffffffu, x - c, l);
+      int s = base + 4 * lane, first = before + x - mine;
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (s == base + 4 * lane + k && first + c[k] <= id) {
+          first += c[k];
+          ++s;
+        }
+      g.seq = __shfl_sync(0xffffffffu, s, l);
+      g.id0 = __shfl_sync(0xffffffffu, first, l);
       g.index = id - g.id0;
-      int64_t b, n, u;
-      g.bad = !run_range(r, g.seq, b, n, u);
-      g.begin = b + g.index * seg_len;
-      g.last = (g.index + 1) * seg_len >= n;
-      g.len = g.last ? n - g.index * seg_len : seg_len;
-      return true;
+      break;
     }
     before += __shfl_sync(0xffffffffu, x, 31);
   }
-  return false;
+  const bool full = g.seq >= 0;
+  if (!full) {
+    g.seq = id - before;
+    if (g.seq >= r.n) return false;
+  }
+  int64_t b, n, u;
+  g.bad = !run_range(r, g.seq, b, n, u);
+  if (!full) {
+    g.index = front(g.seq);
+    g.id0 = 0;
+    if (g.index > 0) {  // where its others are: the sum over the sequences in front of it
+      int sum = 0;
+      for (int s = lane; s < g.seq; s += 32) sum += front(s);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      g.id0 = sum;
+    }
+  }
+  g.last = !full;
+  g.begin = static_cast<int>(b + g.index * seg_len);
+  g.len = static_cast<int>(full ? seg_len : n - g.index * seg_len);
+  return true;
 }
 
 // STATE_ONLY: the first pass over the segments (no C, no output).
@@ -233,21 +263,39 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
   const uint32_t sb = smem_u32(smem);
   const Smem S{smem, sb};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // The second pass may start on the SMs that the last segments of the first one leave idle; its state
+  // warps wait for all of them.
+  if (STATE_ONLY) grid_launch_dependents();
   if ((sb & 1023u) != 0) {  // the swizzled layouts need 1024-byte alignment
     if (tid == 0) atomicOr(a.status, KDA_ERR_UNSUPPORTED);
     return;
   }
-  Segment seg;
+  // One warp looks the segment up, the roles read of it what they need.
   const int id = blockIdx.x / p.blocks, block = blockIdx.x % p.blocks;
-  if (!find_segment(a.runs, p.seg_len, id, seg)) return;
-  if (seg.bad && block == 0 && tid == 0) atomicOr(a.status, KDA_ERR_SHAPE);
-  if (seg.bad || (STATE_ONLY && seg.last)) return;
+  Segment &seg = *reinterpret_cast<Segment *>(smem + SM_MISC + 16);
+  if (warp == 0) {
+    Segment found;
+    if (!find_segment(a.runs, p.seg_len, id, p.uncut, found)) {
+      found.len = -1;
+    } else {
+      // offsets that are not in order can make more segments than the tokens have room for
+      if (found.id0 + found.index > p.parts || (!found.last && id >= p.parts)) found.bad = 1;
+      if (found.bad && block == 0 && lane == 0) atomicOr(a.status, KDA_ERR_SHAPE);
+      if (found.bad || (STATE_ONLY && found.last)) found.len = -1;
+    }
+    if (lane == 0) seg = found;
+  }
+  __syncthreads();
+  if (seg.len < 0) {
+    grid_dependency_wait();  // (this grid does not end before the first pass does)
+    return;
+  }
   const int per_group = a.H / a.G, blocks_per_group = p.blocks / a.G;
   const int g = block / blocks_per_group;
   const int first_in_group = (block % blocks_per_group) * HEADS;
   const int h0 = g * per_group + first_in_group;
   const int heads = per_group - first_in_group < HEADS ? 1 : HEADS;
-  const int n_chunks = static_cast<int>((seg.len + kQ - 1) / kQ);
+  const int n_chunks = (seg.len + kQ - 1) / kQ;
 
   auto bar = [&](int kind, int c) { return sb + SM_BAR + 16u * kind + 8u * (c & 1); };
   constexpr int DECS = STATE_ONLY ? 4 : 2;  // buffers of decays
@@ -326,7 +374,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         bool ok = true;
         int c = 0;
         for (; c < n_chunks; ++c) {
-          const int t = static_cast<int>(seg.begin + static_cast<int64_t>(c) * kQ);
+          const int t = seg.begin + c * kQ;
           auto load_bc = [&](const CUtensorMap *map, uint32_t to, uint32_t b) {
             mbar_expect_tx(b, BC_BYTES);
             for (int r = 0; r < N / 64; ++r)
@@ -449,9 +497,9 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
       // next one's steps are on their way (and widened only where they are used).
       uint32_t next[4];
       auto fetch = [&](int it) {
-        const int64_t at = seg.begin + static_cast<int64_t>(it / HEADS) * kQ + 4 * lane;
-        const int left = static_cast<int>(seg.begin + seg.len - at < 4 ? seg.begin + seg.len - at : 4);
-        const kda_bf16 *from = a.dt + at * a.lddt + h0 + it % HEADS;
+        const int at = it / HEADS * kQ + 4 * lane, left = seg.len - at;
+        const kda_bf16 *from =
+            a.dt + static_cast<int64_t>(seg.begin + at) * a.lddt + h0 + it % HEADS;
 #pragma unroll
         for (int i = 0; i < 4; ++i, from += a.lddt) {
           next[i] = 0;
@@ -463,9 +511,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
 #pragma unroll 1
       for (int it = first; it < n_chunks * HEADS; it += DECAY_WARPS) {
         const int c = it / HEADS, hh = it % HEADS;
-        const int len = seg.len - static_cast<int64_t>(c) * kQ < kQ
-                            ? static_cast<int>(seg.len - static_cast<int64_t>(c) * kQ)
-                            : kQ;
+        const int len = seg.len - c * kQ < kQ ? seg.len - c * kQ : kQ;
         uint32_t raw[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) raw[i] = next[i];
@@ -561,13 +607,12 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
       const int r0 = lane >> 3, piece = lane & 7;
       const bool gate = a.z && in;
       // row r0 of this warp's 32, in the gate and in the result
-      const int64_t row0 = (seg.begin + quad * 32 + r0);
+      const int64_t row0 = seg.begin + quad * 32 + r0;
       const kda_bf16 *gate_at = a.z + row0 * a.ldz + cols + 8 * piece;
       kda_bf16 *out_at = a.o + row0 * a.ldo + cols + 8 * piece;
 #pragma unroll 1
       for (int c = 0; c < n_chunks; ++c, gate_at += kQ * a.ldz, out_at += kQ * a.ldo) {
-        const int64_t behind = seg.len - static_cast<int64_t>(c) * kQ - quad * 32;
-        const int left = behind < 32 ? static_cast<int>(behind) : 32;  // rows of this warp
+        const int left = seg.len - c * kQ - quad * 32;  // rows of this warp, if under 32
         const uint32_t stage = tile_x(c) + half * REG128 + quad * 4096u;
         uint4 z[8];
         if (gate) {
@@ -575,9 +620,9 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
 #pragma unroll
           for (int i = 0; i < 8; ++i, from += 4 * a.ldz)
             if (4 * i + r0 < left) z[i] = *reinterpret_cast<const uint4 *>(from);
-          if (piece == 0 && behind > kQ) {  // the next chunk's lines
+          if (piece == 0 && left > kQ) {  // the next chunk's lines
             from = gate_at + kQ * a.ldz;
-            for (int i = r0; i < 32 && i + kQ < behind; i += 4, from += 4 * a.ldz)
+            for (int i = r0; i < 32 && i + kQ < left; i += 4, from += 4 * a.ldz)
               asm volatile("prefetch.global.L2 [%0];" ::"l"(from));
           }
         }
@@ -831,6 +876,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
       float s[NT];
 #pragma unroll
       for (int i = 0; i < NT; ++i) s[i] = 0.f;
+      grid_dependency_wait();
       if (in) {
         if (a.S_in) {
           const float *from = a.S_in + seg.seq * state + at0;
@@ -911,9 +957,12 @@ constexpr int kSMs = 152;
 
 int column_blocks(int H, int P, int G) { return P == 128 ? H : G * ((H / G + 1) / 2); }
 
-// Tokens of a segment.  Costs in chunks of the second pass, for sequences of the mean length cut into
-// k segments each: a chunk of the first pass is 0.45 of one, starting a CTA one.
-int64_t segment_tokens(int n_seq, int64_t total, int blocks) {
+// Tokens of a segment (0: no sequence is cut).  The host knows the mean length alone.  Costs in chunks of
+// the second pass, for sequences of the mean length cut into k segments each: a chunk of the first
+// pass is 0.4 of one (2.5 us against 6.2), starting a CTA one.  Where whole sequences do best but
+// the lengths may differ, those longer than an SM's share of all chunks are still cut: one long prompt
+// among short ones would keep its own few SMs busy long after the others are done.
+int64_t segment_tokens(int n_seq, int64_t total, int blocks, bool ragged) {
   const int64_t chunks = (total / n_seq + kQ) / kQ;
   auto waves = [&](int64_t tasks) { return (tasks + kSMs - 1) / kSMs; };
   int64_t best = 0;
@@ -922,17 +971,26 @@ int64_t segment_tokens(int n_seq, int64_t total, int blocks) {
     const int64_t per = (chunks + k - 1) / k;
     const int64_t tasks = static_cast<int64_t>(n_seq) * blocks;
     const double cost =
-        waves(tasks * k) * (per + 1.0) + (k > 1 ? waves(tasks * (k - 1)) * (0.45 * per + 1.0) : 0.0);
+        waves(tasks * k) * (per + 1.0) + (k > 1 ? waves(tasks * (k - 1)) * (0.4 * per + 1.0) : 0.0);
     if (k == 1 || cost < least) {
       least = cost;
-      best = k == 1 ? 0 : per * kQ;  // 0: not cut
+      best = k == 1 ? 0 : per * kQ;
     }
+  }
+  if (best == 0 && ragged && n_seq > 1) {
+    const int64_t share = waves(total / kQ * blocks), least_cut = share > 12 ? share : 12;
+    if (total >= 2 * least_cut * kQ) best = least_cut * kQ;
   }
   return best;
 }
 
-size_t segments_most(int n_seq, int64_t total, int64_t seg_len) {
-  return seg_len ? static_cast<size_t>(total / seg_len + n_seq) : static_cast<size_t>(n_seq);
+// Segments in front of the last ones, at most: each holds seg_len tokens of its own.
+size_t front_most(int64_t total, int64_t seg_len) {
+  return seg_len ? static_cast<size_t>(total / seg_len) : 0;
+}
+
+size_t segment_bytes(int64_t total, int64_t seg_len, int H, int P, int N) {
+  return front_most(total, seg_len) * H * (static_cast<size_t>(N) * P + 4) * sizeof(float);
 }
 
 bool row_map(CUtensorMap *map, const kda_bf16 *base, int64_t cols, int64_t rows, int64_t ld) {
@@ -949,13 +1007,14 @@ bool row_map(CUtensorMap *map, const kda_bf16 *base, int64_t cols, int64_t rows,
 }
 
 template <int N, int P, bool STATE_ONLY>
-cudaError_t launch(const ChunkArgs &p, const CUtensorMap (&maps)[3], unsigned grid,
+cudaError_t launch(const ChunkArgs &p, const CUtensorMap (&maps)[3], unsigned grid, bool early,
                    cudaStream_t st) {
+  const auto kernel = ssm_chunk_kernel<N, P, STATE_ONLY>;
   const cudaError_t err =
-      cudaFuncSetAttribute(ssm_chunk_kernel<N, P, STATE_ONLY>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, SM_BYTES);
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM_BYTES);
   if (err != cudaSuccess) return err;
-  ssm_chunk_kernel<N, P, STATE_ONLY><<<grid, kThreads, SM_BYTES, st>>>(maps[0], maps[1], maps[2], p);
+  if (early) return launch_pdl(kernel, dim3(grid), dim3(kThreads), SM_BYTES, st, maps[0], maps[1], maps[2], p);
+  kernel<<<grid, kThreads, SM_BYTES, st>>>(maps[0], maps[1], maps[2], p);
   return cudaGetLastError();
 }
 
@@ -969,24 +1028,24 @@ cudaError_t run(ChunkArgs p, int64_t seg_len, cudaStream_t st) {
        !row_map(&maps[1], a.B, static_cast<int64_t>(a.G) * N, a.runs.total, a.ldb) ||
        !row_map(&maps[2], a.C, static_cast<int64_t>(a.G) * N, a.runs.total, a.ldc)))
     return cudaErrorInvalidValue;
-  p.single = seg_len == 0;
+  p.uncut = seg_len == 0;
   p.seg_len = seg_len ? seg_len : (a.runs.total / kQ + 1) * kQ;
-  const size_t blocks = segments_most(a.runs.n, a.runs.total, seg_len) * p.blocks;
+  p.parts = static_cast<int>(front_most(a.runs.total, seg_len));
+  const size_t front = static_cast<size_t>(p.parts) * p.blocks;
+  const size_t blocks = front + static_cast<size_t>(a.runs.n) * p.blocks;
   if (blocks > 0x7fffffffull) return cudaErrorInvalidValue;
-  const unsigned grid = static_cast<unsigned>(blocks);
-  if (seg_len) {
-    const cudaError_t err = launch<N, P, true>(p, maps, grid, st);
+  if (front > 0) {
+    const cudaError_t err = launch<N, P, true>(p, maps, static_cast<unsigned>(front), false, st);
     if (err != cudaSuccess) return err;
   }
-  return launch<N, P, false>(p, maps, grid, st);
+  return launch<N, P, false>(p, maps, static_cast<unsigned>(blocks), front > 0, st);
 }
 
 }  // namespace
 
 size_t ssm_chunk_workspace(int n_seq, int64_t total, int H, int P, int G, int N) {
-  const int64_t seg_len = segment_tokens(n_seq, total, column_blocks(H, P, G));
-  if (!seg_len) return 0;
-  return segments_most(n_seq, total, seg_len) * H * (static_cast<size_t>(N) * P + 4) * sizeof(float);
+  const int64_t seg_len = segment_tokens(n_seq, total, column_blocks(H, P, G), true);
+  return segment_bytes(total, seg_len, H, P, N);
 }
 
 // Without a workspace of that size no sequence is cut into segments.
@@ -995,13 +1054,13 @@ cudaError_t ssm_chunk_launch(const SsmArgs &a, int P, int G, int N, void *worksp
   ChunkArgs p{};
   p.a = a;
   p.blocks = column_blocks(a.H, P, G);
-  int64_t seg_len = segment_tokens(a.runs.n, a.runs.total, p.blocks);
+  int64_t seg_len = segment_tokens(a.runs.n, a.runs.total, p.blocks, a.runs.cu != nullptr);
   if (seg_len) {
-    if (!workspace || bytes < ssm_chunk_workspace(a.runs.n, a.runs.total, a.H, P, G, N)) {
+    if (!workspace || bytes < segment_bytes(a.runs.total, seg_len, a.H, P, N)) {
       seg_len = 0;
     } else {
       p.part = static_cast<float *>(workspace);
-      p.part_decay = p.part + segments_most(a.runs.n, a.runs.total, seg_len) * a.H * N * P;
+      p.part_decay = p.part + front_most(a.runs.total, seg_len) * a.H * N * P;
     }
   }
   if (N == 64) return P == 64 ? run<64, 64>(p, seg_len, st) : run<64, 128>(p, seg_len, st);

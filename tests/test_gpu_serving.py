@@ -434,3 +434,34 @@ def test_speculative_step_in_a_graph():
     for a, b in zip((*got, *pools[1]), (*want, *pools[0])):
         assert torch.equal(a, b)
     assert kda.device_status() == 0
+
+
+def test_ssm_offsets_out_of_order_make_no_more_segments_than_there_is_room_for():
+    """The same tokens over and over: every pair of offsets that rises is in range by itself."""
+    d = {k: cuda(v) for k, v in ref.ssm_inputs(4096, 2, 64, 1, 64, 1).items()}
+    assert kda.ssm_workspace_bytes(9, 4096, 2, 64, 1, 64) > 0  # sequences are cut
+    cu = torch.tensor([0, 4096] * 5, dtype=torch.int32, device="cuda")
+    final = torch.zeros(9, 2, 64, 64, device="cuda")
+    kda.ssm_fwd(cu_seqlens=cu, S_final=final, **d)
+    assert kda.device_status() == kda.KDA_ERR_SHAPE
+
+
+@pytest.mark.parametrize("lens", [[2000, 0, 1, 700, 3000, 128], [1] * 130 + [4000], [5000] + [3] * 150])
+def test_ssm_fwd_cut_sequences_among_short_ones(lens):
+    """Segments of long sequences between empty and short ones; the states of all of them."""
+    H, P, N = 2, 64, 64
+    i, S0 = scan_case(lens, H, P, 1, N, seed=len(lens))
+    i["A"], i["dt_bias"] = i["A"] * 0 - 0.3, i["dt_bias"] * 0 - 3.0
+    assert kda.ssm_workspace_bytes(len(lens), sum(lens), H, P, 1, N) > 0
+    want, last, size, size_s = ref.ssm(lens=lens, S=S0, **i)
+    d = {k: cuda(v) for k, v in i.items()}
+    final = torch.empty(len(lens), H, N, P, device="cuda")
+    got = kda.ssm_fwd(cu_seqlens=cu_of(lens), S0=cuda(S0), S_final=final, **d)
+    within(got, want, HALF_STEP * size)
+    check_states(final, last, size_s)
+    # without the room for segments each sequence is one chain: the same up to rounding
+    got = kda.ssm_fwd(cu_seqlens=cu_of(lens), S0=cuda(S0), S_final=final,
+                      workspace=torch.empty(16, dtype=torch.uint8, device="cuda"), **d)
+    within(got, want, HALF_STEP * size)
+    check_states(final, last, size_s)
+    assert kda.device_status() == 0

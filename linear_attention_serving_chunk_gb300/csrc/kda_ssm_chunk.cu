@@ -116,7 +116,7 @@ __device__ __forceinline__ constexpr uint32_t tm_m(int h, int k) {
   return 32 * (k >> 1) + 16 * h + 8 * (k & 1);
 }
 
-constexpr uint32_t kPolls = 1u << 24;
+constexpr uint32_t kPolls = 1u << 20;
 
 struct ChunkArgs {
   SsmArgs a;
@@ -580,7 +580,9 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
           if (lane == 4)
             S.f32(at + DC_T + 16) = exp2f((blocks[0] + blocks[1]) + (blocks[2] + blocks[3]));
         }
-        if (len < kQ && hh == 0) {  // clear what lies behind the sequence's end
+        // Clear what lies behind the sequence's end (the first pass has whole chunks only).  The tiles'
+        // barriers are not a phase behind: their last users have freed this buffer of decays.
+        if (!STATE_ONLY && len < kQ && hh == 0) {
           if (!warp_wait_c(FX, c) || !warp_wait_c(FB, c)) break;
           for (int i = lane; i < (kQ - len) * 8; i += 32) {
             const uint32_t off = static_cast<uint32_t>(len) * 128u + 16u * i;

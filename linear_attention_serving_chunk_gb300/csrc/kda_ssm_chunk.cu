@@ -39,6 +39,17 @@
 // when its M is built; M takes the columns of its G, 32 tokens at a time.  The gate and the result
 // pass through the chunk's X tile once nothing reads it any more.  In the first pass the token warps
 // build X' too, and the output warps keep the state.
+// What bounds it (32768 packed tokens x 64 heads of 64, N = 128, gate: 554 us, of which the first pass
+// 154; 131072 tokens x 16 heads of 128: 776 us, of which 200).  A chunk of 128 tokens x 128 columns takes
+// 12,000 cycles in the second pass and 6,000 in the first.  Its products would take 3,600 at the
+// tensor cores' rate (they are busy 26 % of the time; leaving most of them out saved 2 %), its
+// tiles 1,200 at the memory's.  The element-wise work decides: about 25,000 warp instructions, which
+// the 24 working warps issue at 0.45 a cycle and scheduler, each waiting for its own results (shared
+// memory, TMEM, exponentials) most of the time.  Left out, the gate saved 13 %, the weights M 15 %.  So
+// the roles run side by side instead of one after another (one group of 16 warps that did all of it in
+// turn took 667 us), the loops are rolled where they can be (the code of the roles shares the instruction
+// caches: with 206 KB of it a quarter of all stalls were for instructions) and a wait is a few
+// instructions.
 #include <string.h>
 
 #include "kda_pdl.cuh"

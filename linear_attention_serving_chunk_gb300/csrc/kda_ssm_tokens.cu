@@ -11,6 +11,11 @@
 // of S^T C per token in shared memory: two barriers per TB tokens.  The arithmetic is packed fp32x2
 // over column pairs.
 //
+// One token on 512 x 32 states of 128 x 128: 315 us, 6.85 TB/s, the rate of a plain copy.  Runs of 1 to 5
+// tokens without commit on 256 x 32 states of 128 x 64: 65 us, 4.3 TB/s; there the 54 million warp
+// instructions of the tokens (schedulers 57 % busy) weigh against 41 us of reading.  Four CTAs an SM
+// (64 registers) instead of three took 10 us off, five spill.
+//
 // A decay near 1 is applied as S + ((a - 1) S + B dt x) with a - 1 from expm1: rounded to fp32, a itself
 // is off by up to 2^-24 the same way at every token, which over the hundreds of tokens that such a
 // state remembers adds up to several 1e-6.  Below 1/2, where a S loses nothing, a is used as it is.

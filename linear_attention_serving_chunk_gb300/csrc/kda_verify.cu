@@ -12,6 +12,11 @@
 // lane is in double precision.  The row is cut into segments of kSeg elements whose sums stay in
 // shared memory; the segment that the target falls into is read a second time, from L2, 32
 // neighbouring elements a lane, and then the 32 of the lane that it falls into, one a lane.
+//
+// 256 runs over 131072 words in fp32: 42.5 us; the rows that this batch needs are 240 MB, 5.6 TB/s.  A
+// few runs over 32000 words take 11 us on the device, a chain of dependent reads (offsets, drafted tokens,
+// their probabilities, the row, its two searches).  CTAs of 256 threads, two of them for a row at
+// this size: four took 47 us, one of 512 threads 44; four vectors in flight a lane: two took 46, eight 51.
 #include "kda_serving.cuh"
 
 namespace kda {

@@ -5,16 +5,16 @@
 //   S <- a S + B (dt x)^T,   o = (S^T C + D_h x) silu(z)
 //
 // Bound by memory for short runs: a state is read once and, with commit, written once.  One
-// 256-thread CTA owns one state; TPR = P / 4 threads lie along a row (4 columns each) and 256 / TPR
-// row groups along N, as in the KDA decode step.  The tokens of a run are staged TB at a time (B, C
+// CTA owns one state; TPR = P / 4 of its threads lie along a row (4 columns each) and its row groups along
+// N, as in the KDA decode step.  The tokens of a run are staged TB at a time (B, C
 // and x in fp32), a thread then takes its block of the state through all of them and leaves its part
 // of S^T C per token in shared memory: two barriers per TB tokens.  The arithmetic is packed fp32x2
 // over column pairs.
 //
 // One token on 512 x 32 states of 128 x 128: 315 us, 6.85 TB/s, the rate of a plain copy.  Runs of 1 to 5
-// tokens without commit on 256 x 32 states of 128 x 64: 65 us, 4.3 TB/s; there the 54 million warp
-// instructions of the tokens (schedulers 57 % busy) weigh against 41 us of reading.  Four CTAs an SM
-// (64 registers) instead of three took 10 us off, five spill.
+// tokens without commit on 256 x 32 states of 128 x 64: 60 us, 4.6 TB/s.  There a CTA's own chain counts
+// (offsets, rows, a barrier, the tokens, a barrier, the result) against the states that an SM has on their
+// way meanwhile; a quarter fewer instructions per token changed nothing.
 //
 // A decay near 1 is applied as S + ((a - 1) S + B dt x) with a - 1 from expm1: rounded to fp32, a itself
 // is off by up to 2^-24 the same way at every token, which over the hundreds of tokens that such a
@@ -25,11 +25,16 @@ namespace kda {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+// Threads of a CTA, and CTAs that an SM is to hold: 64 values of the state a thread and as many states on
+// their way as the registers allow.  (Runs on 128 x 64 states: 5 CTAs of 128 threads 60 us, 4 of 256 threads
+// 65, 4 of 128 threads 68, 6 spill; one token on 128 x 128 states: 2 of 256 threads 315, 128 threads 322.)
+constexpr int threads_of(int state) { return state > 8192 ? 256 : 128; }
+constexpr int ctas_of(int state) { return state > 8192 ? 2 : state > 4096 ? 5 : 8; }
 
 template <int N, int P, int TB>
-__global__ void __launch_bounds__(kThreads, N * P <= 8192 ? 4 : 2) ssm_tokens_kernel(const SsmArgs a) {
+__global__ void __launch_bounds__(threads_of(N * P), ctas_of(N * P))
+ssm_tokens_kernel(const SsmArgs a) {
+  constexpr int kThreads = threads_of(N * P), kWarps = kThreads / 32;
   constexpr int TPR = P / 4;           // threads along a row
   constexpr int RG = kThreads / TPR;   // row groups
   constexpr int RPT = N / RG;          // rows per thread
@@ -143,10 +148,11 @@ __global__ void __launch_bounds__(kThreads, N * P <= 8192 ? 4 : 2) ssm_tokens_ke
 template <int N, int P>
 cudaError_t run(const SsmArgs &a, bool single, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(a.runs.n) * a.H;
+  constexpr int threads = threads_of(N * P);
   if (single)
-    ssm_tokens_kernel<N, P, 1><<<grid, kThreads, 0, st>>>(a);
+    ssm_tokens_kernel<N, P, 1><<<grid, threads, 0, st>>>(a);
   else
-    ssm_tokens_kernel<N, P, N * P <= 8192 ? 8 : 4><<<grid, kThreads, 0, st>>>(a);
+    ssm_tokens_kernel<N, P, N * P <= 8192 ? 8 : 4><<<grid, threads, 0, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -59,10 +59,12 @@ __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 // log(1 + exp(x)) = max(x, 0) + log(1 + v), v = exp(-|x|), to a few 1e-7 relative everywhere.
 // log(1 + v) = 2 artanh(s) with s = v / (2 + v) <= 1/3, by its series in s^2 up to s^13 / 13 (the next
 // term is under 2e-8 of the first).  The product |x| log2(e) is kept in two parts, since its rounding
-// would come back as a relative error of v.
+// would come back as a relative error of v; |x| is held at 100, where v is 0 already, so that -inf
+// gives 0 (a step that leaves the state as it is) and +inf itself.
 __device__ __forceinline__ float softplus(float x) {
-  const float m = -fabsf(x), hi = m * 1.44269504f;
-  const float lo = fmaf(m, 1.44269504f, -hi) + m * 1.92596299e-8f;  // log2(e) - 1.44269504
+  const float m = -fminf(fabsf(x), 100.f), hi = m * 1.44269504f;
+  // (the second factor: log2(e) less the fp32 value of the first)
+  const float lo = fmaf(m, 1.44269504f, -hi) + m * 1.92596299e-8f;
   float v = ex2(hi);
   v = fmaf(v, 0.69314718f * lo, v);
   const float s = v * rcp(2.f + v), s2 = s * s;
@@ -72,7 +74,7 @@ __device__ __forceinline__ float softplus(float x) {
   q = fmaf(q, s2, 1.f / 5.f);
   q = fmaf(q, s2, 1.f / 3.f);
   q = fmaf(q * s2, s, s);
-  return fmaxf(x, 0.f) + (q + q);
+  return x != x ? x : fmaxf(x, 0.f) + (q + q);
 }
 
 struct ConvArgs {

@@ -465,3 +465,55 @@ def test_ssm_fwd_cut_sequences_among_short_ones(lens):
     within(got, want, HALF_STEP * size)
     check_states(final, last, size_s)
     assert kda.device_status() == 0
+
+
+@pytest.mark.parametrize("low", [float("-inf"), torch.finfo(torch.bfloat16).min, -90.0])
+def test_ssm_steps_of_nothing_leave_the_state_as_it_is(low):
+    """A step of -inf, of the type's lowest value or far below 0 is 0 after softplus, in both forms."""
+    lens, H, P, N = [200, 3], 2, 64, 64
+    i, S0 = scan_case(lens, H, P, 1, N, seed=21)
+    i["dt"] = i["dt"].clone()
+    i["dt"][5:150] = low
+    i["dt"][202] = low
+    want, last, size, size_s = ref.ssm(lens=lens, S=S0, **i)
+    d = {k: cuda(v) for k, v in i.items()}
+    final = torch.empty(2, H, N, P, device="cuda")
+    got = kda.ssm_fwd(cu_seqlens=cu_of(lens), S0=cuda(S0), S_final=final, **d)
+    within(got, want, HALF_STEP * size)
+    check_states(final, last, size_s)
+    pool = cuda(S0)
+    got = kda.ssm_tokens(state_pool=pool, cu_seqlens=cu_of(lens), **d)
+    within(got, want, SUM32 * size)
+    check_states(pool, last, size_s)
+
+
+@pytest.mark.parametrize("value", [1e4, 40.0, 21.0, 19.0, 1.0, 0.0, -1.0, -20.0])
+def test_ssm_softplus_over_its_range(value):
+    """One token from nothing: the state is dt B x^T, so its step shows."""
+    H, P, N = 1, 64, 64
+    i, _ = scan_case([1], H, P, 1, N, seed=22, drop=("dt_bias", "z"))
+    i["dt"] = torch.full((1, 1), value, dtype=torch.bfloat16)
+    i["A"] = torch.tensor([-1e-6])
+    S = torch.zeros(1, H, N, P)
+    _, last, _, size_s = ref.ssm(lens=[1], S=S, **i)
+    d = {k: cuda(v) for k, v in i.items()}
+    for form in (0, 1):
+        pool = cuda(S)
+        if form:
+            kda.ssm_tokens(state_pool=pool, **d)
+        else:
+            kda.ssm_fwd(S_final=pool, **d)
+        check_states(pool, last, size_s)
+
+
+def test_ssm_nan_step_is_not_lost():
+    i, S0 = scan_case([4], 1, 64, 1, 64, seed=23)
+    i["dt"] = i["dt"].clone()
+    i["dt"][2] = float("nan")
+    d = {k: cuda(v) for k, v in i.items()}
+    pool = cuda(S0)
+    o = kda.ssm_tokens(state_pool=pool, cu_seqlens=cu_of([4]), **d)
+    assert torch.isnan(pool).all() and torch.isnan(o[2:]).all() and not torch.isnan(o[:2]).any()
+    final = torch.empty(1, 1, 64, 64, device="cuda")
+    kda.ssm_fwd(S0=cuda(S0), S_final=final, **d)
+    assert torch.isnan(final).all()

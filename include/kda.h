@@ -362,10 +362,15 @@ int kda_conv_tokens(const kda_bf16 *x, int64_t ldx, const kda_bf16 *weight, cons
  * 127 tokens before it on; other sequences are not touched by it.
  * Rows of x, B, C, z and o start on 16-byte boundaries (pointers 16-byte
  * aligned, strides multiples of 8); dt has no alignment beyond its type's.
- *   workspace   device scratch, 16-byte aligned, of workspace_bytes bytes
- *               (kda_ssm_fwd_workspace_bytes); not to be shared by calls that
- *               overlap on the GPU.
- *   Errors: KDA_ERR_NULL, _SHAPE, _ALIGN, _UNSUPPORTED, _WORKSPACE, _CUDA.
+ *   workspace   device scratch, 16-byte aligned, of workspace_bytes bytes; not
+ *               to be shared by calls that overlap on the GPU.  With fewer
+ *               bytes than kda_ssm_fwd_workspace_bytes() (or NULL) no sequence
+ *               is cut into segments that run side by side: the same results
+ *               up to rounding, slower for few long sequences.
+ * With softplus, a step of -inf (or far below 0) is 0: that token leaves the
+ * state as it is.  Bounded in-kernel waits that give up are recorded as
+ * KDA_ERR_TIMEOUT in the device status word.
+ *   Errors: KDA_ERR_NULL, _SHAPE, _ALIGN, _UNSUPPORTED, _CUDA.
  */
 int kda_ssm_fwd(const kda_bf16 *x, int64_t ldx, const kda_bf16 *dt, int64_t lddt, const float *A,
                 const kda_bf16 *B, int64_t ldb, const kda_bf16 *C, int64_t ldc, const float *D,

@@ -517,3 +517,48 @@ def test_ssm_nan_step_is_not_lost():
     final = torch.empty(1, 1, 64, 64, device="cuda")
     kda.ssm_fwd(S0=cuda(S0), S_final=final, **d)
     assert torch.isnan(final).all()
+
+
+# ---- offsets beyond 32 bits ----------------------------------------------------------------------
+
+def test_rows_and_slots_beyond_two_to_the_31():
+    """Rows of a buffer of 2.6e9 elements, and the last slots of pools as large: the same as small ones."""
+    total, ld, D, H, P, N = 40000, 65536, 64, 1, 64, 64
+    buf = torch.empty(total, ld, dtype=torch.bfloat16, device="cuda")
+    small = torch.randn(total, D, device="cuda").bfloat16()
+    x = buf[:, 1024:1024 + D]
+    x.copy_(small)
+    w = torch.randn(D, 4, device="cuda").bfloat16()
+    assert torch.equal(kda.conv_fwd(x, w), kda.conv_fwd(small, w))
+    rest = ref.ssm_inputs(total, H, P, 1, N, 5)
+    d = {k: cuda(v) for k, v in rest.items()}
+    want = kda.ssm_fwd(**dict(d, x=small.view(total, H, P)))
+    assert torch.equal(kda.ssm_fwd(**dict(d, x=x.unflatten(1, (H, P)))), want)
+    out = buf[:, 4096:4096 + D].unflatten(1, (H, P))
+    kda.ssm_fwd(o=out, **dict(d, x=small.view(total, H, P)))
+    assert torch.equal(out, want)
+    del buf, x, out
+    n, slots = 3, 600000
+    pool = torch.empty(slots, H, N, P, device="cuda")
+    conv = torch.empty(slots * 20, 3, D, dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([slots - 1, 5, slots - 7], dtype=torch.int32, device="cuda")
+    few = torch.randn(n, H, N, P, device="cuda")
+    held = torch.randn(n, 3, D, device="cuda").bfloat16()
+    pool[at.long()], conv[at.long() * 20] = few, held
+    t = {k: v[:n] if k in ("x", "dt", "B", "C", "z") else v for k, v in d.items()}
+    assert torch.equal(kda.ssm_tokens(state_pool=pool, slots=at, **t), kda.ssm_tokens(state_pool=few, **t))
+    assert torch.equal(pool[at.long()], few)
+    assert torch.equal(kda.conv_tokens(small[:n], w, None, conv, slots=at * 20),
+                       kda.conv_tokens(small[:n], w, None, held))
+    assert torch.equal(conv[at.long() * 20], held)
+
+
+def test_verify_rows_beyond_two_to_the_31():
+    n, V = 20000, 131072
+    p = torch.zeros(n, V, device="cuda")
+    want = torch.randint(0, V, (n,), device="cuda")
+    p[torch.arange(n, device="cuda"), want] = 1.0
+    out, count = kda.verify_draft(p, torch.zeros(n, dtype=torch.int32, device="cuda"),
+                                  torch.rand(n, device="cuda"),
+                                  torch.arange(n + 1, dtype=torch.int32, device="cuda"))
+    assert torch.equal(out.long(), want) and (count == 1).all()

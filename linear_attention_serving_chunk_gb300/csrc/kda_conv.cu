@@ -288,8 +288,8 @@ bool vector_rows(const ConvArgs &a) {
          aligned16(a.state_out);
 }
 
-// Tokens of a tile: as many as leave every SM two threads' worth of its 2048 slots (a tile reads W - 1
-// rows in front of its own again), between 8 and 64.
+// Tokens of a tile, 8 to 64: as many as leave 1024 threads to every SM (a tile reads W - 1 rows in front
+// of its own again).
 constexpr int64_t kTargetThreads = 152 * 1024;
 
 template <int W, int VEC>

@@ -4,12 +4,11 @@
 //   dt = softplus(raw + dt_bias),  a = exp(dt A_h)
 //   S <- a S + B (dt x)^T,   o = (S^T C + D_h x) silu(z)
 //
-// Bound by memory for short runs: a state is read once and, with commit, written once.  One
-// CTA owns one state; TPR = P / 4 of its threads lie along a row (4 columns each) and its row groups along
-// N, as in the KDA decode step.  The tokens of a run are staged TB at a time (B, C
-// and x in fp32), a thread then takes its block of the state through all of them and leaves its part
-// of S^T C per token in shared memory: two barriers per TB tokens.  The arithmetic is packed fp32x2
-// over column pairs.
+// Bound by memory for short runs: a state is read once and, with commit, written once.  One CTA owns one
+// state; TPR = P / 4 of its threads lie along a row (4 columns each) and its row groups along N, as in the
+// KDA decode step.  The tokens of a run are staged TB at a time (B, C and x in fp32), a thread then takes
+// its block of the state through all of them and leaves its part of S^T C per token in shared memory: two
+// barriers per TB tokens.  The arithmetic is packed fp32x2 over column pairs.
 //
 // One token on 512 x 32 states of 128 x 128: 315 us, 6.85 TB/s, the rate of a plain copy.  Runs of 1 to 5
 // tokens without commit on 256 x 32 states of 128 x 64: 60 us, 4.6 TB/s.  There a CTA's own chain counts

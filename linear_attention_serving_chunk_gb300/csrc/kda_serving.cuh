@@ -114,12 +114,11 @@ struct VerifyArgs {
 };
 
 // The step of one token: dt after bias and softplus.
-__device__ __forceinline__ float ssm_step(const SsmArgs &a, float raw, int h) {
-  if (a.dt_bias) raw += a.dt_bias[h];
-  return a.softplus ? softplus(raw) : raw;
+__device__ __forceinline__ float ssm_step(const SsmArgs &a, float raw, float bias) {
+  return a.softplus ? softplus(raw + bias) : raw + bias;
 }
 __device__ __forceinline__ float ssm_dt(const SsmArgs &a, int64_t t, int h) {
-  return ssm_step(a, bf2f(a.dt[t * a.lddt + h]), h);
+  return ssm_step(a, bf2f(a.dt[t * a.lddt + h]), a.dt_bias ? a.dt_bias[h] : 0.f);
 }
 
 int *status_word(cudaStream_t st);

@@ -39,8 +39,8 @@
 // when its M is built; M takes the columns of its G, 32 tokens at a time.  The gate and the result
 // pass through the chunk's X tile once nothing reads it any more.  In the first pass the token warps
 // build X' too, and the output warps keep the state.
-// What bounds it (32768 packed tokens x 64 heads of 64, N = 128, gate: 554 us, of which the first pass
-// 154; 131072 tokens x 16 heads of 128: 776 us, of which 200).  A chunk of 128 tokens x 128 columns takes
+// What bounds it (32768 packed tokens x 64 heads of 64, N = 128, gate: 527 us, of which the first pass
+// 154; 131072 tokens x 16 heads of 128: 721 us, of which 200).  A chunk of 128 tokens x 128 columns takes
 // 12,000 cycles in the second pass and 6,000 in the first.  Its products would take 3,600 at the
 // tensor cores' rate (they are busy 26 % of the time; leaving most of them out saved 2 %), its
 // tiles 1,200 at the memory's.  The element-wise work decides: about 25,000 warp instructions, which
@@ -83,24 +83,32 @@ constexpr uint32_t TILE = 32 * KiB;
 constexpr uint32_t SM_X = 0;                // X, two chunks
 constexpr uint32_t SM_B = 2 * TILE;         // (first pass: two chunks)
 constexpr uint32_t SM_C = 3 * TILE;
-constexpr uint32_t SM_XP = 4 * TILE;        // X': 32 tokens (first pass: three buffers)
+constexpr uint32_t SM_XP = 4 * TILE;        // X': 32 tokens (first pass: three of them)
 constexpr uint32_t SM_SP = SM_XP + 24 * KiB;  // S^T: two planes of [128 columns][N / 64 regions]
 constexpr uint32_t SP_PLANE = 32 * KiB;
 constexpr uint32_t SM_DEC = SM_SP + 2 * SP_PLANE;  // decays: [2 chunks][2 heads] (first pass: 2 more)
 constexpr uint32_t SM_DEC2 = SM_XP + 72 * KiB;
 constexpr uint32_t DEC_BYTES = 5 * 512 + 32;
 constexpr uint32_t SM_BAR = SM_DEC + 4 * DEC_BYTES;
-constexpr uint32_t SM_MISC = SM_BAR + 304;
+constexpr uint32_t SM_MISC = SM_BAR + 320;
 constexpr uint32_t SM_BYTES = SM_MISC + 64;
 static_assert(SM_BYTES <= 232448 && SM_DEC2 + 4 * DEC_BYTES <= SM_DEC, "shared memory budget");
 
-// X' of a round: [3 planes][2 regions of 64 columns][TOKENS rows]
+// X' of a round: [3 planes][2 regions of 64 columns][TOKENS rows].  In the second pass rounds 0 and 3 of
+// a chunk share a buffer; 1 and 2 take the place of the state's planes, which C S has read by then (with
+// the one buffer for all four, a quarter of the state warps' time went into waiting for it).
 template <bool STATE_ONLY>
 struct Weighted {
-  static constexpr int TOKENS = 32, BUFS = STATE_ONLY ? 3 : 1;
+  static constexpr int TOKENS = 32, BUFS = STATE_ONLY ? 3 : 4;
   static constexpr int ROUNDS = kQ / TOKENS;
   static constexpr uint32_t REGION = TOKENS * 128, PLANE = 2 * REGION, BYTES = 3 * PLANE;
-  static_assert(SM_XP + BUFS * BYTES <= (STATE_ONLY ? SM_DEC2 : SM_SP), "X' buffers");
+  static_assert(STATE_ONLY ? SM_XP + 3 * BYTES <= SM_DEC2
+                           : SM_XP + BYTES <= SM_SP && SM_SP + 2 * BYTES <= SM_DEC, "X' buffers");
+  static __device__ __forceinline__ uint32_t place(int i) {
+    const uint32_t k = i % BUFS;
+    if (STATE_ONLY) return SM_XP + k * BYTES;
+    return k == 1 || k == 2 ? SM_SP + (k - 1) * BYTES : SM_XP;
+  }
 };
 
 // Decays of one (chunk, head): offsets in bytes
@@ -114,10 +122,10 @@ constexpr uint32_t DC_T = 2560;      // log2 decays of the four blocks; then the
 // mbarriers.  Two of each kind: of chunk c the one of its parity, in phase c / 2.  F: a tile has come;
 // D: an MMA is done; A: warps have arrived.  FIN is for a wait that has given up.
 enum Bar : int { FX, FC, FB, DG, DCS, DDS, DY, AM, AS, AY, AO, FIN, NBAR };
-// One for each X' buffer: filled, and read.
-constexpr uint32_t BAR_AXP = SM_BAR + 16 * NBAR, BAR_DXP = BAR_AXP + 24;
+// One for each X' buffer (second pass: for each round of a chunk): filled, and read.
+constexpr uint32_t BAR_AXP = SM_BAR + 16 * NBAR, BAR_DXP = BAR_AXP + 32;
 // One for each buffer of decays: written, and no longer needed.
-constexpr uint32_t BAR_PREP = BAR_DXP + 24, BAR_DFREE = BAR_PREP + 32;
+constexpr uint32_t BAR_PREP = BAR_DXP + 32, BAR_DFREE = BAR_PREP + 32;
 static_assert(BAR_DFREE + 32 <= SM_MISC, "barriers");
 
 // TMEM columns: two of G, Y, dS (the first pass: two of dS, and S)
@@ -488,7 +496,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
           tc_fence_after();
           if (one) {
             const uint64_t xp =
-                sw128_desc(sb + SM_XP + (i % XP::BUFS) * XP::BYTES, XP::REGION, 1024u);
+                sw128_desc(sb + XP::place(i), XP::REGION, 1024u);
             constexpr int STEPS = XP::TOKENS / 16;
 #pragma unroll
             for (int k = 0; k < 3 * STEPS; ++k)
@@ -518,6 +526,12 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         }
       };
       const int first = warp == kDecayWarp ? 0 : 1;
+      float A2s[HEADS], biases[HEADS];
+#pragma unroll
+      for (int h = 0; h < HEADS; ++h) {
+        A2s[h] = h < heads ? a.A[h0 + h] * 1.44269504088896340736f : 0.f;
+        biases[h] = h < heads && a.dt_bias ? a.dt_bias[h0 + h] : 0.f;
+      }
       fetch(first);
 #pragma unroll 1
       for (int it = first; it < n_chunks * HEADS; it += DECAY_WARPS) {
@@ -530,11 +544,12 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         if (c >= DECS && !warp_wait(dec_free(c), c / DECS - 1)) break;
         {
           const bool mine = hh < heads;
-          const float A2 = mine ? a.A[h0 + hh] * 1.44269504088896340736f : 0.f;
+          const float A2 = hh ? A2s[HEADS - 1] : A2s[0];
+          const float bias = hh ? biases[HEADS - 1] : biases[0];
           float dt[4], pre[4], suf[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            dt[i] = mine && 4 * lane + i < len ? ssm_step(a, __uint_as_float(raw[i] << 16), h0 + hh) : 0.f;
+            dt[i] = mine && 4 * lane + i < len ? ssm_step(a, __uint_as_float(raw[i] << 16), bias) : 0.f;
           pre[0] = dt[0] * A2;
 #pragma unroll
           for (int i = 1; i < 4; ++i) pre[i] = pre[i - 1] + dt[i] * A2;
@@ -633,11 +648,9 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
 #pragma unroll
           for (int i = 0; i < 8; ++i, from += 4 * a.ldz)
             if (4 * i + r0 < left) z[i] = *reinterpret_cast<const uint4 *>(from);
-          if (piece == 0 && left > kQ) {  // the next chunk's lines
-            from = gate_at + kQ * a.ldz;
-            for (int i = r0; i < 32 && i + kQ < left; i += 4, from += 4 * a.ldz)
-              asm volatile("prefetch.global.L2 [%0];" ::"l"(from));
-          }
+          if (lane + kQ < left)  // the next chunk's lines
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                a.z + static_cast<int64_t>(seg.begin + (c + 1) * kQ + quad * 32 + lane) * a.ldz + cols));
         }
         // X is read by the state's warps until dS is done, by the others until Y is
         if (!warp_wait_c(DDS, c) || !warp_wait_c(DY, c)) break;
@@ -837,7 +850,12 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     // X' of the tokens of round r of chunk c: a thread takes 8 columns of a row, of one region or both
     auto put_weighted = [&](int c, int r) -> bool {
       const int i = XP::ROUNDS * c + r;
-      if (i >= XP::BUFS && !warp_wait(xp_read(i), i / XP::BUFS - 1)) return false;
+      if constexpr (STATE_ONLY) {
+        if (i >= XP::BUFS && !warp_wait(xp_read(i), i / XP::BUFS - 1)) return false;
+      } else {
+        if (r == 1 && !warp_wait_c(DCS, c)) return false;
+        if (r == 3 && !warp_wait(xp_read(0), c)) return false;
+      }
       const int j = tid & 7, row = (tid >> 3) % XP::TOKENS, tok = XP::TOKENS * r + row;
       const uint32_t flip = static_cast<uint32_t>(j ^ (row & 7)) << 4;
       const uint32_t dec = decays(c, 0) + DC_W + 4 * tok;
@@ -858,7 +876,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
           f = __fadd2_rn(f, make_float2(-truncated(f.x), -truncated(f.y)));
           out[2][e] = upper(f.x, f.y);
         }
-        const uint32_t to = sb + SM_XP + (i % XP::BUFS) * XP::BYTES + region * XP::REGION + row * 128u + flip;
+        const uint32_t to = sb + XP::place(i) + region * XP::REGION + row * 128u + flip;
 #pragma unroll
         for (int k = 0; k < 3; ++k)
           S.u128(to + k * XP::PLANE) = make_uint4(out[k][0], out[k][1], out[k][2], out[k][3]);
@@ -945,10 +963,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         }
         tc_fence_before();
         arrive(dec_free(c));
-        if (c + 1 < n_chunks) {
-          if (!(ok = warp_wait_c(DCS, c))) break;  // the planes are read until then
-          put_state(c + 1);
-        }
+        if (c + 1 < n_chunks) put_state(c + 1);
       }
       if (ok && in && seg.last && a.S_out) {
         float *to = a.S_out + seg.seq * state + at0;

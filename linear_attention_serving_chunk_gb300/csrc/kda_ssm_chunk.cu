@@ -8,8 +8,9 @@
 // One CTA carries 128 state columns (two heads of 64 that share their B and C, or one head of 128)
 // through the chunks of one segment of a sequence.  All products are tcgen05 MMAs of 128 rows:
 //   G   [token x token]  = C B^T                       operands as they came by TMA
-//   Y   [token x column] = C S                         then scaled by e^{l_t}, D x added
-//                       += M X                         M = G * e^{l_t - l_s} dt_s, causal, from TMEM
+//   C S [token x column]
+//   Y   [token x column] = M X                         M = G * e^{l_t - l_s} dt_s, causal, from TMEM;
+//                                                      then e^{l_t} (C S) and D x are added
 //   dS^T[column x n]     = X'^T B                      X' = e^{l_end - l_s} dt_s x_s
 //
 // Roundings.  x, B and C are bf16 and enter exactly.  X' is split into three bf16 planes that hold
@@ -30,22 +31,24 @@
 //
 // Roles, each at its own pace and with its own registers, joined by mbarriers:
 //   state    (8 warps)  X', 32 tokens at a time; the state and its planes for the next chunk
-//   token    (8 warps)  M; Y = e^{l_t} C S + D x before M X is added
+//   token    (8 warps)  M; e^{l_t} C S + D x added to M X
 //   output   (8 warps)  gate and store
-//   one warp each       TMA loads; the MMAs of Y; the other MMAs; the decays of the chunks ahead, and
+//   one warp each       TMA loads; G, C S and M X; dS; the decays of the chunks ahead, and
 //                       the rows behind a sequence's end cleared, so that nothing of the next
 //                       sequence is multiplied, not even by zero
-// X has two buffers, C and B have one.  G has two places in TMEM, so that the next chunk's G is there
-// when its M is built; M takes the columns of its G, 32 tokens at a time.  The gate and the result
+// X has two buffers, C and B have one.  M takes the columns of its G, 16 tokens at a time.  C S and M X
+// have a place of their own in TMEM, so that the next chunk's C S need not wait for the result's warps
+// (added up in one place, with G in two, 527 us instead of 487).  The gate and the result
 // pass through the chunk's X tile once nothing reads it any more.  In the first pass the token warps
 // build X' too, and the output warps keep the state.
-// What bounds it (32768 packed tokens x 64 heads of 64, N = 128, gate: 527 us, of which the first pass
-// 154; 131072 tokens x 16 heads of 128: 721 us, of which 200).  A chunk of 128 tokens x 128 columns takes
-// 12,000 cycles in the second pass and 6,000 in the first.  Its products would take 3,600 at the
-// tensor cores' rate (they are busy 26 % of the time; leaving most of them out saved 2 %), its
-// tiles 1,200 at the memory's.  The element-wise work decides: about 25,000 warp instructions, which
-// the 24 working warps issue at 0.45 a cycle and scheduler, each waiting for its own results (shared
-// memory, TMEM, exponentials) most of the time.  Left out, the gate saved 13 %, the weights M 15 %.  So
+// What bounds it (32768 packed tokens x 64 heads of 64, N = 128, gate: 487 us, of which the first pass
+// 154; 131072 tokens x 16 heads of 128: 725 us, of which 200).  A chunk of 128 tokens x 128 columns takes
+// about 10,000 cycles in the second pass (9,000 without the gate) and 5,000 in the first.  Its products
+// would take 3,600 at the tensor cores' rate, its tiles 1,200 at the memory's.  The element-wise work
+// decides, each warp waiting for its own results (shared memory, TMEM, exponentials) most of the time: by
+// the clock the state's warps are at work for 80 % of a chunk, the result's for 75, the token's for 60,
+// the rest being the way from one role to the next.  In the first pass no part stands out: without the
+// products 15 us less, without the second and third plane 30, without the state's sum 10.  So
 // the roles run side by side instead of one after another (one group of 16 warps that did all of it in
 // turn took 667 us), the loops are rolled where they can be (the code of the roles shares the instruction
 // caches: with 206 KB of it a quarter of all stalls were for instructions) and a wait is a few
@@ -90,7 +93,7 @@ constexpr uint32_t SM_DEC = SM_SP + 2 * SP_PLANE;  // decays: [2 chunks][2 heads
 constexpr uint32_t SM_DEC2 = SM_XP + 72 * KiB;
 constexpr uint32_t DEC_BYTES = 5 * 512 + 32;
 constexpr uint32_t SM_BAR = SM_DEC + 4 * DEC_BYTES;
-constexpr uint32_t SM_MISC = SM_BAR + 320;
+constexpr uint32_t SM_MISC = SM_BAR + 336;
 constexpr uint32_t SM_BYTES = SM_MISC + 64;
 static_assert(SM_BYTES <= 232448 && SM_DEC2 + 4 * DEC_BYTES <= SM_DEC, "shared memory budget");
 
@@ -120,20 +123,19 @@ constexpr uint32_t DC_W = 2048;      // decay to the chunk's end, times dt
 constexpr uint32_t DC_T = 2560;      // log2 decays of the four blocks; then the chunk's decay
 
 // mbarriers.  Two of each kind: of chunk c the one of its parity, in phase c / 2.  F: a tile has come;
-// D: an MMA is done; A: warps have arrived.  FIN is for a wait that has given up.
-enum Bar : int { FX, FC, FB, DG, DCS, DDS, DY, AM, AS, AY, AO, FIN, NBAR };
+// D: an MMA is done; A: warps have arrived (AM: M is there; AF: the result; AS: the state's planes; AY: Y has
+// been read, in the first pass dS; AO: the result has left X's tile).  FIN is for a wait that has given up.
+enum Bar : int { FX, FC, FB, DG, DCS, DDS, DY, AM, AF, AS, AY, AO, FIN, NBAR };
 // One for each X' buffer (second pass: for each round of a chunk): filled, and read.
 constexpr uint32_t BAR_AXP = SM_BAR + 16 * NBAR, BAR_DXP = BAR_AXP + 32;
 // One for each buffer of decays: written, and no longer needed.
 constexpr uint32_t BAR_PREP = BAR_DXP + 32, BAR_DFREE = BAR_PREP + 32;
 static_assert(BAR_DFREE + 32 <= SM_MISC, "barriers");
 
-// TMEM columns: two of G, Y, dS (the first pass: two of dS, and S)
-constexpr uint32_t TM_Y = 256, TM_DS = 384, TM_S = 256;
-// M of head h in the columns of its G: tokens [16 k, 16 k + 16) in 8 of the 32 that held their G
-__device__ __forceinline__ constexpr uint32_t tm_m(int h, int k) {
-  return 32 * (k >> 1) + 16 * h + 8 * (k & 1);
-}
+// TMEM columns: G (later M), C S, Y, dS (the first pass: two of dS, and S)
+constexpr uint32_t TM_CS = 128, TM_Y = 256, TM_DS = 384, TM_S = 256;
+// M of head h in the columns of its G: tokens [16 k, 16 k + 16) in 8 of the 16 that held their G
+__device__ __forceinline__ constexpr uint32_t tm_m(int h, int k) { return 16 * k + 8 * h; }
 
 constexpr uint32_t kPolls = 1u << 20;
 
@@ -168,6 +170,13 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uin
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
       : "memory");
 }
 
@@ -329,7 +338,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
   if (tid == 0) {
     for (int k = 0; k < NBAR; ++k) {
       uint32_t count = 1;
-      if (k == AM) count = kTokenWarps;
+      if (k == AM || k == AF) count = kTokenWarps;
       if (k == AS) count = kStateWarps;
       if (k == AY || k == AO) count = kOutWarps;
       mbar_init(bar(k, 0), count);
@@ -403,10 +412,10 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
           mbar_expect_tx(bar(FX, c), TILE);
           for (int r = 0; r < 2; ++r)
             tma_load_2d(tile_x(c) + r * REG128, &tm_x, h0 * P + 64 * r, t, bar(FX, c));
-          if (!STATE_ONLY && c > 0 && !(ok = wait_c(DDS, c - 1))) break;
+          if (!STATE_ONLY && c > 0 && !(ok = wait_c(DDS, c - 1) && wait_c(DG, c - 1))) break;
           load_bc(&tm_b, tile_b(c), bar(FB, c));
           if constexpr (!STATE_ONLY) {
-            if (c > 0 && !(ok = wait_c(DCS, c - 1) && wait_c(DG, c - 1))) break;
+            if (c > 0 && !(ok = wait_c(DCS, c - 1))) break;
             load_bc(&tm_c, tile_c, bar(FC, c));
           }
         }
@@ -421,14 +430,27 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     } else if (warp == kTokenMma && !STATE_ONLY) {
       // A whole warp goes through an MMA loop (so that addresses and descriptors stay in uniform
       // registers); one lane issues.
-      constexpr uint32_t ID_CS = idesc_mma(128, 128, kFmtBF16, kFmtBF16, 0, 0);
+      constexpr uint32_t ID_G = idesc_mma(128, 128, kFmtBF16, kFmtBF16, 0, 0), ID_CS = ID_G;
       constexpr uint32_t ID_MX = idesc_mma(128, P, kFmtBF16, kFmtBF16, 0, 1);
       const uint64_t c_k = sw128_desc(tile_c, 16u, 1024u), s_k = sw128_desc(sb + SM_SP, 16u, 1024u);
       const bool one = elect();
       bool ok = true;
       for (int c = 0; c < n_chunks; ++c) {
         const uint64_t x_mn = sw128_desc(tile_x(c), REG128, 1024u);
-        ok = warp_wait_c(FC, c) && warp_wait_c(AS, c) && (c == 0 || warp_wait_c(AY, c - 1));
+        ok = warp_wait_c(FB, c) && warp_wait_c(FC, c) && (c == 0 || warp_wait_c(DY, c - 1));
+        if (!ok) break;
+        tc_fence_after();
+        if (one) {
+          const uint64_t b_k = sw128_desc(tile_b(c), 16u, 1024u);
+#pragma unroll 1
+          for (int r = 0; r < N / 64; ++r)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f16(tmem, c_k + r * (REG128 >> 4) + 2 * k, b_k + r * (REG128 >> 4) + 2 * k, ID_G,
+                      r + k > 0);
+          mma_commit(bar(DG, c));
+        }
+        ok = warp_wait_c(AS, c) && (c == 0 || warp_wait_c(AF, c - 1));
         if (!ok) break;
         tc_fence_after();
         if (one) {
@@ -437,22 +459,22 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             const uint32_t at = (r % (N / 64)) * (REG128 >> 4);
             const uint64_t cd = c_k + at, sd = s_k + at + (r / (N / 64)) * (SP_PLANE >> 4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f16(tmem + TM_Y, cd + 2 * k, sd + 2 * k, ID_CS, r + k > 0);
+            for (int k = 0; k < 4; ++k) mma_f16(tmem + TM_CS, cd + 2 * k, sd + 2 * k, ID_CS, r + k > 0);
           }
           mma_commit(bar(DCS, c));
         }
-        ok = warp_wait_c(FX, c) && warp_wait_c(AM, c);
+        ok = warp_wait_c(FX, c) && warp_wait_c(AM, c) && (c == 0 || warp_wait_c(AY, c - 1));
         if (!ok) break;
         tc_fence_after();
         if (one) {
 #pragma unroll 1
           for (int r = 0; r < 2 * HEADS; ++r) {  // (head, 64 tokens); 16 tokens in a step
             const int h = r / 2, k0 = 4 * (r % 2);
-            const uint32_t m = tmem + 128 * (c & 1) + tm_m(h, k0);
+            const uint32_t m = tmem + tm_m(h, k0);
             const uint64_t xd = x_mn + ((h * REG128 + k0 * 2048u) >> 4);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f16_ta(tmem + TM_Y + 64 * h, m + tm_m(0, k), xd + 128 * k, ID_MX, 1);
+              mma_f16_ta(tmem + TM_Y + 64 * h, m + tm_m(0, k), xd + 128 * k, ID_MX, k0 + k > 0);
           }
           mma_commit(bar(DY, c));
         }
@@ -462,28 +484,12 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         mbar_wait_bounded(bar(FIN, 0), 0, 1u << 16);
       }
     } else if (warp == kStateMma) {
-      constexpr uint32_t ID_G = idesc_mma(128, 128, kFmtBF16, kFmtBF16, 0, 0);
       constexpr uint32_t ID_DS = idesc_mma(128, N, kFmtBF16, kFmtBF16, 1, 1);
       const bool one = elect();
       bool ok = true;
       for (int c = 0; c < n_chunks && ok; ++c) {
         ok = warp_wait_c(FB, c) && warp_wait(prepared(c), c / DECS);
-        if constexpr (!STATE_ONLY) {
-          ok = ok && warp_wait_c(FC, c) && (c < 2 || warp_wait_c(DY, c - 2));
-          if (!ok) break;
-          tc_fence_after();
-          if (one) {
-            const uint64_t c_k = sw128_desc(tile_c, 16u, 1024u);
-            const uint64_t b_k = sw128_desc(tile_b(c), 16u, 1024u);
-#pragma unroll 1
-            for (int r = 0; r < N / 64; ++r)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_f16(tmem + 128 * (c & 1), c_k + r * (REG128 >> 4) + 2 * k,
-                        b_k + r * (REG128 >> 4) + 2 * k, ID_G, r + k > 0);
-            mma_commit(bar(DG, c));
-          }
-        } else {
+        if constexpr (STATE_ONLY) {
           ok = ok && (c < 2 || warp_wait_c(AY, c - 2));
         }
         const uint64_t b_mn = sw128_desc(tile_b(c), REG128, 1024u);
@@ -653,7 +659,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 a.z + static_cast<int64_t>(seg.begin + (c + 1) * kQ + quad * 32 + lane) * a.ldz + cols));
         }
         // X is read by the state's warps until dS is done, by the others until Y is
-        if (!warp_wait_c(DDS, c) || !warp_wait_c(DY, c)) break;
+        if (!warp_wait_c(DDS, c) || !warp_wait_c(AF, c)) break;
         tc_fence_after();
         if (gate) {
 #pragma unroll
@@ -756,45 +762,45 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         const uint32_t dec = decays(c, 0);
         if (!warp_wait(prepared(c), c / DECS) || !warp_wait_c(FX, c) || !warp_wait_c(DG, c)) break;
         tc_fence_after();
-        // M, 32 tokens s at a time: blocks 0 and 3, or 1 and 2
+        // M, 32 tokens s at a time, of which a warp takes 16
 #pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
-          const int b = k == 0 ? half : 3 - half;
-          const uint32_t block = lanes + 128 * (c & 1) + tm_m(0, 2 * b);
-          float m[32];
+        for (int b = 0; b < 4; ++b) {
+          const int s0 = 32 * b + 16 * half;
+          float m[16];
           if (b > quad) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) m[i] = 0.f;
-            tmem_st32(block, m);
+            for (int i = 0; i < 16; ++i) m[i] = 0.f;
+            tmem_st16(lanes + s0, m);
             continue;
           }
-          tmem_ld32(block, m);
+          tmem_ld16(lanes + s0, m);
           tmem_wait_ld();
-#pragma unroll 1
+#pragma unroll
           for (int h = 0; h < HEADS; ++h) {
             const uint32_t d = dec + h * DEC_BYTES;
             const float lt = S.f32(d + DC_L + 4 * row);
-            float words[16];
+            uint32_t words[8];
             if (b < quad) {
               float l = lt;  // from the block's end to t
               for (int q = b + 1; q < quad; ++q) l += S.f32(d + DC_T + 4 * q);
               const float e = ex2(l);
               const float2 e2 = make_float2(e, e);
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(S.ptr(d + DC_F + 4 * (32 * b + i)));
+              for (int i = 0; i < 16; i += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(S.ptr(d + DC_F + 4 * (s0 + i)));
                 const float2 u = __fmul2_rn(make_float2(m[i], m[i + 1]),
                                             __fmul2_rn(make_float2(f.x, f.y), e2));
                 const float2 v = __fmul2_rn(make_float2(m[i + 2], m[i + 3]),
                                             __fmul2_rn(make_float2(f.z, f.w), e2));
-                words[i / 2] = __uint_as_float(pack_bf16x2(u.x, u.y));
-                words[i / 2 + 1] = __uint_as_float(pack_bf16x2(v.x, v.y));
+                words[i / 2] = pack_bf16x2(u.x, u.y);
+                words[i / 2 + 1] = pack_bf16x2(v.x, v.y);
               }
             } else {
+              const int t = lane - 16 * half;
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 l = *reinterpret_cast<const float4 *>(S.ptr(d + DC_L + 4 * (32 * b + i)));
-                const float4 w = *reinterpret_cast<const float4 *>(S.ptr(d + DC_DT + 4 * (32 * b + i)));
+              for (int i = 0; i < 16; i += 4) {
+                const float4 l = *reinterpret_cast<const float4 *>(S.ptr(d + DC_L + 4 * (s0 + i)));
+                const float4 w = *reinterpret_cast<const float4 *>(S.ptr(d + DC_DT + 4 * (s0 + i)));
                 const float2 d0 = __fadd2_rn(make_float2(lt, lt), make_float2(-l.x, -l.y));
                 const float2 d1 = __fadd2_rn(make_float2(lt, lt), make_float2(-l.z, -l.w));
                 const float2 u = __fmul2_rn(make_float2(m[i], m[i + 1]),
@@ -804,44 +810,46 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                                             __fmul2_rn(make_float2(ex2(d1.x), ex2(d1.y)),
                                                        make_float2(w.z, w.w)));
                 // (a choice, not a product: what lies in the future may be infinite)
-                words[i / 2] = __uint_as_float(pack_bf16x2(i <= lane ? u.x : 0.f,
-                                                           i + 1 <= lane ? u.y : 0.f));
-                words[i / 2 + 1] = __uint_as_float(pack_bf16x2(i + 2 <= lane ? v.x : 0.f,
-                                                               i + 3 <= lane ? v.y : 0.f));
+                words[i / 2] = pack_bf16x2(i <= t ? u.x : 0.f, i + 1 <= t ? u.y : 0.f);
+                words[i / 2 + 1] = pack_bf16x2(i + 2 <= t ? v.x : 0.f, i + 3 <= t ? v.y : 0.f);
               }
             }
-            tmem_st16(block + 16 * h, words);
+            tmem_st8(lanes + s0 + 8 * h, words);
           }
-        }
-        if (!warp_wait_c(DCS, c)) break;
-        tc_fence_after();
-        // C S, scaled to each token, and D x
-        const float e = S.f32(dec + hout * DEC_BYTES + DC_E + 4 * row);
-        const float2 e2 = make_float2(e, e), skip2 = make_float2(skip, skip);
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
-          float y[32];
-          tmem_ld32(lanes + TM_Y + 64 * half + 32 * k, y);
-          tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 raw = S.u128(tile_x(c) + half * REG128 + row * 128u +
-                                     (static_cast<uint32_t>((4 * k + j) ^ (row & 7)) << 4));
-            const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int i = 8 * j + 2 * q;
-              const float2 f = __ffma2_rn(e2, make_float2(y[i], y[i + 1]),
-                                          __fmul2_rn(skip2, unpack_bf16x2(in[q])));
-              y[i] = f.x;
-              y[i + 1] = f.y;
-            }
-          }
-          tmem_st32(lanes + TM_Y + 64 * half + 32 * k, y);
         }
         tmem_wait_st();
         tc_fence_before();
         arrive(bar(AM, c));
+        if (!warp_wait_c(DCS, c) || !warp_wait_c(DY, c)) break;
+        tc_fence_after();
+        // C S, scaled to each token, and D x join M X
+        const float e = S.f32(dec + hout * DEC_BYTES + DC_E + 4 * row);
+        const float2 e2 = make_float2(e, e), skip2 = make_float2(skip, skip);
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          float y[16], cs[16];
+          tmem_ld16(lanes + TM_CS + 64 * half + 16 * k, cs);
+          tmem_ld16(lanes + TM_Y + 64 * half + 16 * k, y);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint4 raw = S.u128(tile_x(c) + half * REG128 + row * 128u +
+                                     (static_cast<uint32_t>((2 * k + j) ^ (row & 7)) << 4));
+            const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int i = 8 * j + 2 * q;
+              const float2 f = __ffma2_rn(e2, make_float2(cs[i], cs[i + 1]),
+                                          __ffma2_rn(skip2, unpack_bf16x2(in[q]), make_float2(y[i], y[i + 1])));
+              y[i] = f.x;
+              y[i + 1] = f.y;
+            }
+          }
+          tmem_st16(lanes + TM_Y + 64 * half + 16 * k, y);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(bar(AF, c));
         if (lane == 0) mbar_arrive(dec_free(c));
       }
   } else {
@@ -987,7 +995,7 @@ int column_blocks(int H, int P, int G) { return P == 128 ? H : G * ((H / G + 1) 
 
 // Tokens of a segment (0: no sequence is cut).  The host knows the mean length alone.  Costs in chunks of
 // the second pass, for sequences of the mean length cut into k segments each: a chunk of the first
-// pass is 0.4 of one (2.5 us against 6.2), starting a CTA one.  Where whole sequences do best but
+// pass is 0.5 of one (2.5 us against 5), starting a CTA one.  Where whole sequences do best but
 // the lengths may differ, those longer than an SM's share of all chunks are still cut: one long prompt
 // among short ones would keep its own few SMs busy long after the others are done.
 int64_t segment_tokens(int n_seq, int64_t total, int blocks, bool ragged) {
@@ -999,7 +1007,7 @@ int64_t segment_tokens(int n_seq, int64_t total, int blocks, bool ragged) {
     const int64_t per = (chunks + k - 1) / k;
     const int64_t tasks = static_cast<int64_t>(n_seq) * blocks;
     const double cost =
-        waves(tasks * k) * (per + 1.0) + (k > 1 ? waves(tasks * (k - 1)) * (0.4 * per + 1.0) : 0.0);
+        waves(tasks * k) * (per + 1.0) + (k > 1 ? waves(tasks * (k - 1)) * (0.5 * per + 1.0) : 0.0);
     if (k == 1 || cost < least) {
       least = cost;
       best = k == 1 ? 0 : per * kQ;

@@ -38,21 +38,22 @@
 //                       sequence is multiplied, not even by zero
 // X has two buffers, C and B have one.  M takes the columns of its G, 16 tokens at a time.  C S and M X
 // have a place of their own in TMEM, so that the next chunk's C S need not wait for the result's warps
-// (added up in one place, with G in two, 527 us instead of 487).  The gate and the result
+// (added up in one place, with G in two, 527 us where this took 487).  The gate and the result
 // pass through the chunk's X tile once nothing reads it any more.  In the first pass the token warps
 // build X' too, and the output warps keep the state.
-// What bounds it (32768 packed tokens x 64 heads of 64, N = 128, gate: 487 us, of which the first pass
-// 154; 131072 tokens x 16 heads of 128: 725 us, of which 200).  A chunk of 128 tokens x 128 columns takes
-// about 10,000 cycles in the second pass (9,000 without the gate) and 5,000 in the first.  Its products
-// would take 3,600 at the tensor cores' rate, its tiles 1,200 at the memory's.  The element-wise work
-// decides, each warp waiting for its own results (shared memory, TMEM, exponentials) most of the time: by
-// the clock the state's warps are at work for 80 % of a chunk, the result's for 75, the token's for 60,
-// the rest being the way from one role to the next.  In the first pass no part stands out: without the
-// products 15 us less, without the second and third plane 30, without the state's sum 10.  So
-// the roles run side by side instead of one after another (one group of 16 warps that did all of it in
-// turn took 667 us), the loops are rolled where they can be (the code of the roles shares the instruction
-// caches: with 206 KB of it a quarter of all stalls were for instructions) and a wait is a few
-// instructions.
+//
+// What bounds it (32768 packed tokens x 64 heads of 64, N = 128, gate: 443 us, of which the first pass
+// 108; 131072 tokens x 16 heads of 128: 721 us, of which 196).  A chunk of 128 tokens x 128 columns takes
+// 11,000 cycles in the second pass (9,000 without the gate) and 5,000 in the first.  Its products would
+// take 3,600 at the tensor cores' rate, its tiles 1,200 at the memory's.  The element-wise work decides,
+// each warp waiting for its own results (shared memory, TMEM, exponentials) most of the time: by the
+// clock the state's warps are at work for 80 % of a chunk, the result's for 75, the token's for 60, the
+// rest being the way from one role to the next.  In the first pass no part stands out: without the
+// products 15 us less, without the second and third plane 30, without the state's sum 10.  So the roles
+// run side by side instead of one after another (one group of 16 warps that did all of it in turn took
+// 667 us when this form took 655), the loops are rolled where they can be (the code of the roles shares
+// the instruction caches: with 206 KB of it a quarter of all stalls were for instructions) and a wait is
+// a few instructions.
 #include <string.h>
 
 #include "kda_pdl.cuh"
@@ -995,9 +996,12 @@ int column_blocks(int H, int P, int G) { return P == 128 ? H : G * ((H / G + 1) 
 
 // Tokens of a segment (0: no sequence is cut).  The host knows the mean length alone.  Costs in chunks of
 // the second pass, for sequences of the mean length cut into k segments each: a chunk of the first
-// pass is 0.5 of one (2.5 us against 5), starting a CTA one.  Where whole sequences do best but
-// the lengths may differ, those longer than an SM's share of all chunks are still cut: one long prompt
-// among short ones would keep its own few SMs busy long after the others are done.
+// pass is 0.5 of one (2.5 us against 5), starting a CTA one.  Where whole sequences do best but the
+// lengths may differ, long ones are still cut: one long prompt among short ones would keep its own few
+// SMs busy long after the others are done.  Cut at an SM's share of all chunks, the segments in front
+// are one wave at most; at half of it two, which leaves shorter pieces for the end.  (6 prompts of 1 to
+// 12001 tokens x 64 heads of 64, a share of 54 chunks: cut at 54 482 us, at 27 442, at 18 458; 16000 and
+// nine times 500 tokens, a share of 34: at 34 265 us, at 24 356, at 17 297.)
 int64_t segment_tokens(int n_seq, int64_t total, int blocks, bool ragged) {
   const int64_t chunks = (total / n_seq + kQ) / kQ;
   auto waves = [&](int64_t tasks) { return (tasks + kSMs - 1) / kSMs; };
@@ -1014,8 +1018,9 @@ int64_t segment_tokens(int n_seq, int64_t total, int blocks, bool ragged) {
     }
   }
   if (best == 0 && ragged && n_seq > 1) {
-    const int64_t share = waves(total / kQ * blocks), least_cut = share > 12 ? share : 12;
-    if (total >= 2 * least_cut * kQ) best = least_cut * kQ;
+    const int64_t share = waves(total / kQ * blocks);
+    const int64_t cut = share >= 48 ? share / 2 : share > 12 ? share : 12;
+    if (total >= 2 * cut * kQ) best = cut * kQ;
   }
   return best;
 }

@@ -422,7 +422,8 @@ int kda_ssm_tokens(const kda_bf16 *x, int64_t ldx, const kda_bf16 *dt, int64_t l
  *   n_out       int32 [n]: how many there are, accepted + 1.  It is also how
  *               many of the run's tokens belong in the recurrent states: the
  *               `used` of kda_conv_tokens and kda_ssm_tokens.
- * A drafted token outside [0, V) is refused and recorded as KDA_ERR_SHAPE; a
+ * A drafted token outside [0, V) is refused and recorded as KDA_ERR_SHAPE (a
+ * certain one has no weight to take out: the next token comes from p); a
  * malformed run gives n_out = 0 and KDA_ERR_SHAPE; a row without any finite
  * positive weight sum gives the token -1, not counted in n_out, and
  * KDA_ERR_RANGE.  V <= 2^22.

@@ -59,7 +59,7 @@ __device__ __forceinline__ float prob(const kda_bf16 *p, int64_t i) { return bf2
 template <typename T>
 struct Weights {
   const T *p, *q;
-  int without;  // -1: none
+  int without;  // a token of the row, or -1: none
 
   // w = hi + lo: the rounded difference, and what its rounding lost
   static __device__ __forceinline__ void weight(float pv, float qv, float &hi, float &lo) {
@@ -104,6 +104,17 @@ __device__ __forceinline__ double warp_scan(double v, int lane) {
 // side; otherwise 32 neighbouring ones a lane.
 template <typename T, bool VECTOR, bool SPREAD>
 __device__ __forceinline__ double segment_sum(const Weights<T> &w, int i0, int V, int lane) {
+  // The one segment that holds the token taken out is added element by element, without it (in double
+  // precision: what is left of it may be far smaller than that token's weight).
+  if (static_cast<unsigned>(w.without - i0) < kSeg) {
+    double v = 0.0;
+#pragma unroll 4
+    for (int k = 0; k < kSeg / 32; ++k) {
+      const int i = i0 + (SPREAD ? k * 32 + lane : lane * 32 + k);
+      if (i < V) v += w.one(i);
+    }
+    return v;
+  }
   Sum s;
   if constexpr (VECTOR) {
     constexpr int E = 16 / sizeof(T), STEPS = kSeg / (32 * E), AHEAD = STEPS < 4 ? STEPS : 4;
@@ -139,12 +150,6 @@ __device__ __forceinline__ double segment_sum(const Weights<T> &w, int i0, int V
       if (i < V) Weights<T>::weight(prob(w.p, i), w.q ? prob(w.q, i) : 0.f, hi, lo);
       s.add(hi, lo);
     }
-  }
-  // the token that is taken out, by the lane that added it
-  const int out = w.without - i0;
-  if (out >= 0 && out < kSeg) {
-    constexpr int E = VECTOR ? 16 / sizeof(T) : 1;
-    if (lane == (SPREAD ? out / E % 32 : out / 32)) s.add(-fmaxf(prob(w.p, w.without), 0.f), 0.f);
   }
   return s.value();
 }
@@ -197,8 +202,11 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(const VerifyArgs a) {
     for (int j = tid; j <= k; j += kVThreads)
       if (j != got) a.out_tokens[t0 + j] = j < got ? a.tokens[t0 + j + 1] : -1;
 
-  Weights<T> w{target + (t0 + got) * a.V, cut && draft ? draft + (t0 - b + got) * a.V : nullptr,
-               cut && !draft ? a.tokens[t0 + got + 1] : -1};
+  Weights<T> w{target + (t0 + got) * a.V, cut && draft ? draft + (t0 - b + got) * a.V : nullptr, -1};
+  if (cut && !draft) {
+    const int x = a.tokens[t0 + got + 1];
+    if (x >= 0 && x < a.V) w.without = x;  // (a token outside the row has no weight to take out)
+  }
   const int segs = (a.V + kSeg - 1) / kSeg;
   const int seg0 = static_cast<int>(static_cast<int64_t>(segs) * rank / ranks);
   const int seg1 = static_cast<int>(static_cast<int64_t>(segs) * (rank + 1) / ranks);

@@ -20,7 +20,10 @@
 // result, which adds an error of the size of the result's own rounding.
 //
 // Log decays are summed in blocks of 32 tokens from both ends (prefix for what is read at t, suffix
-// for what is kept of s), so that an exponent never comes from the difference of two long sums.  A
+// for what is kept of s), so that an exponent is the difference of two sums inside a block alone.  There
+// a token's log2 decay counts as -160 where it is below (its decay is 0 in fp32 either way), so that a
+// token that forgets everything leaves the decays behind it as they are: its -160 in both sums costs them
+// a few 2^-17, where a step of 1e5 would have cost them a third and an infinite sum made NaN of them.  A
 // block pair (t-block > s-block) takes its decay as the product of e^{l_t - l_end(s-block)} and
 // e^{l_end(s-block) - l_s}, both at most 1: one exponential per thread and block instead of 32.
 //
@@ -139,6 +142,8 @@ constexpr uint32_t TM_CS = 128, TM_Y = 256, TM_DS = 384, TM_S = 256;
 __device__ __forceinline__ constexpr uint32_t tm_m(int h, int k) { return 16 * k + 8 * h; }
 
 constexpr uint32_t kPolls = 1u << 20;
+
+constexpr float kLeastDecay = -160.f;  // log2: below the smallest fp32 value, 2^-149
 
 struct ChunkArgs {
   SsmArgs a;
@@ -553,17 +558,22 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
           const bool mine = hh < heads;
           const float A2 = hh ? A2s[HEADS - 1] : A2s[0];
           const float bias = hh ? biases[HEADS - 1] : biases[0];
-          float dt[4], pre[4], suf[4];
+          float dt[4], ld[4], pre[4], suf[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             dt[i] = mine && 4 * lane + i < len ? ssm_step(a, __uint_as_float(raw[i] << 16), bias) : 0.f;
-          pre[0] = dt[0] * A2;
 #pragma unroll
-          for (int i = 1; i < 4; ++i) pre[i] = pre[i - 1] + dt[i] * A2;
+          for (int i = 0; i < 4; ++i) {
+            ld[i] = dt[i] * A2;
+            ld[i] = ld[i] < kLeastDecay ? kLeastDecay : ld[i];  // (NaN stays)
+          }
+          pre[0] = ld[0];
+#pragma unroll
+          for (int i = 1; i < 4; ++i) pre[i] = pre[i - 1] + ld[i];
           suf[3] = 0.f;
 #pragma unroll
-          for (int i = 2; i >= 0; --i) suf[i] = suf[i + 1] + dt[i + 1] * A2;
-          const float four = suf[0] + dt[0] * A2;
+          for (int i = 2; i >= 0; --i) suf[i] = suf[i + 1] + ld[i + 1];
+          const float four = suf[0] + ld[0];
           float up = four, down = four;
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) {

@@ -30,8 +30,8 @@ def cu_of(lens):
 def within(got, want, size, relative=HALF_STEP):
     """|got - want| within one rounding of the result and the sums' error."""
     err = (got.double().cpu() - want).abs()
-    worst = (err - relative * want.abs() - size).max()
-    assert not torch.isnan(err).any() and float(worst) <= 0, float(worst)
+    nan, worst = bool(torch.isnan(err).any()), float((err - relative * want.abs() - size).max())
+    assert not nan and worst <= 0, worst
 
 
 def drawn(row, u):
@@ -79,4 +79,42 @@ def test_verify_certain_draft_that_outweighs_the_rest(x):
     out, count = kda.verify_draft(cuda(p), cuda(tokens), cuda(u), cu_of([2] * n))
     assert (count == 1).all() and (out[1::2] == -1).all()
     assert out[::2].tolist() == [drawn(rest, u[2 * b + 1]) for b in range(n)]
+    assert kda.device_status() == 0
+
+
+# ---- selective scan ----------------------------------------------------------------------------
+
+def scan_inputs(lens, H, P, N, seed, **other):
+    i = ref.ssm_inputs(sum(lens), H, P, 1, N, seed)
+    i.update(other)
+    return i, torch.randn(len(lens), H, N, P, generator=torch.Generator().manual_seed(seed + 1))
+
+
+@pytest.mark.parametrize("step", [1e3, 1e5, 3e38])
+@pytest.mark.parametrize("resets", [[3], [0, 31, 32, 64, 200, 255], list(range(0, 300, 4))])
+@pytest.mark.parametrize("P", [64, 128])
+def test_ssm_slow_tokens_behind_one_that_forgets_everything(step, resets, P):
+    """Steps of 0.01 behind one whose decay is 0: what came before it has no part in the decays
+    between the tokens behind it, in the prompt's form as in the token's."""
+    lens, H, N = [300, 40], 2, 64
+    i, S0 = scan_inputs(lens, H, P, N, seed=31, dt_bias=None, z=None)
+    i["dt"] = torch.full((340, H), 0.01, dtype=torch.bfloat16)
+    i["A"] = torch.tensor([-16.0, -1.0])
+    at = torch.tensor(resets)
+    i["dt"][at] = step
+    for k in "xB":  # (its own part would hide everything else)
+        i[k] = i[k].clone()
+        i[k][at] = 0
+    want, last, size, size_s = ref.ssm(lens=lens, S=S0, dt_softplus=False, **i)
+    d = {k: cuda(v) for k, v in i.items()}
+    final = torch.empty(2, H, N, P, device="cuda")
+    got = kda.ssm_fwd(cu_seqlens=cu_of(lens), S0=cuda(S0), S_final=final, dt_softplus=False, **d)
+    # the weights' rounding to bf16, and exponents from the difference of two sums of at most 14
+    # additions, of at most 8 x 160 in a block of 32 tokens: 14 half steps of 2^-14, times log 2
+    within(got, want, (HALF_STEP + 2.0 ** -10) * size)
+    within(final, last, SUM32 * size_s, relative=0.0)
+    pool = cuda(S0)
+    got = kda.ssm_tokens(state_pool=pool, cu_seqlens=cu_of(lens), dt_softplus=False, **d)
+    within(got, want, SUM32 * size)
+    within(pool, last, SUM32 * size_s, relative=0.0)
     assert kda.device_status() == 0

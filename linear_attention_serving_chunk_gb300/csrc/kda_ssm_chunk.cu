@@ -701,8 +701,9 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 const float2 f = unpack_bf16x2(in4[q]);
                 const float2 l = __fmul2_rn(f, make_float2(-1.44269504f, -1.44269504f));
                 const float2 d = __fadd2_rn(make_float2(ex2(l.x), ex2(l.y)), make_float2(1.f, 1.f));
-                const float2 v = __fmul2_rn(__fmul2_rn(make_float2(y[i], y[i + 1]), f),
-                                            make_float2(rcp(d.x), rcp(d.y)));
+                // (z times its sigmoid first: y times a gate near the type's lowest value is infinite)
+                const float2 v = __fmul2_rn(make_float2(y[i], y[i + 1]),
+                                            __fmul2_rn(f, make_float2(rcp(d.x), rcp(d.y))));
                 y[i] = v.x;
                 y[i + 1] = v.y;
               }

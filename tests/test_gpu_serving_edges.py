@@ -118,3 +118,20 @@ def test_ssm_slow_tokens_behind_one_that_forgets_everything(step, resets, P):
     within(got, want, SUM32 * size)
     within(pool, last, SUM32 * size_s, relative=0.0)
     assert kda.device_status() == 0
+
+
+@pytest.mark.parametrize("low", [torch.finfo(torch.bfloat16).min, -1e38])
+@pytest.mark.parametrize("P", [64, 128])
+def test_ssm_gate_of_the_lowest_value_closes(low, P):
+    """silu of the type's lowest value is 0, whatever it is multiplied with."""
+    lens, H, N = [150, 7], 2, 64
+    i, S0 = scan_inputs(lens, H, P, N, seed=32)
+    i["D"] = i["D"] * 100
+    i["z"] = i["z"].clone()
+    i["z"][5:140:3] = low
+    i["z"][152] = low
+    want, _, size, _ = ref.ssm(lens=lens, S=S0, **i)
+    assert (want[152] == 0).all()
+    d = {k: cuda(v) for k, v in i.items()}
+    within(kda.ssm_fwd(cu_seqlens=cu_of(lens), S0=cuda(S0), **d), want, HALF_STEP * size)
+    within(kda.ssm_tokens(state_pool=cuda(S0), cu_seqlens=cu_of(lens), **d), want, SUM32 * size)

@@ -306,6 +306,10 @@ int kda_state_snapshot(const float *snaps, int64_t n_rows, const int64_t *src_id
  *    recorded as KDA_ERR_SHAPE, as a slot outside [0, n_slots) is.
  *  - Slots must be distinct.  A token form with commit == 0 leaves the pool
  *    unchanged; with commit != 0, o may be NULL (only the state is advanced).
+ *  - Outputs overlap no input, since blocks that run side by side read the one
+ *    while they write the other; the same pointer for both is KDA_ERR_SHAPE.
+ *    What one block alone reads may be written in place: o may be z in the
+ *    scan, x in kda_ssm_tokens, and x in kda_conv_tokens with commit == 0.
  */
 
 /* Flag of the convolution: o = silu(...); 0 = no activation. */
@@ -322,8 +326,7 @@ int kda_state_snapshot(const float *snaps, int64_t n_rows, const int64_t *src_id
  *   conv0       [n_seq, W - 1, D] bf16: the inputs in front of each sequence,
  *               oldest first; NULL = zeros.
  *   conv_final  [n_seq, W - 1, D] bf16: the last W - 1 inputs of each sequence
- *               (reaching back into conv0 where it is shorter), or NULL.  Must
- *               not overlap conv0 (the same pointer is KDA_ERR_SHAPE).
+ *               (reaching back into conv0 where it is shorter), or NULL.
  * Any D and any alignment of 2 bytes; fastest where D, ldx and ldo are
  * multiples of 8 and the pointers are 16-byte aligned.
  *   Errors: KDA_ERR_NULL, _SHAPE, _ALIGN, _UNSUPPORTED, _CUDA.
@@ -355,8 +358,7 @@ int kda_conv_tokens(const kda_bf16 *x, int64_t ldx, const kda_bf16 *weight, cons
  *   x, z, o     [total, H, P] bf16 (z NULL: no gate)
  *   B, C        [total, G, N] bf16; G divides H
  *   dt          [total, H] bf16; A, D, dt_bias [H] fp32 (D, dt_bias may be NULL)
- *   S0, S_final [n_seq, H, N, P] fp32 or NULL (zeros / not wanted).  They must
- *               not overlap (the same pointer is KDA_ERR_SHAPE).
+ *   S0, S_final [n_seq, H, N, P] fp32 or NULL (zeros / not wanted).
  * N, P in {64, 128}.  A <= 0 and dt >= 0 are expected (decays in (0, 1]).  A
  * non-finite input makes the outputs of its own sequence undefined from up to
  * 127 tokens before it on; other sequences are not touched by it.

@@ -77,7 +77,8 @@ int kda_conv_fwd(const kda_bf16 *x, int64_t ldx, const kda_bf16 *weight, const k
   if (int e = check_conv(a, W)) return e;
   if (n_seq == 0) return KDA_OK;
   if (total_tokens > 0 && !o) return KDA_ERR_NULL;
-  if (conv0 && conv0 == conv_final) return KDA_ERR_SHAPE;  // read by blocks that run beside its writers
+  // read by blocks that run beside its writers
+  if ((o && o == x) || (conv0 && conv0 == conv_final)) return KDA_ERR_SHAPE;
   if (total_tokens == 0 && !conv_final) return KDA_OK;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (!(a.status = status_word(st))) return KDA_ERR_CUDA;
@@ -99,6 +100,7 @@ int kda_conv_tokens(const kda_bf16 *x, int64_t ldx, const kda_bf16 *weight, cons
   if (!aligned(slots, 4) || !aligned(used, 4)) return KDA_ERR_ALIGN;
   if (total_tokens == 0) return KDA_OK;  // no token: every slot stays as it is
   if (!conv_pool || (!o && !commit)) return KDA_ERR_NULL;
+  if (commit && o == x) return KDA_ERR_SHAPE;  // the last rows of x are read again behind the output
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (!(a.status = status_word(st))) return KDA_ERR_CUDA;
   return launched(conv_tokens_launch(a, W, st));
@@ -119,7 +121,8 @@ int kda_ssm_fwd(const kda_bf16 *x, int64_t ldx, const kda_bf16 *dt, int64_t lddt
   if (int e = check_ssm(a, P, N, flags)) return e;
   if (n_seq == 0) return KDA_OK;
   if (total_tokens > 0 && !o) return KDA_ERR_NULL;
-  if (S0 && S0 == S_final) return KDA_ERR_SHAPE;
+  // read by blocks that run beside its writers (x by the first pass over long sequences)
+  if ((S0 && S0 == S_final) || (o && (o == x || o == B || o == C || o == dt))) return KDA_ERR_SHAPE;
   if (!aligned16(workspace)) return KDA_ERR_ALIGN;
   if (total_tokens == 0 && !S_final) return KDA_OK;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -152,6 +155,7 @@ int kda_ssm_tokens(const kda_bf16 *x, int64_t ldx, const kda_bf16 *dt, int64_t l
   if (!aligned(slots, 4) || !aligned(used, 4)) return KDA_ERR_ALIGN;
   if (total_tokens == 0) return KDA_OK;  // no token: every state stays as it is
   if (!state_pool || (!o && !commit)) return KDA_ERR_NULL;
+  if (o && (o == B || o == C || o == dt)) return KDA_ERR_SHAPE;  // read by the blocks of other heads
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (!(a.status = status_word(st))) return KDA_ERR_CUDA;
   return launched(ssm_tokens_launch(a, P, N, fixed_len == 1, st));
@@ -170,6 +174,7 @@ int kda_verify_draft(const void *target, const void *draft, int prob_bytes, int 
   for (const void *p : words)
     if (!aligned(p, 4)) return KDA_ERR_ALIGN;
   if (!aligned(target, prob_bytes) || !aligned(draft, prob_bytes)) return KDA_ERR_ALIGN;
+  if (out_tokens == tokens) return KDA_ERR_SHAPE;  // read by the other blocks of the run's cluster
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   VerifyArgs a{target, draft, tokens, u, cu_seqlens, n, V, total_tokens, out_tokens, n_out,
                status_word(st)};

@@ -200,6 +200,8 @@ def ssm_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, cu_s
     else:
         if not workspace.is_cuda or workspace.get_device() != dev:
             _refuse(workspace, "workspace", dev)
+        if not workspace.is_contiguous():  # (its elements say how large it is)
+            raise ValueError("workspace must be contiguous")
         size = workspace.numel() * workspace.element_size()
     st = L.kda_ssm_fwd(*args, cu, n_seq, total, H, P, G, N, _dense(S0, "S0", _F32, states, dev),
                        op, ldo, _dense(S_final, "S_final", _F32, states, dev),

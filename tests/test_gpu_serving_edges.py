@@ -135,3 +135,14 @@ def test_ssm_gate_of_the_lowest_value_closes(low, P):
     d = {k: cuda(v) for k, v in i.items()}
     within(kda.ssm_fwd(cu_seqlens=cu_of(lens), S0=cuda(S0), **d), want, HALF_STEP * size)
     within(kda.ssm_tokens(state_pool=cuda(S0), cu_seqlens=cu_of(lens), **d), want, SUM32 * size)
+
+
+def test_ssm_workspace_that_is_smaller_than_its_elements_is_refused():
+    """One byte seen as many is no room for the segments."""
+    d = {k: cuda(v) for k, v in ref.ssm_inputs(4096, 2, 64, 1, 64, 1).items()}
+    need = kda.ssm_workspace_bytes(1, 4096, 2, 64, 1, 64)
+    assert need > 0
+    with pytest.raises(ValueError):
+        kda.ssm_fwd(workspace=torch.empty(1, dtype=torch.uint8, device="cuda").expand(need), **d)
+    with pytest.raises(ValueError):
+        kda.ssm_fwd(workspace=torch.empty(need, dtype=torch.uint8), **d)

@@ -151,8 +151,7 @@ struct ChunkArgs {
   int blocks;        // column blocks: of a group, times G
   float *part;       // [segments, H, N, P]: what the first pass leaves
   float *part_decay; // [segments, H]
-  int uncut;         // one segment for each sequence
-  int parts;         // segments that `part` has room for
+  int parts;         // segments that `part` has room for (0: no sequence is cut)
 };
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y,
@@ -217,11 +216,14 @@ struct Segment {
   int last, bad;
 };
 
-// Segment `id` of the batch.  The segments in front of a sequence's last one are all seg_len long and
-// come first, sequence after sequence; then come the last ones, one for each sequence.  So the full
-// ones start first, and the shorter ones fill the end.  Called by a whole warp, which looks at 128
-// sequences at a time; false beyond the last.
-__device__ __forceinline__ bool find_segment(const Runs &r, int64_t seg_len, int id, bool uncut,
+// Segment `id` of the batch.  The segments in front of a sequence's last one are all seg_len long; ids
+// [0, parts) are theirs, sequence after sequence (as many as the tokens have room for: the spare ones are
+// none), and the last ones, one for each sequence, come behind.  So the full ones start first, and the
+// shorter ones fill the end.  Called by a whole warp.  A segment in front is found by a walk over the
+// sequences, 128 at a time; a last one is its sequence's number, and only one that has others in front sums
+// up where they are.  (With the last ones behind the used ids alone every one of them took the walk:
+// 32768 prompts of one token x 8 heads 191 ms, where this takes 8.3.)
+__device__ __forceinline__ bool find_segment(const Runs &r, int64_t seg_len, int parts, int id,
                                              Segment &g) {
   const int lane = threadIdx.x & 31;
   auto front = [&](int s) -> int {  // segments in front of the last one
@@ -230,56 +232,57 @@ __device__ __forceinline__ bool find_segment(const Runs &r, int64_t seg_len, int
     run_range(r, s, b, n, u);
     return n <= seg_len ? 0 : static_cast<int>((n - 1) / seg_len);
   };
-  int before = 0;
-  g.seq = -1;
-  for (int base = 0; base < r.n && !uncut; base += 128) {
-    int c[4], mine = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) mine += c[k] = front(base + 4 * lane + k);
-    int x = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    const unsigned m = __ballot_sync(0xffffffffu, before + x > id);
-    if (m) {
-      const int l = __ffs(m) - 1;
-      int s = base + 4 * lane, first = before + x - mine;
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-        if (s == base + 4 * lane + k && first + c[k] <= id) {
-          first += c[k];
-          ++s;
-        }
-      g.seq = __shfl_sync(0xffffffffu, s, l);
-      g.id0 = __shfl_sync(0xffffffffu, first, l);
-      g.index = id - g.id0;
-      break;
-    }
-    before += __shfl_sync(0xffffffffu, x, 31);
-  }
-  const bool full = g.seq >= 0;
-  if (!full) {
-    g.seq = id - before;
-    if (g.seq >= r.n) return false;
-  }
-  int64_t b, n, u;
-  g.bad = !run_range(r, g.seq, b, n, u);
-  if (!full) {
+  g.last = id >= parts;
+  g.id0 = 0;
+  if (g.last) {
+    g.seq = id - parts;
     g.index = front(g.seq);
-    g.id0 = 0;
     if (g.index > 0) {  // where its others are: the sum over the sequences in front of it
       int sum = 0;
-      for (int s = lane; s < g.seq; s += 32) sum += front(s);
+      for (int s = lane; s < g.seq; s += 32) {
+        sum += front(s);
+        sum = sum < parts ? sum : parts;  // (offsets that are not in order: no number to wrap around)
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       g.id0 = sum;
     }
+  } else {
+    int before = 0;
+    g.seq = -1;
+    for (int base = 0; base < r.n; base += 128) {
+      int c[4], mine = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mine += c[k] = front(base + 4 * lane + k);
+      int x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, before + x > id);
+      if (m) {
+        const int l = __ffs(m) - 1;
+        int s = base + 4 * lane, first = before + x - mine;
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          if (s == base + 4 * lane + k && first + c[k] <= id) {
+            first += c[k];
+            ++s;
+          }
+        g.seq = __shfl_sync(0xffffffffu, s, l);
+        g.id0 = __shfl_sync(0xffffffffu, first, l);
+        g.index = id - g.id0;
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (g.seq < 0) return false;
   }
-  g.last = !full;
+  int64_t b, n, u;
+  g.bad = !run_range(r, g.seq, b, n, u);
   g.begin = static_cast<int>(b + g.index * seg_len);
-  g.len = static_cast<int>(full ? seg_len : n - g.index * seg_len);
+  g.len = static_cast<int>(g.last ? n - g.index * seg_len : seg_len);
   return true;
 }
 
@@ -309,13 +312,13 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
   Segment &seg = *reinterpret_cast<Segment *>(smem + SM_MISC + 16);
   if (warp == 0) {
     Segment found;
-    if (!find_segment(a.runs, p.seg_len, id, p.uncut, found)) {
+    if (!find_segment(a.runs, p.seg_len, p.parts, id, found)) {
       found.len = -1;
     } else {
       // offsets that are not in order can make more segments than the tokens have room for
-      if (found.id0 + found.index > p.parts || (!found.last && id >= p.parts)) found.bad = 1;
+      if (found.last && found.id0 + found.index > p.parts) found.bad = 1;
       if (found.bad && block == 0 && lane == 0) atomicOr(a.status, KDA_ERR_SHAPE);
-      if (found.bad || (STATE_ONLY && found.last)) found.len = -1;
+      if (found.bad) found.len = -1;
     }
     if (lane == 0) seg = found;
   }
@@ -1080,7 +1083,6 @@ cudaError_t run(ChunkArgs p, int64_t seg_len, cudaStream_t st) {
        !row_map(&maps[1], a.B, static_cast<int64_t>(a.G) * N, a.runs.total, a.ldb) ||
        !row_map(&maps[2], a.C, static_cast<int64_t>(a.G) * N, a.runs.total, a.ldc)))
     return cudaErrorInvalidValue;
-  p.uncut = seg_len == 0;
   p.seg_len = seg_len ? seg_len : (a.runs.total / kQ + 1) * kQ;
   p.parts = static_cast<int>(front_most(a.runs.total, seg_len));
   const size_t front = static_cast<size_t>(p.parts) * p.blocks;

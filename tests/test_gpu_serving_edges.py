@@ -146,3 +146,27 @@ def test_ssm_workspace_that_is_smaller_than_its_elements_is_refused():
         kda.ssm_fwd(workspace=torch.empty(1, dtype=torch.uint8, device="cuda").expand(need), **d)
     with pytest.raises(ValueError):
         kda.ssm_fwd(workspace=torch.empty(need, dtype=torch.uint8), **d)
+
+
+def test_ssm_many_prompts_of_one_token_cost_no_more_where_they_may_be_cut():
+    """The work of each prompt does not grow with the number of prompts beside it."""
+    n, H, P, N = 16384, 4, 64, 64
+    d = {k: cuda(v) for k, v in ref.ssm_inputs(n, H, P, 1, N, 1).items()}
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    size = kda.ssm_workspace_bytes(n, n, H, P, 1, N)
+    assert size > 0
+    took, got = [], []
+    for room in (size, 16):
+        ws = torch.empty(room, dtype=torch.uint8, device="cuda")
+        times = []
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            o = kda.ssm_fwd(cu_seqlens=cu, workspace=ws, **d)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        took.append(min(times))
+        got.append(o)
+    assert torch.equal(*got)
+    assert took[0] < 2 * took[1], took

@@ -870,7 +870,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
   } else {
     // the state's warps; in the first pass the token's beside them, every other round each
     set_registers<kStateRegs, true, !STATE_ONLY>();
-    // X' of the tokens of round r of chunk c: a thread takes 8 columns of a row, of one region or both
+    // X' of the tokens of round r of chunk c: a thread takes 8 columns of a row in both regions
     auto put_weighted = [&](int c, int r) -> bool {
       const int i = XP::ROUNDS * c + r;
       if constexpr (STATE_ONLY) {
@@ -883,8 +883,7 @@ ssm_chunk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
       const uint32_t flip = static_cast<uint32_t>(j ^ (row & 7)) << 4;
       const uint32_t dec = decays(c, 0) + DC_W + 4 * tok;
 #pragma unroll
-      for (int u = 0; u < XP::TOKENS / 16; ++u) {
-        const int region = XP::TOKENS == 16 ? (tid >> 7) & 1 : u;
+      for (int region = 0; region < 2; ++region) {
         const float w = S.f32(dec + (HEADS == 2 ? region : 0) * DEC_BYTES);
         const uint4 raw = S.u128(tile_x(c) + region * REG128 + tok * 128u + flip);
         const uint32_t in4[4] = {raw.x, raw.y, raw.z, raw.w};

@@ -58,8 +58,7 @@ ssm_tokens_kernel(const SsmArgs a) {
   float2 s[RPT][2];
 #pragma unroll
   for (int r = 0; r < RPT; ++r) {
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (a.S_in) v = __ldcs(reinterpret_cast<const float4 *>(a.S_in + at + r * P));
+    const float4 v = __ldcs(reinterpret_cast<const float4 *>(a.S_in + at + r * P));
     s[r][0] = make_float2(v.x, v.y);
     s[r][1] = make_float2(v.z, v.w);
   }
@@ -137,7 +136,7 @@ ssm_tokens_kernel(const SsmArgs a) {
   if (a.o)
     for (int64_t i = used * P + tid; i < len * P; i += kThreads)
       a.o[(begin + i / P) * a.ldo + h * P + i % P] = 0;
-  if (a.S_out && (used > 0 || a.S_in != a.S_out))
+  if (a.S_out && used > 0)
 #pragma unroll
     for (int r = 0; r < RPT; ++r)
       __stcs(reinterpret_cast<float4 *>(a.S_out + at + r * P),

@@ -418,7 +418,7 @@ int kda_ssm_tokens(const kda_bf16 *x, int64_t ldx, const kda_bf16 *dt, int64_t l
  * the accepted ones is the smallest i with w_0 + ... + w_i > u sum(w), where w
  * is max(p - q, 0) of the first refused row (p where that is zero everywhere;
  * without `draft`, p with the refused token taken out) or, with none refused,
- * the run's last row of the target.  The sums carry at least 48 bits.  NaN and
+ * the run's last row of the target.  The sums carry at least 43 bits.  NaN and
  * negative weights count as zero.
  *   out_tokens  int32 [total]: the accepted tokens, the drawn one, then -1.
  *   n_out       int32 [n]: how many there are, accepted + 1.  It is also how

@@ -6,15 +6,16 @@
 // row, by the inverse distribution: the smallest i with w_0 + ... + w_i > u (sum of w).
 //
 // Bound by memory: one row of p (and of q) per run is read.  A cluster of CTAs shares a run's row.
-// Which token a sum lands on must not depend on the order of the additions, so sums carry 48 bits:
-// a lane adds its elements in pairs of fp32 (the value and what its rounding lost; double-precision
+// Which token a sum lands on must hardly depend on the order of the additions, so sums carry 43 bits
+// at least: a lane adds its elements in fp32 together with what the roundings lost (double-precision
 // adds run at 2 per SM and cycle here, below the rate at which elements arrive), everything above a
 // lane is in double precision.  The row is cut into segments of kSeg elements whose sums stay in
 // shared memory; the segment that the target falls into is read a second time, from L2, 32
 // neighbouring elements a lane, and then the 32 of the lane that it falls into, one a lane.
 //
-// 256 runs over 131072 words in fp32: 42.5 us; the rows that this batch needs are 240 MB, 5.6 TB/s.  A
-// few runs over 32000 words take 11 us on the device, a chain of dependent reads (offsets, drafted tokens,
+// 256 runs over 131072 words in fp32: 43.0 us for the 190 MB of the rows that this batch needs, 4.4 TB/s
+// (with what the roundings lost in one fp32 sum, right to 38 bits in the worst case, 42.5; with that sum
+// kept exact element by element, 47 bits, 52).  A few runs over 32000 words take 11 us on the device, a chain of dependent reads (offsets, drafted tokens,
 // their probabilities, the row, its two searches).  CTAs of 256 threads, two of them for a row at
 // this size: four took 47 us, one of 512 threads 44; four vectors in flight a lane: two took 46, eight 51.
 #include "kda_serving.cuh"
@@ -55,6 +56,20 @@ __device__ __forceinline__ double peer_load(const double *p, unsigned rank) {
 __device__ __forceinline__ float prob(const float *p, int64_t i) { return p[i]; }
 __device__ __forceinline__ float prob(const kda_bf16 *p, int64_t i) { return bf2f(p[i]); }
 
+__device__ __forceinline__ float minus(float a, float b) { return a - b; }
+__device__ __forceinline__ float2 minus(float2 a, float2 b) {
+  return __ffma2_rn(b, make_float2(-1.f, -1.f), a);
+}
+__device__ __forceinline__ float plus(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 plus(float2 a, float2 b) { return __fadd2_rn(a, b); }
+// a + b rounded, and what the rounding lost
+template <typename V>
+__device__ __forceinline__ V exact(V a, V b, V &lost) {
+  const V s = plus(a, b), r = minus(s, a);
+  lost = plus(minus(a, minus(s, r)), minus(b, r));
+  return s;
+}
+
 // The row's weights: max(p - q, 0), p without one token, or p.  NaN counts as 0.
 template <typename T>
 struct Weights {
@@ -66,6 +81,12 @@ struct Weights {
     hi = fmaxf(pv - qv, 0.f);
     lo = hi > 0.f ? (pv - hi) - qv : 0.f;
   }
+  static __device__ __forceinline__ void weight(float2 pv, float2 qv, float2 &hi, float2 &lo) {
+    hi = minus(pv, qv);
+    hi = make_float2(fmaxf(hi.x, 0.f), fmaxf(hi.y, 0.f));
+    lo = minus(minus(pv, hi), qv);
+    lo = make_float2(hi.x > 0.f ? lo.x : 0.f, hi.y > 0.f ? lo.y : 0.f);
+  }
   __device__ __forceinline__ double one(int i) const {
     float hi, lo;
     weight(prob(p, i), q ? prob(q, i) : 0.f, hi, lo);
@@ -73,15 +94,30 @@ struct Weights {
   }
 };
 
-struct Sum {  // hi + lo
-  float hi = 0.f, lo = 0.f;
-  __device__ __forceinline__ void add(float x, float xl) {
-    const float s = hi + x, r = s - hi;
-    lo += (hi - (s - r)) + (x - r) + xl;
-    hi = s;
+// Two sums side by side, hi + lo + tail each: the sum, what its roundings lost, and what the roundings of
+// that lost.  With u = 2^-24: four elements of sum g lose 2 u g at most among themselves and u g in their
+// differences; adding these seven terms plainly is off by 18 u^2 g, so a lane's sum is right to 18 u^2 = 2^-43.8.
+struct Sum {
+  float2 hi = {0.f, 0.f}, lo = {0.f, 0.f}, tail = {0.f, 0.f};
+
+  // Four elements each, x with xl lost before: first among themselves, so that what their roundings lose is
+  // small against the group and may be added as it is.
+  __device__ __forceinline__ void add(const float2 (&x)[4], const float2 (&xl)[4]) {
+    float2 a, b, c, d, again;
+    const float2 four = exact(exact(x[0], x[1], a), exact(x[2], x[3], b), c);
+    hi = exact(hi, four, d);
+    a = plus(plus(plus(a, b), c), plus(plus(xl[0], xl[1]), plus(xl[2], xl[3])));
+    lo = exact(lo, d, again);
+    tail = plus(tail, again);
+    lo = exact(lo, a, again);
+    tail = plus(tail, again);
   }
+  // both sums
   __device__ __forceinline__ double value() const {
-    return static_cast<double>(hi) + static_cast<double>(lo);
+    float a, b, c, d;
+    const float top = exact(hi.x, hi.y, a), low = exact(exact(lo.x, lo.y, b), a, c);
+    const float sum = exact(top, low, d);
+    return static_cast<double>(sum) + static_cast<double>(d + ((tail.x + tail.y) + (b + c)));
   }
 };
 
@@ -133,21 +169,35 @@ __device__ __forceinline__ double segment_sum(const Weights<T> &w, int i0, int V
         }
       }
 #pragma unroll
-      for (int k = 0; k < AHEAD; ++k)
+      for (int g = 0; g < AHEAD * E; g += 8) {
+        float2 hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          float hi, lo;
-          Weights<T>::weight(prob(reinterpret_cast<const T *>(&pv[k]), e),
-                             prob(reinterpret_cast<const T *>(&qv[k]), e), hi, lo);
-          s.add(hi, lo);
+        for (int e = 0; e < 4; ++e) {
+          const T *pe = reinterpret_cast<const T *>(pv) + g + 2 * e, *qe = reinterpret_cast<const T *>(qv) + g + 2 * e;
+          Weights<T>::weight(make_float2(prob(pe, 0), prob(pe, 1)), make_float2(prob(qe, 0), prob(qe, 1)),
+                             hi[e], lo[e]);
         }
+        s.add(hi, lo);
+      }
     }
   } else {
-#pragma unroll 8
-    for (int k = 0; k < kSeg / 32; ++k) {
-      const int i = i0 + (SPREAD ? k * 32 + lane : lane * 32 + k);
-      float hi = 0.f, lo = 0.f;
-      if (i < V) Weights<T>::weight(prob(w.p, i), w.q ? prob(w.q, i) : 0.f, hi, lo);
+#pragma unroll 1
+    for (int k = 0; k < kSeg / 32; k += 8) {
+      float pv[8], qv[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = i0 + (SPREAD ? (k + e) * 32 + lane : lane * 32 + k + e);
+        pv[e] = qv[e] = 0.f;
+        if (i < V) {
+          pv[e] = prob(w.p, i);
+          if (w.q) qv[e] = prob(w.q, i);
+        }
+      }
+      float2 hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        Weights<T>::weight(make_float2(pv[2 * e], pv[2 * e + 1]), make_float2(qv[2 * e], qv[2 * e + 1]),
+                           hi[e], lo[e]);
       s.add(hi, lo);
     }
   }

@@ -82,6 +82,41 @@ def test_verify_certain_draft_that_outweighs_the_rest(x):
     assert kda.device_status() == 0
 
 
+@pytest.mark.parametrize("V", [4096, 4099])
+@pytest.mark.parametrize("with_draft", [False, True])
+def test_verify_sums_of_large_and_small_weights(V, with_draft):
+    """The sums' 43 bits: every lane of the first segment adds 31 weights of 0.94 2^-24 to one of 1,
+    and tokens of 2^-38 are drawn from behind it.  In pairs of fp32 alone the sum of what the
+    roundings lost is rounded itself, which is 2^-40 of each lane's sum and 3 such tokens."""
+    small, fine = float(torch.tensor(0.94275 * 2 ** -24)), 2.0 ** -38
+    p = torch.zeros(V, dtype=torch.float64)
+    p[:1024] = small
+    # the first element of each lane, vectors of four or single ones
+    p[:128:4] = 1.0
+    if V % 4:
+        p[:128:4], p[:32] = small, 1.0
+    front = 32 * (1 + 31 * small)                   # (48 bits: exact in 64)
+    p[1024:2048] = fine
+    left = front + fine
+    for i in range(3):                              # the same again, in three weights, and half a token
+        part = torch.tensor(left)
+        part = part if float(part) <= left else torch.nextafter(part, torch.tensor(0.0))
+        p[2048 + 40 * i] = float(part)
+        left -= float(part)
+    assert left == 0 and (p == p.float().double()).all()
+    p = p.float()
+    tokens = torch.full((2,), V - 50, dtype=torch.int32)
+    if with_draft:  # the drafted token has no weight in p; 2^-60 less for all others
+        q = torch.full((1, V), 2.0 ** -60)
+        out, n = kda.verify_draft(cuda(p.repeat(2, 1)), cuda(tokens), torch.full((2,), 0.5).cuda(), cu_of([2]),
+                                  draft=cuda(q))
+    else:
+        out, n = kda.verify_draft(cuda(p[None]), cuda(tokens[:1]), torch.full((1,), 0.5).cuda(), cu_of([1]))
+    # half of all is the front and 512.5 of the 1024 tokens behind it
+    assert n.tolist() == [1] and int(out[0]) == 1024 + 512
+    assert kda.device_status() == 0
+
+
 # ---- selective scan ----------------------------------------------------------------------------
 
 def scan_inputs(lens, H, P, N, seed, **other):

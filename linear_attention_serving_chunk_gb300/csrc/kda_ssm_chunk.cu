@@ -1012,9 +1012,14 @@ int column_blocks(int H, int P, int G) { return P == 128 ? H : G * ((H / G + 1) 
 // pass is 0.5 of one (2.5 us against 5), starting a CTA one.  Where whole sequences do best but the
 // lengths may differ, long ones are still cut: one long prompt among short ones would keep its own few
 // SMs busy long after the others are done.  Cut at an SM's share of all chunks, the segments in front
-// are one wave at most; at half of it two, which leaves shorter pieces for the end.  (6 prompts of 1 to
-// 12001 tokens x 64 heads of 64, a share of 54 chunks: cut at 54 482 us, at 27 442, at 18 458; 16000 and
-// nine times 500 tokens, a share of 34: at 34 265 us, at 24 356, at 17 297.)
+// are one wave at most; at half of it two, which leaves shorter pieces for the end but more for the first
+// pass.  Half is taken where the share is long (48 chunks) and the whole sequences are two waves of CTAs at
+// most, so that there is little else to fill the SMs with.  Measured on 48 ragged batches (3 to 32 prompts of
+// 16 to 100,000 tokens, 16 to 128 heads), half against whole shares, us: up to two waves 452 / 491 (6 prompts
+// of 1 to 12001 tokens x 64 heads of 64, a share of 54), 637 / 683 (x 96 heads, 81), 1001 / 1148 (6 of 143557
+// tokens in all, 118), the others even; beyond that from 881 / 696 (the first one's prompts x 128 heads, 108)
+// and 476 / 439 (30000 and nine times 500, 57) to 575 / 737, as often worse as better; under 48 chunks
+// 281 / 251 (x 32 heads, 27), 369 / 340 (x 48 heads, 41), 316 / 284 (16000 and nine times 500, 34).
 int64_t segment_tokens(int n_seq, int64_t total, int blocks, bool ragged) {
   const int64_t chunks = (total / n_seq + kQ) / kQ;
   auto waves = [&](int64_t tasks) { return (tasks + kSMs - 1) / kSMs; };
@@ -1032,7 +1037,8 @@ int64_t segment_tokens(int n_seq, int64_t total, int blocks, bool ragged) {
   }
   if (best == 0 && ragged && n_seq > 1) {
     const int64_t share = waves(total / kQ * blocks);
-    const int64_t cut = share >= 48 ? share / 2 : share > 12 ? share : 12;
+    const bool half = share >= 48 && waves(static_cast<int64_t>(n_seq) * blocks) <= 2;
+    const int64_t cut = half ? share / 2 : share > 12 ? share : 12;
     if (total >= 2 * cut * kQ) best = cut * kQ;
   }
   return best;

@@ -205,3 +205,31 @@ def test_ssm_many_prompts_of_one_token_cost_no_more_where_they_may_be_cut():
         got.append(o)
     assert torch.equal(*got)
     assert took[0] < 2 * took[1], took
+
+
+def test_ssm_cut_sequences_in_a_graph():
+    """Both passes, the second launched beside the first's end, captured once and replayed on new inputs."""
+    lens, H, P, N = [3000, 0, 40, 1500], 4, 64, 128
+    size = kda.ssm_workspace_bytes(len(lens), sum(lens), H, P, 1, N)
+    assert size > 0
+    cu, ws = cu_of(lens), torch.empty(size, dtype=torch.uint8, device="cuda")
+    cases = [scan_inputs(lens, H, P, N, seed) for seed in (41, 42, 43)]
+    want = []
+    for i, S0 in cases:
+        final = torch.empty(len(lens), H, N, P, device="cuda")
+        o = kda.ssm_fwd(cu_seqlens=cu, S0=cuda(S0), S_final=final, workspace=ws, **{k: cuda(v) for k, v in i.items()})
+        want.append((o, final))
+    d = {k: cuda(v) for k, v in cases[0][0].items()}
+    S0, final = cuda(cases[0][1]), torch.empty_like(want[0][1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = kda.ssm_fwd(cu_seqlens=cu, S0=S0, S_final=final, workspace=ws, **d)
+    for (i, S), (want_o, want_s) in zip(cases, want):
+        for k, v in i.items():
+            d[k].copy_(v)
+        S0.copy_(S)
+        for _ in range(3):  # one replay behind another
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want_o) and torch.equal(final, want_s)
+    assert kda.device_status() == 0

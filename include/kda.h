@@ -369,6 +369,10 @@ int kda_conv_tokens(const kda_bf16 *x, int64_t ldx, const kda_bf16 *weight, cons
  *               bytes than kda_ssm_fwd_workspace_bytes() (or NULL) no sequence
  *               is cut into segments that run side by side: the same results
  *               up to rounding, slower for few long sequences.
+ * Precision: states carry fp32 accuracy.  For o the weights between the tokens
+ * of a chunk of 128 are rounded to bf16 once before they meet x, which makes
+ * its error 1.1 times that of its own rounding to bf16 (in the 2-norm;
+ * kda_ssm_tokens has no such rounding).
  * With softplus, a step of -inf (or far below 0) is 0: that token leaves the
  * state as it is.  Bounded in-kernel waits that give up are recorded as
  * KDA_ERR_TIMEOUT in the device status word.

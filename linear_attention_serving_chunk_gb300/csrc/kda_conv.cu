@@ -17,8 +17,9 @@ namespace kda {
 
 namespace {
 
-// One warp to a CTA: 20 CTAs of 32 threads and 102 registers took 98 us for 32768 x 4352 tokens x
-// channels, 5 of 128 threads 105 us: the tiles of a long prompt end more evenly.
+// One warp to a CTA: 20 CTAs of 32 threads took 98 us for 32768 x 4352 tokens x channels, 5 of 128 threads
+// 105 us: the tiles of a long prompt end more evenly.  They leave 96 registers a thread, for which the form of
+// vectors and 4 taps keeps 48 bytes on the stack (60 bytes of spill stores; 3 taps 16, 2 taps 32).
 constexpr int kConvThreads = 32;
 
 template <int VEC>

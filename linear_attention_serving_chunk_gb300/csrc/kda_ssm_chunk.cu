@@ -17,7 +17,9 @@
 // all 24 bits of its fp32 value, and the state itself stays in fp32 registers (S^T: a thread has one
 // column and half of n), so S and S_final carry fp32 accuracy.  For the output, S enters as two
 // planes (16 bits) and M as one (8 bits): the in-chunk weights are rounded once to the type of the
-// result, which adds an error of the size of the result's own rounding.
+// result, which makes its error 1.1 times that of its own rounding (1.85e-3 against 1.66e-3 in the 2-norm).
+// M in two planes leaves 1.66e-3, but its second plane has no columns of TMEM to itself: in those of C S, M
+// can only be made once C S is there, which took 529 us where this takes 444 and 757 where this takes 720.
 //
 // Log decays are summed in blocks of 32 tokens from both ends (prefix for what is read at t, suffix
 // for what is kept of s), so that an exponent is the difference of two sums inside a block alone.  There
@@ -45,8 +47,8 @@
 // pass through the chunk's X tile once nothing reads it any more.  In the first pass the token warps
 // build X' too, and the output warps keep the state.
 //
-// What bounds it (32768 packed tokens x 64 heads of 64, N = 128, gate: 443 us, of which the first pass
-// 108; 131072 tokens x 16 heads of 128: 721 us, of which 196).  A chunk of 128 tokens x 128 columns takes
+// What bounds it (32768 packed tokens x 64 heads of 64, N = 128, gate: 444 us, of which the first pass
+// 108; 131072 tokens x 16 heads of 128: 720 us, of which 196).  A chunk of 128 tokens x 128 columns takes
 // 11,000 cycles in the second pass (9,000 without the gate) and 5,000 in the first.  Its products would
 // take 3,600 at the tensor cores' rate, its tiles 1,200 at the memory's.  The element-wise work decides,
 // each warp waiting for its own results (shared memory, TMEM, exponentials) most of the time: by the

@@ -441,6 +441,105 @@ int kda_verify_draft(const void *target, const void *draft, int prob_bytes, int 
                      kda_stream_t stream);
 
 /*
+ * The paged cache: what the full attention layers of a hybrid model keep of
+ * their sequences, beside the recurrent layers' states, on the same kind of
+ * batch.  These operators are additions of this library; the pages have no
+ * counterpart.
+ *
+ *   cache   bf16 [n_pages, 2, H, page, D] of one layer: for each page the keys
+ *           and then the values of H heads, `page` tokens each.  The operators
+ *           on pages take all layers of a model at once, [layers, n_pages, 2,
+ *           H, page, D]; a layer's part of it is the cache of that layer.
+ *   table   device int32 [n_slots, max_pages]: the pages of each slot's
+ *           sequence in order.  Token i of slot s is row i % page of page
+ *           table[s][i / page].
+ *   lens    device int32 [n_slots]: the tokens of each slot's sequence, 0 for a
+ *           slot without one.  A page is in use where a row of the table reaches
+ *           it within its length: nothing else records it, a sequence is freed
+ *           by setting its length to 0, and what a row holds behind its length
+ *           is not looked at.
+ * page in {16, 32, 64, 128}, D in {64, 128}; n_pages and max_pages at most 2^20,
+ * n_slots at most 2^14 where pages are given out, shared or moved.
+ *
+ * Run b of a batch belongs to slot slots[b] (NULL: slot b), and its tokens
+ * follow the lens[slot] tokens of that slot: token j stands at position
+ * lens[slot] + j.  Neither call changes lens: the caller adds what stands (all
+ * of a prompt, kda_verify_draft's n_out of a drafted run).  A step is
+ *   kda_pages_grow, kda_kv_append and kda_attn_paged in each layer, lens += ...
+ * Device-side entries are checked before use; a slot outside [0, n_slots), a
+ * length that is negative or that its row cannot hold, and a page outside
+ * [0, n_pages) that is needed are recorded as KDA_ERR_SHAPE.
+ */
+
+/*
+ * kda_kv_append - write the keys and values of a batch of runs into the pages
+ * of their sequences.
+ *   k, v   [total, H, D] bf16, rows ldk / ldv elements apart, 16-byte aligned
+ *          (ldk, ldv multiples of 8).  They do not lie in the cache.
+ * The pages are there before (kda_pages_grow).  A token without a valid page
+ * is not written and recorded.  Slots are distinct.  Tokens of k and v
+ * outside all runs are not read.
+ *   Errors: KDA_ERR_NULL, _SHAPE, _ALIGN, _UNSUPPORTED, _CUDA.
+ */
+int kda_kv_append(const kda_bf16 *k, int64_t ldk, const kda_bf16 *v, int64_t ldv,
+                  const int32_t *cu_seqlens, int n, int64_t total_tokens, int H, int D,
+                  kda_bf16 *cache, int n_pages, int page, const int32_t *table, int max_pages,
+                  const int32_t *lens, int n_slots, const int32_t *slots, kda_stream_t stream);
+
+/*
+ * kda_pages_grow - give rows of the table the pages that sequences of want[s]
+ * instead of lens[s] tokens need (int32 [n_slots]; no more than lens[s]: none).
+ * The unused pages are given out in ascending order, to the rows in ascending
+ * order.  A row gets all of its pages or none: from the first row on for which
+ * too few are left, rows get -1 in their place.
+ *   left   int32 [1]: the pages that are still unused, or less than 0: how many
+ *          are missing for all rows.
+ * What rows hold behind lens counts as unused: rows that grew in an earlier call
+ * and whose lens does not say so yet are grown again by the same call.
+ *   Errors: KDA_ERR_NULL, _SHAPE, _ALIGN, _UNSUPPORTED, _CUDA.
+ */
+int kda_pages_grow(int32_t *table, int max_pages, const int32_t *lens, const int32_t *want,
+                   int n_slots, int n_pages, int page, int32_t *left, kda_stream_t stream);
+
+/*
+ * kda_pages_fork - let slot dst[i] continue what slot src[i] holds, for i in
+ * [0, n) (device int32): its row of the table becomes src[i]'s, its length
+ * too, and a last page that is not full is copied, in every layer, to the
+ * lowest unused page (in the order of i), so that both may append.  Full pages
+ * are shared.  What dst[i] held before is given up first, and its pages are
+ * among the unused ones.  Entries of the row behind its pages become -1.
+ * A fork is left out and recorded as KDA_ERR_SHAPE where an index is outside
+ * [0, n_slots), where an earlier one has the same dst, or where src[i] is the
+ * dst of any.  One that finds no page left leaves dst[i] with no tokens.
+ *   left        int32 [1], as for kda_pages_grow.
+ *   workspace   device scratch of kda_pages_workspace_bytes(n) bytes, 16-byte
+ *               aligned, not to be shared by calls that overlap on the GPU.
+ *   Errors: KDA_ERR_NULL, _SHAPE, _ALIGN, _UNSUPPORTED, _WORKSPACE, _CUDA.
+ */
+int kda_pages_fork(kda_bf16 *cache, int layers, int n_pages, int H, int page, int D,
+                   int32_t *table, int max_pages, int32_t *lens, int n_slots, const int32_t *src,
+                   const int32_t *dst, int n, int32_t *left, void *workspace,
+                   size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * kda_pages_compact - move the pages in use to the front of the pool.  With u
+ * pages in use, those from u on move, in ascending order, to the unused ones
+ * below u, in ascending order; the others stay.
+ *   table_out   int32 [n_slots, max_pages]: the table with the moved pages'
+ *               numbers, -1 behind each row's length.  May be `table`.
+ *   used        int32 [1]: u.
+ *   workspace   as for kda_pages_fork, of kda_pages_workspace_bytes(n_pages).
+ *   Errors: KDA_ERR_NULL, _SHAPE, _ALIGN, _UNSUPPORTED, _WORKSPACE, _CUDA.
+ */
+int kda_pages_compact(kda_bf16 *cache, int layers, int n_pages, int H, int page, int D,
+                      const int32_t *table, int max_pages, const int32_t *lens, int n_slots,
+                      int32_t *table_out, int32_t *used, void *workspace, size_t workspace_bytes,
+                      kda_stream_t stream);
+
+/* Workspace bytes of kda_pages_fork (n forks) and kda_pages_compact (n pages). */
+size_t kda_pages_workspace_bytes(int n);
+
+/*
  * kda_device_status - read (and with reset != 0, clear) the library's
  * device-side status word on the current device.  Kernels record there what
  * only the GPU can see: KDA_ERR_TIMEOUT (a bounded wait gave up instead of

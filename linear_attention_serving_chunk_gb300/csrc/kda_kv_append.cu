@@ -1,0 +1,98 @@
+// Writes the keys and values of a batch of runs into the pages of their sequences.
+//
+// Bound by memory: each row of k and v is read once and written once.  A block takes kVectors 16-byte
+// vectors a thread of consecutive tokens; the run, slot and page of each of its tokens are looked up
+// once, by one thread each, and the vectors are all in flight before the first is stored.
+#include "kda_paged.cuh"
+
+namespace kda {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVectors = 4;
+constexpr int kTokens = kThreads * kVectors / 16 + 1;  // of a block: a token has 16 vectors at least
+
+// Place of token t's first key in the cache, in elements: -1 where it has none.
+__device__ int64_t place(const AppendArgs &a, int64_t t) {
+  const Runs &r = a.runs;
+  int64_t begin, end;
+  int b;
+  if (r.cu) {
+    int lo = 0, hi = r.n;  // the last run that starts at or before t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (r.cu[mid] <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    b = lo;
+    if (b == r.n) {  // behind the last run, unless the offsets are malformed
+      if (r.cu[b] > t || r.cu[b] < 0) atomicOr(a.status, KDA_ERR_SHAPE);
+      return -1;
+    }
+    if (!seq_range(r.cu, b, r.total, begin, end) || t < begin || t >= end) {
+      atomicOr(a.status, KDA_ERR_SHAPE);
+      return -1;
+    }
+  } else {
+    b = static_cast<int>(t / r.fixed_len);
+    begin = b * r.fixed_len;
+  }
+  const PagedSeqs &s = a.seqs;
+  int slot;
+  int64_t at;
+  bool ok = run_slot(s, b, slot, at);
+  at += t - begin;
+  const int64_t i = at >> s.page_shift;
+  ok = ok && i < s.max_pages;
+  const int page = ok ? s.table[static_cast<int64_t>(slot) * s.max_pages + i] : -1;
+  if (page < 0 || page >= s.n_pages) {
+    atomicOr(a.status, KDA_ERR_SHAPE);
+    return -1;
+  }
+  return (((static_cast<int64_t>(page) * 2 * a.H) << s.page_shift) + (at & ((1 << s.page_shift) - 1))) * a.D;
+}
+
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a, int per_token, int per_head) {
+  __shared__ int64_t where[kTokens];
+  // vectors of a token: k's heads, then v's
+  const int64_t v0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kVectors), t0 = v0 / per_token;
+  const int first = static_cast<int>(v0 - t0 * per_token);
+  const int tokens = (first + kThreads * kVectors + per_token - 1) / per_token;
+  for (int i = threadIdx.x; i < tokens; i += kThreads)
+    where[i] = t0 + i < a.runs.total ? place(a, t0 + i) : -1;
+  // the rows are read while the places are looked up
+  uint4 v[kVectors];
+  int token[kVectors];
+  int64_t off[kVectors];
+  const int half = per_token / 2;
+  const int64_t plane = static_cast<int64_t>(a.D) << a.seqs.page_shift;
+#pragma unroll
+  for (int j = 0; j < kVectors; ++j) {
+    const int x = first + j * kThreads + threadIdx.x;
+    token[j] = x / per_token;
+    const int in = x - token[j] * per_token, is_v = in >= half, row = in - (is_v ? half : 0);
+    const int h = row / per_head, e = (row - h * per_head) * 8;
+    const int64_t t = t0 + token[j];
+    off[j] = (static_cast<int64_t>(is_v ? a.H : 0) + h) * plane + e;
+    if (t < a.runs.total)
+      v[j] = *reinterpret_cast<const uint4 *>((is_v ? a.v + t * a.ldv : a.k + t * a.ldk) + row * 8);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kVectors; ++j) {
+    const int64_t at = where[token[j]];
+    if (at >= 0) *reinterpret_cast<uint4 *>(a.cache + at + off[j]) = v[j];
+  }
+}
+
+}  // namespace
+
+cudaError_t kv_append_launch(const AppendArgs &a, cudaStream_t st) {
+  const int per_token = 2 * a.H * a.D / 8;
+  const int64_t blocks = (a.runs.total * per_token + kThreads * kVectors - 1) / (kThreads * kVectors);
+  kv_append_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(a, per_token, a.D / 8);
+  return cudaGetLastError();
+}
+
+}  // namespace kda

@@ -487,6 +487,41 @@ int kda_kv_append(const kda_bf16 *k, int64_t ldk, const kda_bf16 *v, int64_t ldv
                   const int32_t *lens, int n_slots, const int32_t *slots, kda_stream_t stream);
 
 /*
+ * kda_attn_paged - causal attention of a batch of runs over the pages of their
+ * sequences: with the position i of token t of a run,
+ *   o_t = sum_j softmax_j(scale q_t . k_j) v_j      over j <= i, and with
+ *                                                   window > 0 over j > i - window.
+ *   q, o   [total, Hq, D] bf16, rows ldq / ldo elements apart, 16-byte aligned
+ *          (ldq, ldo multiples of 8); H divides Hq, and query head h reads head
+ *          h / (Hq / H) of the cache.  o may be q (with the same rows).
+ *   scale  > 0 and finite; window >= 0 (0: all positions).
+ * The run's own keys and values are in the cache before (kda_kv_append).  Where a
+ * row's window ends, entries of the table for pages that it no longer reaches are
+ * not looked at.  A needed page outside [0, n_pages) is recorded and counts as keys
+ * and values of 0.  A key or value that is not finite makes the outputs of its
+ * own sequence undefined; other sequences are not touched by it, and what pages
+ * hold behind a sequence's end is not used.  Rows of o outside all runs are
+ * left as they were.
+ *   workspace   device scratch, 16-byte aligned, not to be shared by calls that
+ *               overlap on the GPU.  With fewer than
+ *               kda_attn_paged_workspace_bytes() bytes (or NULL) no sequence's
+ *               keys are shared out between SMs: the same results up to
+ *               rounding, slower for few tokens.
+ * Precision: scores, sums and o before its rounding are fp32; the weights are
+ * rounded to bf16 before they meet v.  The same call gives the same bits.
+ * Bounded in-kernel waits that give up are recorded as KDA_ERR_TIMEOUT.
+ *   Errors: KDA_ERR_NULL, _SHAPE, _ALIGN, _UNSUPPORTED, _CUDA.
+ */
+int kda_attn_paged(const kda_bf16 *q, int64_t ldq, const int32_t *cu_seqlens, int n,
+                   int64_t total_tokens, int Hq, int H, int D, const kda_bf16 *cache, int n_pages,
+                   int page, const int32_t *table, int max_pages, const int32_t *lens, int n_slots,
+                   const int32_t *slots, float scale, int window, kda_bf16 *o, int64_t ldo,
+                   void *workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/* Workspace bytes of kda_attn_paged (0: none needed, or unsupported sizes). */
+size_t kda_attn_paged_workspace_bytes(int n, int64_t total_tokens, int Hq, int H, int D);
+
+/*
  * kda_pages_grow - give rows of the table the pages that sequences of want[s]
  * instead of lens[s] tokens need (int32 [n_slots]; no more than lens[s]: none).
  * The unused pages are given out in ascending order, to the rows in ascending

@@ -48,7 +48,8 @@ EXPORTED = ("kda_status_string", "kda_version", "kda_chunk_fwd_workspace_bytes",
             "kda_chunk_fwd_noalloc", "kda_decode_tokens", "kda_chunk_fwd_ex",
             "kda_decode_step_ex", "kda_stream_status_bind", "kda_stream_status",
             "kda_conv_fwd", "kda_conv_tokens", "kda_ssm_fwd", "kda_ssm_fwd_workspace_bytes",
-            "kda_ssm_tokens", "kda_verify_draft", "kda_kv_append", "kda_pages_grow",
+            "kda_ssm_tokens", "kda_verify_draft", "kda_kv_append", "kda_attn_paged",
+            "kda_attn_paged_workspace_bytes", "kda_pages_grow",
             "kda_pages_fork", "kda_pages_compact", "kda_pages_workspace_bytes")
 
 _lib = None
@@ -117,6 +118,11 @@ def lib():
         L.kda_verify_draft.argtypes = [P, P, I, I, P, P, P, I, I64, P, P, P]
         L.kda_kv_append.restype = I
         L.kda_kv_append.argtypes = [P, I64, P, I64, P, I, I64, I, I, P, I, I, P, I, P, I, P, P]
+        L.kda_attn_paged.restype = I
+        L.kda_attn_paged.argtypes = [P, I64, P, I, I64, I, I, I, P, I, I, P, I, P, I, P, F, I, P, I64,
+                                     P, SZ, P]
+        L.kda_attn_paged_workspace_bytes.restype = SZ
+        L.kda_attn_paged_workspace_bytes.argtypes = [I, I64, I, I, I]
         L.kda_pages_grow.restype = I
         L.kda_pages_grow.argtypes = [P, I, P, P, I, I, I, P, P]
         L.kda_pages_fork.restype = I
@@ -339,4 +345,5 @@ def stream_status(stream=None, reset=True):
 from .serving import (conv_fwd, conv_tokens, ssm_fwd, ssm_tokens,  # noqa: E402,F401
                       ssm_workspace_bytes, verify_draft)
 # The paged cache of attention layers.
-from .paged import kv_append, pages_compact, pages_fork, pages_grow  # noqa: E402,F401
+from .paged import (attn_paged, attn_workspace_bytes, kv_append, pages_compact,  # noqa: E402,F401
+                    pages_fork, pages_grow)

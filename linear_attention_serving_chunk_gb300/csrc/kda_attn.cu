@@ -1,0 +1,826 @@
+// Causal attention of a batch of runs over a paged cache, on tcgen05.
+//
+//   o_r = sum_j p_rj v_j / sum_j p_rj,   p_rj = exp(scale q_r . k_j - m_r),   j <= position of r
+//
+// in one pass over the keys, with the running maximum m and sum of each row (a tile that raises the
+// maximum scales what was summed before).  A row is one token and one of the G heads that share a
+// head of keys: rows are packed token by token, so a tile of 128 rows holds 128 / G tokens and
+// every key that is read serves all of them.
+//
+// An item is a (run, head of keys, 256 rows) and its tiles of 128 keys; kda_attn_plan.cuh cuts the
+// items of a call into equal shares of tiles, one for each of 152 CTAs, whatever the lengths: an
+// item that is cut leaves (m, sum, o) of its parts in the workspace and a second kernel joins them.
+// Nothing is taken in turn, so the same call gives the same bits.
+//
+// One CTA: two warpgroups, each with its 128 rows' scores, weights and sums in TMEM, a warp that
+// issues the MMAs, and one that looks up pages and loads tiles by TMA.
+//   S_w = Q_w K^T         128 x 128 x D, K-major tiles
+//   P_w = exp(..) bf16    in the columns of S_w, read from there by the MMA
+//   O_w += P_w V          128 x D x 128, V as it lies in the cache
+// While one warpgroup turns its scores into weights the tensor core works for the other.  Items of
+// more than 128 rows give each warpgroup 128 of them, with the same tiles.  Those of at most 128
+// (tokens, drafted runs) give both the same rows and every other tile: then the keys are what counts,
+// and two chains hide each other's latency; their sums meet in shared memory at the end.
+//
+// Scores, maxima, sums and O are fp32.  The weights are rounded to bf16 for their product with V,
+// which a row's sum does not see: 2^-9 of each weight, in either direction.  A maximum is kept until
+// a score is more than 2^8 above it in the exponent's base: weights up to 256 lose nothing, and most
+// tiles then need no scaling of O.
+//
+// A warp whose rows are all beyond the item (three of four in a step of single tokens) computes
+// nothing.  Keys behind a row's position, or behind the window, weigh nothing whatever they are; the
+// rows of V behind the sequence are zeroed, for 0 times what lies there might not be 0.
+#include <string.h>
+
+#include "kda_attn_plan.cuh"
+#include "kda_paged.cuh"
+#include "kda_pdl.cuh"
+#include "kda_sm100.cuh"
+#include "kda_tc_common.cuh"
+
+namespace kda {
+
+namespace {
+
+using namespace sm100;
+using attn::kCtas;
+using attn::kRows;
+using attn::kTile;
+using attn::Run;
+
+constexpr int kThreads = 384;  // (the last two warps have nothing to do: registers go by warpgroups)
+// Registers a thread: a launch of 384 threads gives 168 to each, 3 x 168 = 2 x 208 + 88.
+constexpr int kRowRegs = 208, kOtherRegs = 88;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr uint32_t kPolls = 1u << 20;
+constexpr float kKeep = 8.f;  // log2
+
+struct AttnArgs {
+  const kda_bf16 *q;
+  int64_t ldq;
+  kda_bf16 *o;
+  int64_t ldo;
+  Runs runs;
+  PagedSeqs seqs;
+  int H, G, window;
+  float scale2;   // scale times log2(e)
+  uint8_t *ws;    // or NULL: no item is cut
+  int *status;
+};
+
+// The workspace: for each CTA what the first item that it cuts off needs, then the parts: 2 c is the
+// end or the middle of an item that an earlier CTA began, 2 c + 1 the beginning of one that CTA c began.
+struct Cut {
+  int rows, row0, token0, head, last;  // last: the CTA of the last part; rows 0: nothing is cut
+  int pad[3];
+};
+constexpr size_t kCutBytes = sizeof(Cut) * kCtas;
+constexpr size_t kStatBytes = sizeof(float2) * kRows * 2 * kCtas;
+constexpr size_t ws_bytes(int D) { return kCutBytes + kStatBytes + sizeof(float) * kRows * 2 * kCtas * D; }
+
+struct Item {
+  int rows;    // of the item; -1: there is none any more
+  int row0;    // its first one in the run
+  int token0;  // the run's first token
+  int head;    // of keys
+  int before;  // tokens in front of the run
+  int reach;   // and with it
+  int lo, n;   // tiles
+  int slot;
+  int part;    // of the workspace, -1: the whole item
+};
+constexpr int kItems = 4;
+
+template <int D>
+struct Smem {
+  static constexpr uint32_t kRegion = kTile * 128;              // 64 columns of a tile
+  static constexpr uint32_t kTileBytes = D / 64 * kRegion;
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr uint32_t Q = 0;
+  static constexpr uint32_t MERGE = kTileBytes;                 // second Q tile, or 128 x 64 fp32
+  static constexpr uint32_t STAGE = MERGE + 32 * 1024;
+  static constexpr uint32_t BAR = STAGE + kStages * kTileBytes;
+  static constexpr uint32_t FULL = BAR, EMPTY = FULL + 8 * kStages, SFULL = EMPTY + 8 * kStages,
+                            PREADY = SFULL + 16, QREADY = PREADY + 16, OFULL = QREADY + 16,
+                            IFULL = OFULL + 16, IEMPTY = IFULL + 8 * kItems,
+                            MFULL = IEMPTY + 8 * kItems, MEMPTY = MFULL + 8, FIN = MEMPTY + 8;
+  static constexpr uint32_t TMEM = FIN + 8;
+  static constexpr uint32_t PLAN = TMEM + 8;                    // int64: units, position, run's first unit; run
+  static constexpr uint32_t ITEM = PLAN + 8 * 16;
+  static constexpr uint32_t STAT = ITEM + sizeof(Item) * kItems;
+  static constexpr uint32_t BYTES = STAT + 128 * sizeof(float2);
+  static_assert(BYTES <= 232448 && STAGE % 1024 == 0 && MERGE % 1024 == 0 && STAT % 8 == 0 && TMEM % 8 == 0, "shared memory");
+};
+
+template <int REGS, bool MORE>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (MORE)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc]^T: A is 128 rows of packed bf16 pairs, one column for two k.
+__device__ __forceinline__ void mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Two values as bf16, the first in the lower half.
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Run b as this call takes it: empty where an entry is malformed.
+struct RunAt {
+  int begin, slot;
+  Run run;
+};
+__device__ __forceinline__ RunAt run_at(const AttnArgs &a, int b, bool &bad) {
+  int64_t begin, len, used, before;
+  int slot;
+  bool ok = run_range(a.runs, b, begin, len, used) && run_slot(a.seqs, b, slot, before);
+  if (ok && before + len > (static_cast<int64_t>(a.seqs.max_pages) << a.seqs.page_shift)) ok = false;
+  if (!ok) {
+    bad = true;
+    return RunAt{0, 0, Run{0, 0, a.G, a.window}};
+  }
+  return RunAt{static_cast<int>(begin), slot, Run{static_cast<int>(before), static_cast<int>(len), a.G, a.window}};
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
+  using M = Smem<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+  grid_launch_dependents();
+  if ((sb & 1023u) != 0) {  // the swizzled tiles need it
+    if (tid == 0) atomicOr(a.status, KDA_ERR_UNSUPPORTED);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < M::kStages; ++i) {
+      mbar_init(sb + M::FULL + 8 * i, 1);
+      mbar_init(sb + M::EMPTY + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sb + M::SFULL + 8 * i, 1);
+      mbar_init(sb + M::PREADY + 8 * i, 4);
+      mbar_init(sb + M::QREADY + 8 * i, 4);
+      mbar_init(sb + M::OFULL + 8 * i, 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(sb + M::IFULL + 8 * i, 1);
+      mbar_init(sb + M::IEMPTY + 8 * i, 9);
+    }
+    mbar_init(sb + M::MFULL, 4);
+    mbar_init(sb + M::MEMPTY, 4);
+    mbar_init(sb + M::FIN, 1);
+    fence_mbar_init();
+  }
+  if (warp == kLoadWarp && lane == 0) prefetch_tensormap(&map);
+  if (warp == kMmaWarp) {
+    tmem_alloc(sb + M::TMEM, 512);
+    tmem_relinquish();
+  }
+
+  // This CTA's share: all units, then the run in which the share begins.
+  int64_t *const plan = reinterpret_cast<int64_t *>(smem + M::PLAN);
+  bool bad = false;
+  int64_t units = 0, mine = 0;
+  for (int b = tid; b < a.runs.n; b += kThreads) {
+    mine = run_at(a, b, bad).run.units() * a.H;
+    units += mine;
+  }
+  auto sum_up = [&](int64_t v, int64_t &before) {  // over the block; `before`: over the threads before
+    int64_t x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) plan[4 + warp] = x;
+    __syncthreads();
+    int64_t all = 0;
+    before = x - v;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += plan[4 + w];
+      all += plan[4 + w];
+    }
+    return all;
+  };
+  int64_t before;
+  units = sum_up(units, before);
+  const int64_t each = attn::share(units), start = each * cta, stop = min(start + each, units);
+  if (start < stop) {
+    int64_t carry = 0;
+    for (int b0 = 0; b0 < a.runs.n; b0 += kThreads) {
+      const int b = b0 + tid;
+      if (a.runs.n > kThreads) mine = b < a.runs.n ? run_at(a, b, bad).run.units() * a.H : 0;
+      const int64_t all = sum_up(mine, before);
+      before += carry;
+      if (before <= start && start < before + mine) {
+        plan[0] = before;
+        plan[1] = b;
+      }
+      carry += all;
+      if (carry > start) break;
+    }
+  }
+  if (bad) atomicOr(a.status, KDA_ERR_SHAPE);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kLoadWarp && start < stop) {  // the item of the first unit, 32 ways at a time
+    const int64_t base = plan[0];
+    const int b = static_cast<int>(plan[1]);
+    const RunAt r = run_at(a, b, bad);
+    const int64_t whole = r.run.units(), h = (start - base) / whole, x = start - base - h * whole;
+    int i = 0;
+    for (int hi = r.run.items(); hi - i > 1;) {
+      const int step = (hi - i + 31) / 32, c = i + lane * step;
+      const unsigned some = __ballot_sync(0xffffffffu, c < hi && r.run.units_before(c) <= x);
+      i += (31 - __clz(some)) * step;
+      hi = min(hi, i + step);
+    }
+    __syncwarp();
+    if (lane == 0) {
+      plan[0] = base + h * whole + r.run.units_before(i);  // where it begins
+      plan[2] = h;
+      plan[3] = i;
+    }
+    __syncwarp();
+  }
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + M::TMEM);
+  Item *const items = reinterpret_cast<Item *>(smem + M::ITEM);
+
+  // Every wait is bounded.  A role whose wait gives up leaves its loop, and those that wait for it
+  // give up in their turn.
+  bool gave_up = false;
+  auto wait = [&](uint32_t bar, uint32_t phase) -> bool {
+    uint32_t left = kPolls;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, phase & 1u))
+      if (--left == 0) {
+        gave_up = true;
+        break;
+      }
+    gave_up = __any_sync(0xffffffffu, gave_up) != 0;  // a warp goes on or stops as one
+    return !gave_up;
+  };
+  auto arrive = [&](uint32_t bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+
+  if (warp >= 8) {
+  set_registers<kOtherRegs, false>();
+  if (warp == kLoadWarp) {
+    // ---- items, pages and tiles ------------------------------------------------------------
+    uint32_t fills = 0, stage = 0, given = 0;
+    bool wrong = false;
+    const int per_tile = kTile >> a.seqs.page_shift, halves = D / 64;
+    auto give = [&](const Item &it) -> bool {
+      const uint32_t s = given % kItems;
+      if (!wait(sb + M::IEMPTY + 8 * s, given / kItems + 1)) return false;
+      if (lane == 0) items[s] = it;
+      arrive(sb + M::IFULL + 8 * s);
+      ++given;
+      return true;
+    };
+    // Tile t of keys (or values): pages that no row needs, and those outside the pool, come as zeros.
+    auto load = [&](const Item &it, int t, int values, int first) -> bool {
+      if (!wait(sb + M::EMPTY + 8 * stage, fills / M::kStages + 1)) return false;
+      const uint32_t bar = sb + M::FULL + 8 * stage, to = sb + M::STAGE + stage * M::kTileBytes;
+      if (lane == 0) mbar_expect_tx(bar, M::kTileBytes);
+      __syncwarp();
+      if (lane < per_tile * halves) {
+        const int p = lane / halves, c = lane - p * halves;
+        const int i = t * per_tile + p, at = i << a.seqs.page_shift;
+        int page = -1;
+        if (at < it.reach && at + (1 << a.seqs.page_shift) > first) {
+          page = a.seqs.table[static_cast<int64_t>(it.slot) * a.seqs.max_pages + i];
+          if (page < 0 || page >= a.seqs.n_pages) {
+            page = -1;
+            wrong = true;
+          }
+        }
+        const int plane = page < 0 ? a.seqs.n_pages * 2 * a.H : (page * 2 + values) * a.H + it.head;
+        tma_load_3d(to + c * M::kRegion + (p << a.seqs.page_shift) * 128, &map, c * 64, 0, plane, bar);
+      }
+      ++fills;
+      if (++stage == M::kStages) stage = 0;
+      return true;
+    };
+    auto load_item = [&](const Item &it) -> bool {
+      const int first = a.window ? max(it.before + it.row0 / a.G - a.window + 1, 0) : 0;
+      const int n = it.n, lo = it.lo;
+      if (!load(it, lo, 0, first)) return false;
+      if (it.rows > 128) {
+        for (int j = 0; j < n; ++j) {
+          if (!load(it, lo + j, 1, first)) return false;
+          if (j + 1 < n && !load(it, lo + j + 1, 0, first)) return false;
+        }
+        return true;
+      }
+      // in the order in which the MMAs want them: K of two tiles ahead behind each V
+      if (n > 1 && !load(it, lo + 1, 0, first)) return false;
+      for (int j = 0; j < n; ++j) {
+        if (!load(it, lo + j, 1, first)) return false;
+        if (j + 2 < n && !load(it, lo + j + 2, 0, first)) return false;
+      }
+      return true;
+    };
+
+    if (a.ws && lane < 8) reinterpret_cast<int *>(a.ws)[cta * 8 + lane] = 0;
+    __syncwarp();
+    if (start < stop) {
+      int64_t at = plan[0];
+      int b = static_cast<int>(plan[1]), h = static_cast<int>(plan[2]), i = static_cast<int>(plan[3]);
+      bool none = false;
+      RunAt r = run_at(a, b, none);
+      while (at < stop) {
+        const int lo = r.run.first(i), n = r.run.end(i) - lo;
+        // this share's part of the item, in tiles
+        const int64_t skip = at + attn::kItemUnits;
+        int from = start > skip ? static_cast<int>(start - skip) : 0;
+        int to = static_cast<int>(min(stop - skip, static_cast<int64_t>(n)));
+        if (!a.ws) {  // an item belongs to the share in which it begins
+          from = 0;
+          to = at >= start ? n : 0;
+        }
+        if (from < to) {
+          Item it;
+          it.row0 = i * kRows;
+          it.rows = min(r.run.rows() - it.row0, kRows);
+          it.token0 = r.begin;
+          it.head = h;
+          it.before = r.run.before;
+          it.reach = r.run.before + r.run.len;
+          it.lo = lo + from;
+          it.n = to - from;
+          it.slot = r.slot;
+          it.part = from > 0 ? 2 * cta : to < n ? 2 * cta + 1 : -1;
+          if (from == 0 && to < n && lane == 0)
+            reinterpret_cast<Cut *>(a.ws)[cta] = Cut{it.rows, it.row0, it.token0, h, static_cast<int>((skip + n - 1) / each), {}};
+          if (!give(it) || !load_item(it)) break;
+        }
+        at = skip + n;
+        if (++i == r.run.items()) {
+          i = 0;
+          if (++h == a.H) {
+            h = 0;
+            do {
+              if (++b >= a.runs.n) break;
+              r = run_at(a, b, none);
+            } while (r.run.len == 0);
+            if (b >= a.runs.n) break;
+          }
+        }
+      }
+    }
+    Item end{};
+    end.rows = -1;
+    if (!gave_up) give(end);
+    if (__any_sync(0xffffffffu, wrong) && lane == 0) atomicOr(a.status, KDA_ERR_SHAPE);
+    if (gave_up) {  // the tiles on their way
+      const uint32_t n = min(fills, static_cast<uint32_t>(M::kStages));
+      for (uint32_t f = fills - n; f < fills; ++f)
+        mbar_wait_bounded(sb + M::FULL + 8 * (f % M::kStages), (f / M::kStages) & 1u, kPolls);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---- MMAs ------------------------------------------------------------------------------
+    constexpr uint32_t ID_S = idesc_mma(128, kTile, kFmtBF16, kFmtBF16, 0, 0);
+    constexpr uint32_t ID_O = idesc_mma(128, D, kFmtBF16, kFmtBF16, 0, 1);
+    uint32_t used = 0, stage = 0, taken = 0, q_n[2] = {0, 0}, p_n[2] = {0, 0};
+    // (descriptors from an address that the compiler cannot see through: hoisted out of the loop, the
+    // sums of all steps would take most of this warp's registers)
+    auto scores = [&](int w, int q, uint32_t k) {
+      if (lane == 0) {
+        uint32_t qa = sb + M::Q + q * M::kTileBytes;
+        asm volatile("" : "+r"(qa), "+r"(k));
+        const uint64_t qd = sw128_desc(qa, 16, 1024), kd = sw128_desc(k, 16, 1024);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint32_t off = ((s >> 2) * M::kRegion + (s & 3) * 32) >> 4;
+          mma_f16(tmem + w * 128, qd + off, kd + off, ID_S, s > 0);
+        }
+        mma_commit(sb + M::SFULL + 8 * w);
+      }
+      __syncwarp();
+    };
+    auto weighted = [&](int w, uint32_t v, bool add) {
+      if (lane == 0) {
+        uint32_t p = tmem + w * 128;
+        asm volatile("" : "+r"(p), "+r"(v));
+        const uint64_t vd = sw128_desc(v, M::kRegion, 1024);
+#pragma unroll
+        for (int s = 0; s < kTile / 16; ++s)
+          mma_ta(p + 256, p + 8 * s, vd + ((s * 2048) >> 4), ID_O, add || s > 0);
+      }
+      __syncwarp();
+    };
+    auto commit = [&](uint32_t bar) {
+      if (lane == 0) mma_commit(bar);
+      __syncwarp();
+    };
+    auto tile = [&](uint32_t &at, uint32_t &free) -> bool {  // the next one in the ring
+      at = sb + M::STAGE + stage * M::kTileBytes;
+      free = sb + M::EMPTY + 8 * stage;
+      const bool ok = wait(sb + M::FULL + 8 * stage, used / M::kStages);
+      ++used;
+      if (++stage == M::kStages) stage = 0;
+      return ok;
+    };
+    auto turn = [&](int w) { return wait(sb + M::PREADY + 8 * w, p_n[w]++); };
+    auto run = [&]() {
+      for (;;) {
+        const uint32_t s = taken % kItems;
+        if (!wait(sb + M::IFULL + 8 * s, taken / kItems)) return;
+        const Item it = items[s];
+        arrive(sb + M::IEMPTY + 8 * s);
+        ++taken;
+        if (it.rows < 0) return;
+        const bool both = it.rows > 128;  // both warpgroups take every tile
+        const int n = it.n;
+        // the tile in which the sequence ends inside a page: V's rows from there on
+        const int zero_tile = (it.reach & ((1 << a.seqs.page_shift) - 1)) ? it.reach / kTile - it.lo : -1;
+        auto clear = [&](uint32_t v) {
+          const int r0 = it.reach % kTile, r1 = (r0 | ((1 << a.seqs.page_shift) - 1)) + 1;
+          for (int x = lane; x < (r1 - r0) * (D / 8); x += 32) {
+            const int r = r0 + x / (D / 8), c = x % (D / 8);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + (c >> 3) * M::kRegion + r * 128 + (c & 7) * 16), "r"(0) : "memory");
+          }
+          fence_proxy_async();
+          __syncwarp();
+        };
+        uint32_t k, v, k_free, v_free;
+        if (!wait(sb + M::QREADY, q_n[0]++)) return;
+        if (both && !wait(sb + M::QREADY + 8, q_n[1]++)) return;
+        tc_fence_after();
+        if (!tile(k, k_free)) return;
+        scores(0, 0, k);
+        if (both) scores(1, 1, k);
+        commit(k_free);
+        if (both) {
+          for (int j = 0; j < n; ++j) {
+            const bool more = j + 1 < n;
+            if (!tile(v, v_free)) return;
+            if (j == zero_tile) clear(v);
+            if (more && !tile(k, k_free)) return;
+            for (int w = 0; w < 2; ++w) {
+              if (!turn(w)) return;
+              tc_fence_after();
+              weighted(w, v, j > 0);
+              if (w == 1) commit(v_free);
+              if (more) scores(w, w, k);
+              else commit(sb + M::OFULL + 8 * w);
+            }
+            if (more) commit(k_free);
+          }
+        } else {
+          if (n > 1) {
+            if (!tile(k, k_free)) return;
+            scores(1, 0, k);
+            commit(k_free);
+          }
+          for (int j = 0; j < n; ++j) {
+            const int w = j & 1;
+            const bool more = j + 2 < n;
+            if (!tile(v, v_free)) return;
+            if (j == zero_tile) clear(v);
+            if (!turn(w)) return;
+            tc_fence_after();
+            weighted(w, v, j > 1);
+            commit(v_free);
+            if (more) {
+              if (!tile(k, k_free)) return;
+              scores(w, 0, k);
+              commit(k_free);
+            } else {
+              commit(sb + M::OFULL + 8 * w);
+            }
+          }
+        }
+      }
+    };
+    run();
+    commit(sb + M::FIN);
+    mbar_wait_bounded(sb + M::FIN, 0, kPolls);
+  }
+  } else {
+    set_registers<kRowRegs, true>();
+    // ---- weights and results ---------------------------------------------------------------
+    const int w = warp >> 2, quad = warp & 3, r = quad * 32 + lane;  // row of the warpgroup's tile
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t ts = tmem + w * 128 + lanes, to = tmem + 256 + w * 128 + lanes;
+    float2 *const stats = reinterpret_cast<float2 *>(smem + M::STAT);
+    uint32_t taken = 0, s_n = 0, o_n = 0, m_n = 0;
+    auto run = [&]() {
+      for (;;) {
+        const uint32_t is = taken % kItems;
+        if (!wait(sb + M::IFULL + 8 * is, taken / kItems)) return;
+        const Item it = items[is];
+        arrive(sb + M::IEMPTY + 8 * is);
+        ++taken;
+        if (it.rows < 0) return;
+        const bool both = it.rows > 128;
+        const int steps = both ? it.n : (it.n + 1 - w) >> 1;
+        const int row_of = both ? w * 128 : 0;  // of the tile, in the item
+        const bool live = row_of + quad * 32 < it.rows, valid = row_of + r < it.rows;
+        if (both || w == 0) {
+          // Q: 16 bytes a thread, eight rows (16 where D = 64) at once; the MMAs of the last item are done
+          if (w == 1 && !wait(sb + M::MEMPTY, m_n + 1)) return;  // the second tile's place is shared
+          constexpr int kAcross = D / 8, kAtOnce = 128 / kAcross;
+          const int c = (tid & 127) % kAcross;
+          const uint32_t col = sb + M::Q + w * M::kTileBytes + (c >> 3) * M::kRegion;
+#pragma unroll 4
+          for (int i = (tid & 127) / kAcross; i < 128; i += kAtOnce) {
+            const int row = it.row0 + row_of + i;
+            if (row_of + i < it.rows) {
+              const int t = row / a.G, g = row - t * a.G;
+              const uint4 x = *reinterpret_cast<const uint4 *>(a.q + (static_cast<int64_t>(it.token0) + t) * a.ldq + (static_cast<int64_t>(it.head) * a.G + g) * D + c * 8);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(col + i * 128 + (((c & 7) ^ (i & 7)) << 4)), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+            }
+          }
+          fence_proxy_async();
+          arrive(sb + M::QREADY + 8 * w);
+        }
+        const int row = it.row0 + row_of + r, tok = row / a.G;
+        // the positions that the row sees: [see0, see1)
+        const int see1 = it.before + tok + 1, see0 = a.window ? max(see1 - a.window, 0) : 0;
+        float m = -INFINITY, l = 0.f;  // log2
+        for (int j = 0; j < steps; ++j) {
+          if (!wait(sb + M::SFULL + 8 * w, s_n++)) return;
+          if (live) {
+            tc_fence_after();
+            float s[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s[c]);
+            tmem_wait_ld();
+            const int p0 = (it.lo + (both ? j : 2 * j + w)) * kTile;
+            const int c1 = min(max(see1 - p0, 0), kTile), c0 = min(max(see0 - p0, 0), kTile);
+            if (__any_sync(0xffffffffu, valid && (c0 > 0 || c1 < kTile))) {
+              const unsigned seen = c1 > c0 ? c1 - c0 : 0;
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  s[c][i] = static_cast<unsigned>(c * 32 + i - c0) < seen ? s[c][i] : -INFINITY;
+            }
+            float mx[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              mx[c] = s[c][0];
+#pragma unroll
+              for (int i = 1; i < 32; ++i) mx[c] = fmaxf(mx[c], s[c][i]);
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
+            const bool higher = top > m + kKeep;  // (the first finite score is: m is -inf)
+            if (__any_sync(0xffffffffu, higher)) {
+              const float f = higher ? ex2(m - top) : 1.f;
+              if (higher) m = top;
+              l *= f;
+              if (j > 0) {  // O of the tiles before: their MMAs are done, the next one waits for P
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                  float o[32];
+                  tmem_ld32(to + 32 * c, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) o[i] *= f;
+                  tmem_st32(to + 32 * c, o);
+                }
+              }
+            }
+            const float neg = m == -INFINITY ? 0.f : -m;  // (nothing seen yet: every weight is 2^-inf)
+            const float2 scale = make_float2(a.scale2, a.scale2), shift = make_float2(neg, neg);
+            float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float p[32];  // 64 weights as bf16
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float *two = &s[2 * c + i / 16][2 * (i % 16)];
+                float2 x = __ffma2_rn(make_float2(two[0], two[1]), scale, shift);
+                x.x = ex2(x.x);
+                x.y = ex2(x.y);
+                sum[i & 1] = __fadd2_rn(sum[i & 1], x);
+                p[i] = __uint_as_float(pack(x.x, x.y));
+              }
+              tmem_st32(ts + 32 * c, p);
+            }
+            l += sum[0].x + sum[0].y + (sum[1].x + sum[1].y);
+            tmem_wait_st();
+            tc_fence_before();
+          }
+          arrive(sb + M::PREADY + 8 * w);
+        }
+        if (steps == 0) continue;
+        if (!wait(sb + M::OFULL + 8 * w, o_n++)) return;
+        tc_fence_after();
+
+        float *const part = it.part < 0 ? nullptr
+                                        : reinterpret_cast<float *>(a.ws + kCutBytes + kStatBytes) +
+                                              (static_cast<int64_t>(it.part) * kRows + row_of + r) * D;
+        kda_bf16 *const out = a.o + (static_cast<int64_t>(it.token0) + tok) * a.ldo +
+                              (static_cast<int64_t>(it.head) * a.G + (row - tok * a.G)) * D;
+        auto put = [&](const float (&o)[32], int c, float f) {  // columns [32 c, 32 c + 32) of this row
+          if (!valid) return;
+          if (part) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4 *>(part + 32 * c + 4 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t x[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = pack(o[8 * i + 2 * e] * f, o[8 * i + 2 * e + 1] * f);
+              *reinterpret_cast<uint4 *>(out + 32 * c + 8 * i) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          }
+        };
+        auto put_stats = [&]() {
+          if (part && valid)
+            reinterpret_cast<float2 *>(a.ws + kCutBytes)[static_cast<int64_t>(it.part) * kRows + row_of + r] = make_float2(m, l);
+        };
+        if (both || it.n == 1) {
+          const float f = l == 0.f ? 0.f : 1.f / l;
+          if (live) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+              tmem_ld32(to + 32 * c, o);
+              tmem_wait_ld();
+              put(o, c, f);
+            }
+            put_stats();
+          }
+          tc_fence_before();
+          continue;
+        }
+        // two chains of the same rows: the second one's sums come through shared memory, 64 columns at a
+        // time, 16-byte words of a row XORed with the row
+        float mine = 1.f, other = 0.f, inv = 0.f;
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half) {
+          const uint32_t at = sb + M::MERGE + r * 256;
+          if (w == 1) {
+            if (!wait(sb + M::MEMPTY, m_n + 1)) return;
+            ++m_n;
+            if (live) {
+              if (half == 0) stats[r] = make_float2(m, l);
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float o[32];
+                tmem_ld32(to + 64 * half + 32 * c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((c * 8 + i) ^ (r & 15)) << 4)), "f"(o[4 * i]), "f"(o[4 * i + 1]), "f"(o[4 * i + 2]), "f"(o[4 * i + 3]) : "memory");
+              }
+            }
+            arrive(sb + M::MFULL);
+          } else {
+            if (!wait(sb + M::MFULL, m_n)) return;
+            ++m_n;
+            if (live) {
+              if (half == 0) {
+                const float2 t = stats[r];
+                const float top = fmaxf(m, t.x), base = top == -INFINITY ? 0.f : top;
+                mine = ex2(m - base);
+                other = ex2(t.x - base);
+                l = l * mine + t.y * other;
+                m = top;
+                inv = l == 0.f ? 0.f : 1.f / l;
+              }
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float o[32];
+                tmem_ld32(to + 64 * half + 32 * c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  float x[4];
+                  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(at + (((c * 8 + i) ^ (r & 15)) << 4)) : "memory");
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) o[4 * i + e] = o[4 * i + e] * mine + x[e] * other;
+                }
+                put(o, 2 * half + c, inv);
+              }
+              if (half == 0) put_stats();
+            }
+            arrive(sb + M::MEMPTY);
+          }
+        }
+        tc_fence_before();
+      }
+    };
+    run();
+  }
+  if (gave_up && lane == 0) atomicOr(a.status, KDA_ERR_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of each item that was cut: a warp takes a row, o = sum 2^(m_p - m) o_p / sum 2^(m_p - m) l_p.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinBlocks = 16;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
+  grid_dependency_wait();
+  const int cta = blockIdx.x, lane = threadIdx.x & 31;
+  const Cut cut = reinterpret_cast<const Cut *>(a.ws)[cta];
+  const float2 *stats = reinterpret_cast<const float2 *>(a.ws + kCutBytes);
+  const float *parts = reinterpret_cast<const float *>(a.ws + kCutBytes + kStatBytes);
+  const int n = cut.last - cta + 1;  // the first is 2 cta + 1, the others 2 c
+  auto place = [&](int p, int r) { return static_cast<int64_t>(p ? 2 * (cta + p) : 2 * cta + 1) * kRows + r; };
+  for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < cut.rows;
+       r += kJoinBlocks * (kJoinThreads / 32)) {
+    float top = -INFINITY;
+    for (int p = lane; p < n; p += 32) top = fmaxf(top, stats[place(p, r)].x);
+#pragma unroll
+    for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if (top == -INFINITY) top = 0.f;
+    constexpr int kCols = D / 32;
+    float o[kCols] = {}, l = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < n; ++p) {
+      const float2 s = stats[place(p, r)];
+      const float f = ex2(s.x - top);
+      l += s.y * f;
+      const float *x = parts + place(p, r) * D + lane * kCols;
+      if constexpr (kCols == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(x);
+        o[0] += v.x * f, o[1] += v.y * f, o[2] += v.z * f, o[3] += v.w * f;
+      } else {
+        const float2 v = *reinterpret_cast<const float2 *>(x);
+        o[0] += v.x * f, o[1] += v.y * f;
+      }
+    }
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    const int row = cut.row0 + r, t = row / a.G, g = row - t * a.G;
+    kda_bf16 *out = a.o + (static_cast<int64_t>(cut.token0) + t) * a.ldo + (static_cast<int64_t>(cut.head) * a.G + g) * D + lane * kCols;
+    uint32_t x[kCols / 2];
+#pragma unroll
+    for (int e = 0; e < kCols / 2; ++e) x[e] = pack(o[2 * e] * f, o[2 * e + 1] * f);
+    if constexpr (kCols == 4) *reinterpret_cast<uint2 *>(out) = make_uint2(x[0], x[1]);
+    else *reinterpret_cast<uint32_t *>(out) = x[0];
+  }
+}
+
+template <int D>
+cudaError_t run(const AttnArgs &a, const kda_bf16 *cache, cudaStream_t st) {
+  const tcx::EncodeTiledFn encode = tcx::tensor_map_encoder();
+  if (!encode) return cudaErrorInvalidValue;
+  CUtensorMap map;
+  memset(&map, 0, sizeof(map));
+  const int page = 1 << a.seqs.page_shift;
+  const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(a.seqs.n_pages) * 2 * a.H};
+  const cuuint64_t strides[2] = {2 * D, static_cast<cuuint64_t>(2) * D * page};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(page), 1};
+  const cuuint32_t step[3] = {1, 1, 1};
+  if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<kda_bf16 *>(cache), dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  const auto kernel = attn_kernel<D>;
+  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::BYTES))
+    return e;
+  kernel<<<kCtas, kThreads, Smem<D>::BYTES, st>>>(map, a);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  if (!a.ws) return cudaSuccess;
+  return launch_pdl(attn_join_kernel<D>, dim3(kCtas, kJoinBlocks), dim3(kJoinThreads), 0, st, a);
+}
+
+}  // namespace
+
+size_t attn_workspace(int D) { return ws_bytes(D); }
+
+cudaError_t attn_launch(const AttnCall &c, int D, cudaStream_t st) {
+  AttnArgs a{c.q, c.ldq, c.o, c.ldo, c.runs, c.seqs, c.H, c.G, c.window,
+             c.scale * 1.44269504088896340736f, static_cast<uint8_t *>(c.workspace), c.status};
+  return D == 64 ? run<64>(a, c.cache, st) : run<128>(a, c.cache, st);
+}
+
+}  // namespace kda

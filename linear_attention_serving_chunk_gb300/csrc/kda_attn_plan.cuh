@@ -1,0 +1,78 @@
+// How the work of paged attention is cut into tiles and shared out.  Host and device: no memory is
+// touched here.
+#pragma once
+
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define KDA_HD __host__ __device__ __forceinline__
+#else
+#define KDA_HD inline
+#endif
+
+namespace kda {
+namespace attn {
+
+constexpr int kRows = 256;     // rows (token, head of the group) of an item, two tiles of 128
+constexpr int kTile = 128;     // positions of a tile of keys
+constexpr int kItemUnits = 1;  // what an item costs beside its tiles, in tiles
+constexpr int kCtas = 152;     // one on each SM
+constexpr int kLeastUnits = 4;
+
+KDA_HD int64_t floor_div(int64_t a, int64_t b) { return a >= 0 ? a / b : -((b - 1 - a) / b); }
+
+// Sum of floor((2 k + b) / G) over k in [0, n), b >= 0.
+//
+// With b < G (the rest is n times b / G) the terms are the y in [1, m] with y G <= 2 k + b, where m
+// is the last term: n m less, for each y, the ceil((y G - b) / 2) values of k that do not reach it.
+KDA_HD int64_t floor_sum(int64_t n, int64_t G, int64_t b) {
+  if (n <= 0) return 0;
+  int64_t sum = n * (b / G);
+  b %= G;
+  if (G == 1) return sum + n * (n - 1);
+  const int64_t m = (2 * (n - 1) + b) / G, odd = G & 1;
+  // the sum of ceil(x / 2), x = y G - b: (x + 1) / 2 where x is odd
+  const int64_t n_odd = odd ? (b & 1 ? m / 2 : (m + 1) / 2) : (b & 1 ? m : 0);
+  return sum + n * m - (G * (m * (m + 1) / 2) - m * b + n_odd) / 2;
+}
+
+// One run: `len` tokens behind `before` ones, G heads a token, rows token by token.  Item i has rows
+// [256 i, 256 i + 256) and the tiles that any of them sees.  Positions are under 2^27 and rows under 2^31.
+struct Run {
+  int before, len, G, window;  // window: the positions a token sees, 0 for all
+
+  KDA_HD int rows() const { return len * G; }
+  KDA_HD int items() const { return static_cast<int>((static_cast<unsigned>(rows()) + kRows - 1) / kRows); }
+  // Tiles in front of the item's first and behind its last.
+  KDA_HD int first(int i) const {
+    if (!window) return 0;
+    const int p = before + i * kRows / G - window + 1;
+    return p > 0 ? p / kTile : 0;
+  }
+  KDA_HD int end(int i) const {
+    const int last = static_cast<int>((static_cast<unsigned>(i + 1) * kRows - 1) / G);
+    return (before + (last < len - 1 ? last : len - 1) + kTile) / kTile;
+  }
+  // Units of the items in front of item i: both ends grow by 256 / (128 G) tiles an item, rounded down.
+  KDA_HD int64_t units_before(int i) const {
+    const int n = items();
+    const int64_t k = i < n ? i : n - 1;
+    if (n == 0) return 0;
+    int64_t sum = k * kItemUnits + floor_sum(k, G, (static_cast<int64_t>(G) * (before + kTile) + kRows - 1) / kTile);
+    if (window) {
+      const int64_t b = floor_div(static_cast<int64_t>(G) * (before - window + 1), kTile), skip = b < 0 ? (1 - b) / 2 : 0;
+      if (k > skip) sum -= floor_sum(k - skip, G, 2 * skip + b);
+    }
+    return i < n ? sum : sum + kItemUnits + end(n - 1) - first(n - 1);
+  }
+  KDA_HD int64_t units() const { return units_before(items()); }
+};
+
+// Units of a CTA.
+KDA_HD int64_t share(int64_t units) {
+  const int64_t each = (units + kCtas - 1) / kCtas;
+  return each > kLeastUnits ? each : kLeastUnits;
+}
+
+}  // namespace attn
+}  // namespace kda

@@ -36,6 +36,20 @@ struct AppendArgs {
   int *status;
 };
 
+struct AttnCall {
+  const kda_bf16 *q;
+  int64_t ldq;
+  kda_bf16 *o;
+  int64_t ldo;
+  Runs runs;
+  PagedSeqs seqs;
+  const kda_bf16 *cache;
+  int H, G, window;  // heads of keys, query heads for each
+  float scale;
+  void *workspace;   // attn_workspace(D) bytes, or NULL
+  int *status;
+};
+
 enum PagesOp { kPagesGrow, kPagesFork, kPagesCompact };
 
 struct PagesArgs {
@@ -65,6 +79,8 @@ __host__ __device__ constexpr int64_t pages_ws_bytes(int64_t n) {
 constexpr int kMaxPages = 1 << 20;  // of a pool, and of a row of the table
 constexpr int kMaxSlots = 1 << 14;
 
+size_t attn_workspace(int D);
+cudaError_t attn_launch(const AttnCall &c, int D, cudaStream_t st);
 cudaError_t kv_append_launch(const AppendArgs &a, cudaStream_t st);
 cudaError_t pages_launch(PagesOp op, const PagesArgs &a, cudaStream_t st);
 // The moves of a plan: `layers` layers of n_pages pages of `planes` planes of row_bytes a token.

@@ -97,6 +97,47 @@ int kda_kv_append(const kda_bf16 *k, int64_t ldk, const kda_bf16 *v, int64_t ldv
   return launched(kv_append_launch(a, st));
 }
 
+int kda_attn_paged(const kda_bf16 *q, int64_t ldq, const int32_t *cu_seqlens, int n,
+                   int64_t total_tokens, int Hq, int H, int D, const kda_bf16 *cache, int n_pages,
+                   int page, const int32_t *table, int max_pages, const int32_t *lens, int n_slots,
+                   const int32_t *slots, float scale, int window, kda_bf16 *o, int64_t ldo,
+                   void *workspace, size_t workspace_bytes, kda_stream_t stream) {
+  int64_t fixed_len;
+  if (int e = check_runs(cu_seqlens, n, total_tokens, &fixed_len)) return e;
+  if (int e = check_table(table, lens, max_pages, n_slots, n_pages, page)) return e;
+  if (int e = check_heads(H, D, cache, n_pages)) return e;
+  if (Hq <= 0 || Hq % H != 0 || Hq > 65535 || window < 0) return KDA_ERR_SHAPE;
+  if (!slots && n > n_slots) return KDA_ERR_SHAPE;
+  // (also refuses NaN)
+  if (!(scale > 0.f && scale <= 3e38f)) return KDA_ERR_UNSUPPORTED;
+  const int64_t cols = static_cast<int64_t>(Hq) * D;
+  if (total_tokens > 1 && (ldq < cols || ldo < cols)) return KDA_ERR_SHAPE;
+  if (total_tokens > 0 && (!q || !o)) return KDA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(o) || !aligned4(slots) || !aligned16(workspace))
+    return KDA_ERR_ALIGN;
+  if (total_tokens > 1 && ((ldq | ldo) & 7)) return KDA_ERR_ALIGN;
+  if (total_tokens == 0) return KDA_OK;
+  if (total_tokens * (Hq / H) > 0x7fffff00LL) return KDA_ERR_UNSUPPORTED;  // rows of a run, in 31 bits
+  if (n_pages == 0) return KDA_ERR_SHAPE;  // no token can have a place
+  const int64_t rows = 2 * ((total_tokens - 1) * ldo + cols);
+  // q is read, and the cache, by blocks that run beside the writers of o; o may be q
+  if ((o != q || ldo != ldq) && overlap(o, rows, q, 2 * ((total_tokens - 1) * ldq + cols)))
+    return KDA_ERR_SHAPE;
+  if (overlap(o, rows, cache, 4LL * H * D * page * n_pages)) return KDA_ERR_SHAPE;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool cut = workspace && workspace_bytes >= attn_workspace(D);
+  AttnCall c{q, ldq, o, ldo, Runs{cu_seqlens, nullptr, n, total_tokens, fixed_len},
+             PagedSeqs{table, max_pages, lens, slots, n_slots, n_pages, page_shift(page)}, cache, H,
+             Hq / H, window, scale, cut ? workspace : nullptr, status_word(st)};
+  if (!c.status) return KDA_ERR_CUDA;
+  return launched(attn_launch(c, D, st));
+}
+
+size_t kda_attn_paged_workspace_bytes(int n, int64_t total_tokens, int Hq, int H, int D) {
+  if (n <= 0 || total_tokens <= 0 || H <= 0 || Hq <= 0 || Hq % H != 0 || !size_ok(D)) return 0;
+  return attn_workspace(D);
+}
+
 int kda_pages_grow(int32_t *table, int max_pages, const int32_t *lens, const int32_t *want,
                    int n_slots, int n_pages, int page, int32_t *left, kda_stream_t stream) {
   if (int e = check_table(table, lens, max_pages, n_slots, n_pages, page)) return e;

@@ -15,7 +15,8 @@ from __future__ import annotations
 import torch
 
 from . import KDA_OK, KDAError, lib
-from .serving import _BF16, _I32, _dense, _device, _empty, _on, _refuse, _rows, _runs, _Tensor
+from .serving import (_BF16, _I32, _dense, _device, _empty, _on, _refuse, _result, _rows, _runs,
+                      _Tensor)
 
 
 def _cache(cache, layers, dev):
@@ -76,6 +77,39 @@ def kv_append(k, v, cache, table, lens, slots=None, cu_seqlens=None, stream=None
                              _dense(slots, "slots", _I32, (n,), dev), _on(stream, dev))
     if st != KDA_OK:
         raise KDAError("kda_kv_append", st)
+
+
+def attn_workspace_bytes(n, total_tokens, Hq, H, D):
+    return int(lib().kda_attn_paged_workspace_bytes(n, total_tokens, Hq, H, D))
+
+
+def attn_paged(q, cache, table, lens, slots=None, cu_seqlens=None, scale=None, window=0, o=None,
+               workspace=None, stream=None):
+    """Causal attention of a batch of runs over the pages of their sequences (kda_attn_paged).  q
+    [total, Hq, D] bf16 (rows may be slices of wider ones); cache, table, lens, slots and
+    cu_seqlens as for kv_append, which has put the runs' own keys and values there; scale: D ** -0.5
+    where it is None; window: the positions a token sees, 0 for all.  workspace:
+    attn_workspace_bytes(...) bytes, allocated where it is None.  Returns o [total, Hq, D] bf16."""
+    dev = _device(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, Hq, D]")
+    total, Hq, D = q.shape
+    cu, n = _runs(cu_seqlens, total, dev)
+    at, _, n_pages, H, page, D_c = _cache(cache, False, dev)
+    if D_c != D:
+        raise ValueError(f"cache has heads of {D_c}, q of {D}")
+    tp, most, lp, n_slots = _table(table, lens, dev)
+    o, op, ldo = _result(o, (total, Hq, D), dev, stream)
+    L = lib()
+    workspace, wp, size = _scratch(
+        workspace, L.kda_attn_paged_workspace_bytes(n, total, Hq, H, D), dev, stream)
+    st = L.kda_attn_paged(*_rows(q, "q", (total, Hq, D), dev), cu, n, total, Hq, H, D, at, n_pages,
+                          page, tp, most, lp, n_slots, _dense(slots, "slots", _I32, (n,), dev),
+                          D ** -0.5 if scale is None else scale, window, op, ldo, wp, size,
+                          _on(stream, dev))
+    if st != KDA_OK:
+        raise KDAError("kda_attn_paged", st)
+    return o
 
 
 def _count(t, name, dev, stream):

@@ -48,10 +48,10 @@ using attn::kRows;
 using attn::kTile;
 using attn::Run;
 
-constexpr int kThreads = 384;  // (the last two warps have nothing to do: registers go by warpgroups)
+constexpr int kThreads = 384;
 // Registers a thread: a launch of 384 threads gives 168 to each, 3 x 168 = 2 x 208 + 88.
 constexpr int kRowRegs = 208, kOtherRegs = 88;
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10, kLoadVWarp = 11;
 constexpr uint32_t kPolls = 1u << 20;
 constexpr float kKeep = 8.f;  // log2
 
@@ -124,6 +124,12 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+__device__ __forceinline__ bool elect() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem desc]^T: A is 128 rows of packed bf16 pairs, one column for two k.
 __device__ __forceinline__ void mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                        uint32_t idesc, uint32_t accumulate) {
@@ -165,7 +171,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
   using M = Smem<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, cta = blockIdx.x;
   grid_launch_dependents();
   if ((sb & 1023u) != 0) {  // the swizzled tiles need it
     if (tid == 0) atomicOr(a.status, KDA_ERR_UNSUPPORTED);
@@ -184,7 +190,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(sb + M::IFULL + 8 * i, 1);
-      mbar_init(sb + M::IEMPTY + 8 * i, 9);
+      mbar_init(sb + M::IEMPTY + 8 * i, 11);
     }
     mbar_init(sb + M::MFULL, 4);
     mbar_init(sb + M::MEMPTY, 4);
@@ -226,46 +232,31 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
   int64_t before;
   units = sum_up(units, before);
   const int64_t each = attn::share(units), start = each * cta, stop = min(start + each, units);
-  if (start < stop) {
+  auto found = [&](int b) {
+    if (before <= start && start < before + mine) {
+      plan[0] = before;
+      plan[1] = mine / a.H;
+      plan[2] = b;
+    }
+  };
+  if (a.runs.n <= kThreads) {
+    found(tid);
+  } else if (start < stop) {
     int64_t carry = 0;
-    for (int b0 = 0; b0 < a.runs.n; b0 += kThreads) {
+    for (int b0 = 0; b0 < a.runs.n && carry <= start; b0 += kThreads) {
       const int b = b0 + tid;
-      if (a.runs.n > kThreads) mine = b < a.runs.n ? run_at(a, b, bad).run.units() * a.H : 0;
+      mine = b < a.runs.n ? run_at(a, b, bad).run.units() * a.H : 0;
       const int64_t all = sum_up(mine, before);
       before += carry;
-      if (before <= start && start < before + mine) {
-        plan[0] = before;
-        plan[1] = b;
-      }
       carry += all;
-      if (carry > start) break;
+      found(b);
     }
   }
   if (bad) atomicOr(a.status, KDA_ERR_SHAPE);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kLoadWarp && start < stop) {  // the item of the first unit, 32 ways at a time
-    const int64_t base = plan[0];
-    const int b = static_cast<int>(plan[1]);
-    const RunAt r = run_at(a, b, bad);
-    const int64_t whole = r.run.units(), h = (start - base) / whole, x = start - base - h * whole;
-    int i = 0;
-    for (int hi = r.run.items(); hi - i > 1;) {
-      const int step = (hi - i + 31) / 32, c = i + lane * step;
-      const unsigned some = __ballot_sync(0xffffffffu, c < hi && r.run.units_before(c) <= x);
-      i += (31 - __clz(some)) * step;
-      hi = min(hi, i + step);
-    }
-    __syncwarp();
-    if (lane == 0) {
-      plan[0] = base + h * whole + r.run.units_before(i);  // where it begins
-      plan[2] = h;
-      plan[3] = i;
-    }
-    __syncwarp();
-  }
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + M::TMEM);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(smem + M::TMEM), 0);
   Item *const items = reinterpret_cast<Item *>(smem + M::ITEM);
 
   // Every wait is bounded.  A role whose wait gives up leaves its loop, and those that wait for it
@@ -289,11 +280,9 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
 
   if (warp >= 8) {
   set_registers<kOtherRegs, false>();
-  if (warp == kLoadWarp) {
-    // ---- items, pages and tiles ------------------------------------------------------------
-    uint32_t fills = 0, stage = 0, given = 0;
-    bool wrong = false;
-    const int per_tile = kTile >> a.seqs.page_shift, halves = D / 64;
+  if (warp == kItemWarp) {
+    // ---- items -----------------------------------------------------------------------------
+    uint32_t given = 0;
     auto give = [&](const Item &it) -> bool {
       const uint32_t s = given % kItems;
       if (!wait(sb + M::IEMPTY + 8 * s, given / kItems + 1)) return false;
@@ -302,57 +291,32 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       ++given;
       return true;
     };
-    // Tile t of keys (or values): pages that no row needs, and those outside the pool, come as zeros.
-    auto load = [&](const Item &it, int t, int values, int first) -> bool {
-      if (!wait(sb + M::EMPTY + 8 * stage, fills / M::kStages + 1)) return false;
-      const uint32_t bar = sb + M::FULL + 8 * stage, to = sb + M::STAGE + stage * M::kTileBytes;
-      if (lane == 0) mbar_expect_tx(bar, M::kTileBytes);
-      __syncwarp();
-      if (lane < per_tile * halves) {
-        const int p = lane / halves, c = lane - p * halves;
-        const int i = t * per_tile + p, at = i << a.seqs.page_shift;
-        int page = -1;
-        if (at < it.reach && at + (1 << a.seqs.page_shift) > first) {
-          page = a.seqs.table[static_cast<int64_t>(it.slot) * a.seqs.max_pages + i];
-          if (page < 0 || page >= a.seqs.n_pages) {
-            page = -1;
-            wrong = true;
-          }
-        }
-        const int plane = page < 0 ? a.seqs.n_pages * 2 * a.H : (page * 2 + values) * a.H + it.head;
-        tma_load_3d(to + c * M::kRegion + (p << a.seqs.page_shift) * 128, &map, c * 64, 0, plane, bar);
-      }
-      ++fills;
-      if (++stage == M::kStages) stage = 0;
-      return true;
-    };
-    auto load_item = [&](const Item &it) -> bool {
-      const int first = a.window ? max(it.before + it.row0 / a.G - a.window + 1, 0) : 0;
-      const int n = it.n, lo = it.lo;
-      if (!load(it, lo, 0, first)) return false;
-      if (it.rows > 128) {
-        for (int j = 0; j < n; ++j) {
-          if (!load(it, lo + j, 1, first)) return false;
-          if (j + 1 < n && !load(it, lo + j + 1, 0, first)) return false;
-        }
-        return true;
-      }
-      // in the order in which the MMAs want them: K of two tiles ahead behind each V
-      if (n > 1 && !load(it, lo + 1, 0, first)) return false;
-      for (int j = 0; j < n; ++j) {
-        if (!load(it, lo + j, 1, first)) return false;
-        if (j + 2 < n && !load(it, lo + j + 2, 0, first)) return false;
-      }
-      return true;
-    };
-
     if (a.ws && lane < 8) reinterpret_cast<int *>(a.ws)[cta * 8 + lane] = 0;
     __syncwarp();
     if (start < stop) {
-      int64_t at = plan[0];
-      int b = static_cast<int>(plan[1]), h = static_cast<int>(plan[2]), i = static_cast<int>(plan[3]);
+      // 32 runs at a time, one in each lane
+      int b = static_cast<int>(plan[2]), held = b;
       bool none = false;
-      RunAt r = run_at(a, b, none);
+      RunAt lot = run_at(a, min(b + lane, a.runs.n - 1), none), r;
+      auto take = [&]() {
+        if (b >= held + 32) {
+          held = b;
+          lot = run_at(a, min(b + lane, a.runs.n - 1), none);
+        }
+        const int from = b - held;
+        r = RunAt{__shfl_sync(0xffffffffu, lot.begin, from), __shfl_sync(0xffffffffu, lot.slot, from),
+                  Run{__shfl_sync(0xffffffffu, lot.run.before, from), __shfl_sync(0xffffffffu, lot.run.len, from), a.G, a.window}};
+      };
+      take();
+      const int64_t whole = plan[1], x0 = start - plan[0], h0 = x0 / whole, x = x0 - h0 * whole;
+      int h = static_cast<int>(h0), i = 0;
+      for (int hi = r.run.items(); hi - i > 1;) {  // the item of the first unit, 32 ways at a time
+        const int step = (hi - i + 31) / 32, c = i + lane * step;
+        const unsigned some = __ballot_sync(0xffffffffu, c < hi && r.run.units_before(c) <= x);
+        i += (31 - __clz(some)) * step;
+        hi = min(hi, i + step);
+      }
+      int64_t at = plan[0] + h * whole + r.run.units_before(i);  // where it begins
       while (at < stop) {
         const int lo = r.run.first(i), n = r.run.end(i) - lo;
         // this share's part of the item, in tiles
@@ -377,32 +341,107 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
           it.part = from > 0 ? 2 * cta : to < n ? 2 * cta + 1 : -1;
           if (from == 0 && to < n && lane == 0)
             reinterpret_cast<Cut *>(a.ws)[cta] = Cut{it.rows, it.row0, it.token0, h, static_cast<int>((skip + n - 1) / each), {}};
-          if (!give(it) || !load_item(it)) break;
+          if (!give(it)) break;
         }
         at = skip + n;
-        if (++i == r.run.items()) {
-          i = 0;
-          if (++h == a.H) {
-            h = 0;
-            do {
-              if (++b >= a.runs.n) break;
-              r = run_at(a, b, none);
-            } while (r.run.len == 0);
-            if (b >= a.runs.n) break;
-          }
-        }
+        if (++i < r.run.items()) continue;
+        i = 0;
+        if (++h < a.H) continue;
+        h = 0;
+        do {
+          if (++b == a.runs.n) break;
+          take();
+        } while (r.run.len == 0);
+        if (b == a.runs.n) break;
       }
     }
     Item end{};
     end.rows = -1;
     if (!gave_up) give(end);
+  } else if (warp != kMmaWarp) {
+    // ---- pages and tiles: one warp loads the keys' and one the values' ------------------------
+    const bool mine_is_v = warp == kLoadVWarp;
+    uint32_t fills = 0, stage = 0, taken = 0;
+    bool wrong = false;
+    const int per_tile = kTile >> a.seqs.page_shift; constexpr int halves = D / 64;
+    // Tile t of keys (or values): pages that no row needs, and those outside the pool, come as zeros.
+    auto load = [&](const Item &it, int t, int values, int first) -> bool {
+      if ((values != 0) != mine_is_v) {  // the other's place in the ring
+        ++fills;
+        if (++stage == M::kStages) stage = 0;
+        return true;
+      }
+      if (!wait(sb + M::EMPTY + 8 * stage, fills / M::kStages + 1)) return false;
+      const uint32_t bar = sb + M::FULL + 8 * stage, to = sb + M::STAGE + stage * M::kTileBytes;
+      if (lane == 0) {
+        mbar_expect_tx(bar, M::kTileBytes);
+        const int ahead = (t + 1) * per_tile + 31;  // the table's next line
+        if (ahead < a.seqs.max_pages)
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(a.seqs.table + static_cast<int64_t>(it.slot) * a.seqs.max_pages + ahead));
+      }
+      __syncwarp();
+      int plane = 0;
+      if (lane < per_tile) {
+        const int p = lane;
+        const int i = t * per_tile + p, at = i << a.seqs.page_shift;
+        int page = -1;
+        if (at < it.reach && at + (1 << a.seqs.page_shift) > first) {
+          page = a.seqs.table[static_cast<int64_t>(it.slot) * a.seqs.max_pages + i];
+          if (page < 0 || page >= a.seqs.n_pages) {
+            page = -1;
+            wrong = true;
+          }
+        }
+        plane = page < 0 ? a.seqs.n_pages * 2 * a.H : (page * 2 + values) * a.H + it.head;
+      }
+      for (int p = 0; p < per_tile; ++p) {
+        const int at = __shfl_sync(0xffffffffu, plane, p);
+        if (elect()) {
+#pragma unroll
+          for (int c = 0; c < halves; ++c)
+            tma_load_3d(to + c * M::kRegion + (p << a.seqs.page_shift) * 128, &map, c * 64, 0, at, bar);
+        }
+      }
+      __syncwarp();
+      ++fills;
+      if (++stage == M::kStages) stage = 0;
+      return true;
+    };
+    auto load_item = [&](const Item &it) -> bool {
+      const int first = a.window ? max(it.before + it.row0 / a.G - a.window + 1, 0) : 0;
+      const int n = it.n, lo = it.lo;
+      if (!load(it, lo, 0, first)) return false;
+      if (it.rows > 128) {
+        for (int j = 0; j < n; ++j) {
+          if (!load(it, lo + j, 1, first)) return false;
+          if (j + 1 < n && !load(it, lo + j + 1, 0, first)) return false;
+        }
+        return true;
+      }
+      // in the order in which the MMAs want them: K of two tiles ahead behind each V
+      if (n > 1 && !load(it, lo + 1, 0, first)) return false;
+      for (int j = 0; j < n; ++j) {
+        if (!load(it, lo + j, 1, first)) return false;
+        if (j + 2 < n && !load(it, lo + j + 2, 0, first)) return false;
+      }
+      return true;
+    };
+
+    for (;;) {
+      const uint32_t s = taken % kItems;
+      if (!wait(sb + M::IFULL + 8 * s, taken / kItems)) break;
+      const Item it = items[s];
+      arrive(sb + M::IEMPTY + 8 * s);
+      ++taken;
+      if (it.rows < 0 || !load_item(it)) break;
+    }
     if (__any_sync(0xffffffffu, wrong) && lane == 0) atomicOr(a.status, KDA_ERR_SHAPE);
     if (gave_up) {  // the tiles on their way
       const uint32_t n = min(fills, static_cast<uint32_t>(M::kStages));
       for (uint32_t f = fills - n; f < fills; ++f)
         mbar_wait_bounded(sb + M::FULL + 8 * (f % M::kStages), (f / M::kStages) & 1u, kPolls);
     }
-  } else if (warp == kMmaWarp) {
+  } else {
     // ---- MMAs ------------------------------------------------------------------------------
     constexpr uint32_t ID_S = idesc_mma(128, kTile, kFmtBF16, kFmtBF16, 0, 0);
     constexpr uint32_t ID_O = idesc_mma(128, D, kFmtBF16, kFmtBF16, 0, 1);
@@ -410,7 +449,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
     // (descriptors from an address that the compiler cannot see through: hoisted out of the loop, the
     // sums of all steps would take most of this warp's registers)
     auto scores = [&](int w, int q, uint32_t k) {
-      if (lane == 0) {
+      if (elect()) {
         uint32_t qa = sb + M::Q + q * M::kTileBytes;
         asm volatile("" : "+r"(qa), "+r"(k));
         const uint64_t qd = sw128_desc(qa, 16, 1024), kd = sw128_desc(k, 16, 1024);
@@ -423,8 +462,10 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       }
       __syncwarp();
     };
-    auto weighted = [&](int w, uint32_t v, bool add) {
-      if (lane == 0) {
+    auto weighted = [&](int w, uint32_t v, bool add) -> bool {
+      if (!wait(sb + M::PREADY + 8 * w, p_n[w]++)) return false;
+      tc_fence_after();
+      if (elect()) {
         uint32_t p = tmem + w * 128;
         asm volatile("" : "+r"(p), "+r"(v));
         const uint64_t vd = sw128_desc(v, M::kRegion, 1024);
@@ -433,9 +474,10 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
           mma_ta(p + 256, p + 8 * s, vd + ((s * 2048) >> 4), ID_O, add || s > 0);
       }
       __syncwarp();
+      return true;
     };
     auto commit = [&](uint32_t bar) {
-      if (lane == 0) mma_commit(bar);
+      if (elect()) mma_commit(bar);
       __syncwarp();
     };
     auto tile = [&](uint32_t &at, uint32_t &free) -> bool {  // the next one in the ring
@@ -446,7 +488,6 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       if (++stage == M::kStages) stage = 0;
       return ok;
     };
-    auto turn = [&](int w) { return wait(sb + M::PREADY + 8 * w, p_n[w]++); };
     auto run = [&]() {
       for (;;) {
         const uint32_t s = taken % kItems;
@@ -483,9 +524,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
             if (j == zero_tile) clear(v);
             if (more && !tile(k, k_free)) return;
             for (int w = 0; w < 2; ++w) {
-              if (!turn(w)) return;
-              tc_fence_after();
-              weighted(w, v, j > 0);
+              if (!weighted(w, v, j > 0)) return;
               if (w == 1) commit(v_free);
               if (more) scores(w, w, k);
               else commit(sb + M::OFULL + 8 * w);
@@ -503,9 +542,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
             const bool more = j + 2 < n;
             if (!tile(v, v_free)) return;
             if (j == zero_tile) clear(v);
-            if (!turn(w)) return;
-            tc_fence_after();
-            weighted(w, v, j > 1);
+            if (!weighted(w, v, j > 1)) return;
             commit(v_free);
             if (more) {
               if (!tile(k, k_free)) return;
@@ -530,36 +567,158 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
     const uint32_t ts = tmem + w * 128 + lanes, to = tmem + 256 + w * 128 + lanes;
     float2 *const stats = reinterpret_cast<float2 *>(smem + M::STAT);
     uint32_t taken = 0, s_n = 0, o_n = 0, m_n = 0;
+    auto next_item = [&](Item &it) -> bool {
+      const uint32_t is = taken % kItems;
+      if (!wait(sb + M::IFULL + 8 * is, taken / kItems)) return false;
+      it = items[is];
+      arrive(sb + M::IEMPTY + 8 * is);
+      ++taken;
+      return true;
+    };
+    auto has_q = [&](const Item &it) { return it.rows > 128 || (w == 0 && it.rows >= 0); };
+    // Q of an item, on its way while the last one's sums are still being made: 16 bytes a thread, eight
+    // rows (16 where D = 64) at once
+    auto fetch_q = [&](const Item &it) -> bool {
+      if (w == 1 && !wait(sb + M::MEMPTY, m_n + 1)) return false;  // the second tile's place is shared
+      constexpr int kAcross = D / 8, kAtOnce = 128 / kAcross;
+      const int c = (tid & 127) % kAcross, row_of = it.rows > 128 ? w * 128 : 0;
+      const uint32_t col = sb + M::Q + w * M::kTileBytes + (c >> 3) * M::kRegion;
+      const kda_bf16 *const q = a.q + static_cast<int64_t>(it.token0) * a.ldq + static_cast<int64_t>(it.head) * a.G * D + c * 8;
+      const int i0 = (tid & 127) / kAcross, step_t = kAtOnce / a.G, step_g = kAtOnce - step_t * a.G;
+      int t = (it.row0 + row_of + i0) / a.G, g = it.row0 + row_of + i0 - t * a.G;
+#pragma unroll 4
+      for (int i = i0; i < 128; i += kAtOnce) {
+        if (row_of + i < it.rows) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(col + i * 128 + (((c & 7) ^ (i & 7)) << 4)),
+                       "l"(__cvta_generic_to_global(q + t * a.ldq + g * D)) : "memory");
+        }
+        t += step_t;
+        if ((g += step_g) >= a.G) {
+          g -= a.G;
+          ++t;
+        }
+      }
+      return true;
+    };
+    auto give_q = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async();
+      arrive(sb + M::QREADY + 8 * w);
+    };
+    // Writes o, or m, l and the sums of a part.
+    auto results = [&](const Item &it, float m, float l) -> bool {
+      const bool both = it.rows > 128;
+      const int row_of = both ? w * 128 : 0, row = it.row0 + row_of + r, tok = row / a.G;
+      const bool live = row_of + quad * 32 < it.rows, valid = row_of + r < it.rows;
+      float *const part = it.part < 0 ? nullptr
+                                      : reinterpret_cast<float *>(a.ws + kCutBytes + kStatBytes) +
+                                            (static_cast<int64_t>(it.part) * kRows + row_of + r) * D;
+      kda_bf16 *const out = a.o + (static_cast<int64_t>(it.token0) + tok) * a.ldo +
+                            (static_cast<int64_t>(it.head) * a.G + (row - tok * a.G)) * D;
+      auto put = [&](const float (&o)[32], int c, float f) {  // columns [32 c, 32 c + 32) of this row
+        if (!valid) return;
+        if (part) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4 *>(part + 32 * c + 4 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = pack(o[8 * i + 2 * e] * f, o[8 * i + 2 * e + 1] * f);
+            *reinterpret_cast<uint4 *>(out + 32 * c + 8 * i) = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+        }
+      };
+      auto put_stats = [&]() {
+        if (part && valid)
+          reinterpret_cast<float2 *>(a.ws + kCutBytes)[static_cast<int64_t>(it.part) * kRows + row_of + r] = make_float2(m, l);
+      };
+      if (both || it.n == 1) {
+        const float f = l == 0.f ? 0.f : 1.f / l;
+        if (live) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            tmem_ld32(to + 32 * c, o);
+            tmem_wait_ld();
+            put(o, c, f);
+          }
+          put_stats();
+        }
+        tc_fence_before();
+        return true;
+      }
+      // two chains of the same rows: the second one's sums come through shared memory, 64 columns at a
+      // time, 16-byte words of a row XORed with the row
+      float mine = 1.f, other = 0.f, inv = 0.f;
+#pragma unroll
+      for (int half = 0; half < D / 64; ++half) {
+        const uint32_t at = sb + M::MERGE + r * 256;
+        if (w == 1) {
+          if (!wait(sb + M::MEMPTY, m_n + 1)) return false;
+          ++m_n;
+          if (live) {
+            if (half == 0) stats[r] = make_float2(m, l);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float o[32];
+              tmem_ld32(to + 64 * half + 32 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((c * 8 + i) ^ (r & 15)) << 4)), "f"(o[4 * i]), "f"(o[4 * i + 1]), "f"(o[4 * i + 2]), "f"(o[4 * i + 3]) : "memory");
+            }
+          }
+          arrive(sb + M::MFULL);
+        } else {
+          if (!wait(sb + M::MFULL, m_n)) return false;
+          ++m_n;
+          if (live) {
+            if (half == 0) {
+              const float2 t = stats[r];
+              const float top = fmaxf(m, t.x), base = top == -INFINITY ? 0.f : top;
+              mine = ex2(m - base);
+              other = ex2(t.x - base);
+              l = l * mine + t.y * other;
+              m = top;
+              inv = l == 0.f ? 0.f : 1.f / l;
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float o[32];
+              tmem_ld32(to + 64 * half + 32 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float x[4];
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(at + (((c * 8 + i) ^ (r & 15)) << 4)) : "memory");
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[4 * i + e] = o[4 * i + e] * mine + x[e] * other;
+              }
+              put(o, 2 * half + c, inv);
+            }
+            if (half == 0) put_stats();
+          }
+          arrive(sb + M::MEMPTY);
+        }
+      }
+      tc_fence_before();
+      return true;
+    };
     auto run = [&]() {
-      for (;;) {
-        const uint32_t is = taken % kItems;
-        if (!wait(sb + M::IFULL + 8 * is, taken / kItems)) return;
-        const Item it = items[is];
-        arrive(sb + M::IEMPTY + 8 * is);
-        ++taken;
-        if (it.rows < 0) return;
+      Item it;
+      if (!next_item(it)) return;
+      if (has_q(it)) {
+        if (!fetch_q(it)) return;
+        give_q();
+      }
+      for (Item next; it.rows >= 0; it = next) {
         const bool both = it.rows > 128;
         const int steps = both ? it.n : (it.n + 1 - w) >> 1;
         const int row_of = both ? w * 128 : 0;  // of the tile, in the item
         const bool live = row_of + quad * 32 < it.rows, valid = row_of + r < it.rows;
-        if (both || w == 0) {
-          // Q: 16 bytes a thread, eight rows (16 where D = 64) at once; the MMAs of the last item are done
-          if (w == 1 && !wait(sb + M::MEMPTY, m_n + 1)) return;  // the second tile's place is shared
-          constexpr int kAcross = D / 8, kAtOnce = 128 / kAcross;
-          const int c = (tid & 127) % kAcross;
-          const uint32_t col = sb + M::Q + w * M::kTileBytes + (c >> 3) * M::kRegion;
-#pragma unroll 4
-          for (int i = (tid & 127) / kAcross; i < 128; i += kAtOnce) {
-            const int row = it.row0 + row_of + i;
-            if (row_of + i < it.rows) {
-              const int t = row / a.G, g = row - t * a.G;
-              const uint4 x = *reinterpret_cast<const uint4 *>(a.q + (static_cast<int64_t>(it.token0) + t) * a.ldq + (static_cast<int64_t>(it.head) * a.G + g) * D + c * 8);
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(col + i * 128 + (((c & 7) ^ (i & 7)) << 4)), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
-            }
-          }
-          fence_proxy_async();
-          arrive(sb + M::QREADY + 8 * w);
-        }
         const int row = it.row0 + row_of + r, tok = row / a.G;
         // the positions that the row sees: [see0, see1)
         const int see1 = it.before + tok + 1, see0 = a.window ? max(see1 - a.window, 0) : 0;
@@ -630,105 +789,25 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
           }
           arrive(sb + M::PREADY + 8 * w);
         }
-        if (steps == 0) continue;
-        if (!wait(sb + M::OFULL + 8 * w, o_n++)) return;
-        tc_fence_after();
-
-        float *const part = it.part < 0 ? nullptr
-                                        : reinterpret_cast<float *>(a.ws + kCutBytes + kStatBytes) +
-                                              (static_cast<int64_t>(it.part) * kRows + row_of + r) * D;
-        kda_bf16 *const out = a.o + (static_cast<int64_t>(it.token0) + tok) * a.ldo +
-                              (static_cast<int64_t>(it.head) * a.G + (row - tok * a.G)) * D;
-        auto put = [&](const float (&o)[32], int c, float f) {  // columns [32 c, 32 c + 32) of this row
-          if (!valid) return;
-          if (part) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float4 *>(part + 32 * c + 4 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t x[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] = pack(o[8 * i + 2 * e] * f, o[8 * i + 2 * e + 1] * f);
-              *reinterpret_cast<uint4 *>(out + 32 * c + 8 * i) = make_uint4(x[0], x[1], x[2], x[3]);
-            }
-          }
-        };
-        auto put_stats = [&]() {
-          if (part && valid)
-            reinterpret_cast<float2 *>(a.ws + kCutBytes)[static_cast<int64_t>(it.part) * kRows + row_of + r] = make_float2(m, l);
-        };
-        if (both || it.n == 1) {
-          const float f = l == 0.f ? 0.f : 1.f / l;
-          if (live) {
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              float o[32];
-              tmem_ld32(to + 32 * c, o);
-              tmem_wait_ld();
-              put(o, c, f);
-            }
-            put_stats();
-          }
-          tc_fence_before();
-          continue;
+        // The next item's Q.  With 128 rows of its own the warpgroup has seen the last scores of this one;
+        // else the other's may still be on their way, and are not when its last sum is there.  The second
+        // tile's place takes sums below.
+        if (!next_item(next)) return;
+        const bool q = has_q(next), q_later = q && !both && w == 1;
+        if (q && both && !fetch_q(next)) return;
+        if (steps > 0) {
+          if (!wait(sb + M::OFULL + 8 * w, o_n++)) return;
+          tc_fence_after();
         }
-        // two chains of the same rows: the second one's sums come through shared memory, 64 columns at a
-        // time, 16-byte words of a row XORed with the row
-        float mine = 1.f, other = 0.f, inv = 0.f;
-#pragma unroll
-        for (int half = 0; half < D / 64; ++half) {
-          const uint32_t at = sb + M::MERGE + r * 256;
-          if (w == 1) {
-            if (!wait(sb + M::MEMPTY, m_n + 1)) return;
-            ++m_n;
-            if (live) {
-              if (half == 0) stats[r] = make_float2(m, l);
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                float o[32];
-                tmem_ld32(to + 64 * half + 32 * c, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((c * 8 + i) ^ (r & 15)) << 4)), "f"(o[4 * i]), "f"(o[4 * i + 1]), "f"(o[4 * i + 2]), "f"(o[4 * i + 3]) : "memory");
-              }
-            }
-            arrive(sb + M::MFULL);
-          } else {
-            if (!wait(sb + M::MFULL, m_n)) return;
-            ++m_n;
-            if (live) {
-              if (half == 0) {
-                const float2 t = stats[r];
-                const float top = fmaxf(m, t.x), base = top == -INFINITY ? 0.f : top;
-                mine = ex2(m - base);
-                other = ex2(t.x - base);
-                l = l * mine + t.y * other;
-                m = top;
-                inv = l == 0.f ? 0.f : 1.f / l;
-              }
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                float o[32];
-                tmem_ld32(to + 64 * half + 32 * c, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  float x[4];
-                  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(at + (((c * 8 + i) ^ (r & 15)) << 4)) : "memory");
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) o[4 * i + e] = o[4 * i + e] * mine + x[e] * other;
-                }
-                put(o, 2 * half + c, inv);
-              }
-              if (half == 0) put_stats();
-            }
-            arrive(sb + M::MEMPTY);
-          }
+        if (q && !q_later) {
+          if (!both && !fetch_q(next)) return;
+          give_q();
         }
-        tc_fence_before();
+        if (steps > 0 && !results(it, m, l)) return;
+        if (q_later) {
+          if (!fetch_q(next)) return;
+          give_q();
+        }
       }
     };
     run();

@@ -15,7 +15,7 @@ namespace attn {
 
 constexpr int kRows = 256;     // rows (token, head of the group) of an item, two tiles of 128
 constexpr int kTile = 128;     // positions of a tile of keys
-constexpr int kItemUnits = 1;  // what an item costs beside its tiles, in tiles
+constexpr int kItemUnits = 5;  // what an item costs beside its tiles, in tiles
 constexpr int kCtas = 152;     // one on each SM
 constexpr int kLeastUnits = 4;
 
@@ -57,7 +57,8 @@ struct Run {
   KDA_HD int64_t units_before(int i) const {
     const int n = items();
     const int64_t k = i < n ? i : n - 1;
-    if (n == 0) return 0;
+    if (n == 0 || i == 0) return 0;
+    if (n == 1) return kItemUnits + end(0) - first(0);
     int64_t sum = k * kItemUnits + floor_sum(k, G, (static_cast<int64_t>(G) * (before + kTile) + kRows - 1) / kTile);
     if (window) {
       const int64_t b = floor_div(static_cast<int64_t>(G) * (before - window + 1), kTile), skip = b < 0 ? (1 - b) / 2 : 0;

@@ -459,7 +459,7 @@ int kda_verify_draft(const void *target, const void *draft, int prob_bytes, int 
  *           by setting its length to 0, and what a row holds behind its length
  *           is not looked at.
  * page in {16, 32, 64, 128}, D in {64, 128}; n_pages and max_pages at most 2^20,
- * n_slots at most 2^14 where pages are given out, shared or moved.
+ * n_slots at most 2^13 where pages are given out, shared or moved.
  *
  * Run b of a batch belongs to slot slots[b] (NULL: slot b), and its tokens
  * follow the lens[slot] tokens of that slot: token j stands at position

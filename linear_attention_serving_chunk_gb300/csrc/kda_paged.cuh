@@ -68,8 +68,7 @@ struct PagesArgs {
 };
 
 // The moves that the planning kernel leaves for the copying one, in int32 words: how many, then
-// ws_n sources, ws_n destinations, and ws_n of the fork's tokens in each page or of the
-// compaction's new page numbers, and the fork's fresh pages.
+// ws_n sources, ws_n destinations, and of a fork the tokens in each page and the fresh pages.
 constexpr int kPagesWsHead = 4;
 constexpr int kPagesWsArrays = 4;
 __host__ __device__ constexpr int64_t pages_ws_bytes(int64_t n) {
@@ -77,7 +76,7 @@ __host__ __device__ constexpr int64_t pages_ws_bytes(int64_t n) {
 }
 
 constexpr int kMaxPages = 1 << 20;  // of a pool, and of a row of the table
-constexpr int kMaxSlots = 1 << 14;
+constexpr int kMaxSlots = 1 << 13;
 
 size_t attn_workspace(int D);
 cudaError_t attn_launch(const AttnCall &c, int D, cudaStream_t st);

@@ -5,18 +5,20 @@
 // by its length alone and shared pages need no care.  One planning kernel does that and what
 // follows from it; a second one moves what the plan says.
 //
-// Planning.  One cluster of 8 CTAs, so that nothing passes through global memory and no launch
-// follows another:
-//   1. mark: a warp takes a row and sets a bit for each of its pages, in a bitmap of its CTA's
-//      shared memory (OR in any order gives the same bits; 128 KB for the largest pool, 2^20);
-//   2. each CTA ORs an eighth of the eight bitmaps, counts the bits that are not set, and learns
-//      from the others' counts the rank of its first unused page;
-//   3. grow: the k-th unused page goes to the row whose demand covers rank k, found by bisection in
-//      the prefix sums of the demands; fork: it goes to the k-th fork with a partial last page;
-//      compact: with u pages in use, the k-th unused page below u takes the k-th used page from u on.
-// What bounds it: the latency of a dozen dependent steps and five cluster barriers, and for large
-// tables the loads of step 1, which 256 warps have in flight at once.  One CTA marks 512 rows of
-// 500 entries eight times slower, and the whole GPU would need a grid-wide barrier.
+// Planning.  One cluster of 8 CTAs, so that little passes through global memory and no launch follows
+// another:
+//   1. mark: a warp takes 256 entries of a row, by prefix sums over the rows' entries, so that long rows are
+//      no one's alone, and sets a bit for each page in a bitmap of its CTA's shared memory (OR in any
+//      order gives the same bits; 128 KB for the largest pool, 2^20);
+//   2. each CTA ORs an eighth of the eight bitmaps, four words a thread, and leaves the words and how many
+//      unused pages of its share lie before each;
+//   3. a warp takes a word and a lane a page: from the word and the counts, read where they lie, follows
+//      the page's rank among the unused (or the used) ones.  grow: the k-th unused page goes to the row
+//      whose demand covers rank k, found by bisection in the prefix sums of the demands; fork: to the k-th
+//      fork with a partial last page; compact: with u pages in use, the k-th unused page below u takes
+//      the k-th used page from u on.
+// What bounds it: the latency of a dozen dependent steps and three or four cluster barriers (1100 cycles
+// each), and for large tables the loads of step 1, which 256 warps have in flight at once.
 //
 // Moving.  A warp takes 4 KB pieces of (page, layer, K or V of a head), eight 16-byte loads in
 // flight a lane; sources and destinations are disjoint, so pieces need no order.  Bound by memory.
@@ -50,6 +52,18 @@ __device__ __forceinline__ uint32_t remote(const void *p, unsigned rank) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(there) : "memory");
   return v;
 }
+__device__ __forceinline__ uint4 remote4(const void *p, unsigned rank) {
+  uint32_t there;
+  uint4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(there)
+               : "r"(sm100::smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(there)
+               : "memory");
+  return v;
+}
 
 // Sum of v over the threads before this one and, in `total`, over all of the block.
 __device__ __forceinline__ int block_scan(int v, int &total) {
@@ -75,9 +89,12 @@ __device__ __forceinline__ int block_scan(int v, int &total) {
   return before + x - v;
 }
 
+constexpr int kPiece32 = 256;  // entries of the table that a warp takes at once, eight a lane
+
 struct Plan {
   const PagesArgs &a;
-  int *rows;  // shared: grow, the prefix sums of the demands; fork, the fork that takes each row
+  int *pieces;  // shared: the prefix sums of the rows' entries in use, in pieces
+  int *rows;    // shared: grow, the prefix sums of the demands; fork, the fork that takes each row
 
   // Pages of `tokens` tokens, or -1 where the table's row cannot hold them.
   __device__ int pages_of(int tokens) const {
@@ -96,21 +113,32 @@ struct Plan {
   __device__ int fork_tail(int i) const { return a.lens[a.src[i]] & ((1 << a.page_shift) - 1); }
 };
 
+// Words of the bitmap that one CTA counts, and of the whole: a multiple of what a thread takes.
+__host__ __device__ constexpr int share_of(int n_pages) {
+  return ((n_pages + 31) / 32 + 4 * kPRanks - 1) / (4 * kPRanks) * 4;
+}
+
 template <PagesOp OP>
 __global__ void __launch_bounds__(kPThreads, 1) pages_plan_kernel(const PagesArgs a) {
-  extern __shared__ uint32_t bits[];
+  extern __shared__ __align__(16) uint32_t bits[];
   __shared__ int s_total;
+  __shared__ int s_rank[kPThreads];  // fork: of the fresh page; -1: needs none, -2: not made
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_rank());
-  const int words = (a.n_pages + 31) / 32, share = (words + kPRanks - 1) / kPRanks;
-  const Plan plan{a, reinterpret_cast<int *>(bits + words)};
-  int *const rows = plan.rows;
+  const int share = share_of(a.n_pages), words = share * kPRanks;
+  int *const counts = reinterpret_cast<int *>(bits + words);  // unused pages of the share before each word
+  const Plan plan{a, counts + share, counts + share + a.n_slots};
+  int *const pieces = plan.pieces, *const rows = plan.rows;
+  const int wid = warp * kPRanks + rank, all_warps = kPRanks * 32;
   int bad = 0;
   if (OP != kPagesGrow) grid_launch_dependents();
 
-  // 1. marks
-  for (int w = tid; w < words; w += kPThreads)
-    bits[w] = w == words - 1 && (a.n_pages & 31) ? ~0u << (a.n_pages & 31) : 0u;
+  // 1. marks; pages that there are not are in use
+  for (int w = tid; w < words; w += kPThreads) {
+    const int n = a.n_pages - w * 32;
+    bits[w] = n >= 32 ? 0u : n <= 0 ? ~0u : ~0u << n;
+  }
+  int want = 0;  // fork: those with a partial last page
   if (OP == kPagesFork) {
     for (int b = tid; b < a.n_slots; b += kPThreads) rows[b] = kNone;
     __syncthreads();
@@ -118,112 +146,176 @@ __global__ void __launch_bounds__(kPThreads, 1) pages_plan_kernel(const PagesArg
       if (plan.fork_in_range(i)) atomicMin(&rows[a.dst[i]], i);
   }
   __syncthreads();
-  for (int b = rank * 32 + warp; b < a.n_slots; b += kPRanks * 32) {
-    if (OP == kPagesFork && rows[b] != kNone && plan.fork_made(rows[b])) continue;
-    const int need = plan.pages_of(a.lens[b]);
-    if (need < 0) bad = 1;
-    const int32_t *row = a.table + static_cast<int64_t>(b) * a.max_pages;
-    for (int i = lane; i < need; i += 32 * 8) {
-      int p[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) p[j] = i + 32 * j < need ? row[i + 32 * j] : kNone;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (p[j] >= 0 && p[j] < a.n_pages)
-          atomicOr(&bits[p[j] >> 5], 1u << (p[j] & 31));
-        else if (p[j] != kNone || i + 32 * j < need)
-          bad = 1;
+  // The entries in use of each row, and what grow's rows want, by all CTAs alike.
+  int n_pieces = 0;
+  int64_t demand = 0;
+  for (int b0 = 0; b0 < a.n_slots; b0 += kPThreads) {
+    const int b = b0 + tid;
+    int have = 0, more = 0, all;
+    if (b < a.n_slots && !(OP == kPagesFork && rows[b] != kNone && plan.fork_made(rows[b]))) {
+      have = plan.pages_of(a.lens[b]);
+      if (OP == kPagesGrow) {
+        const int need = plan.pages_of(a.want[b]);
+        if (need < 0) bad = 1;
+        if (have >= 0 && need > have) more = need - have;
       }
+      if (have < 0) {
+        have = 0;
+        bad = 1;
+      }
+    }
+    const int mine = (have + kPiece32 - 1) / kPiece32, before = block_scan(mine, all);
+    if (b < a.n_slots) pieces[b] = n_pieces + before + mine;
+    n_pieces += all;
+    if (OP == kPagesGrow) {
+      const int wanted = block_scan(more, all);
+      if (b < a.n_slots) rows[b] = static_cast<int>(min(demand + wanted + more, int64_t(1) << 30));
+      demand += all;
+    }
+  }
+  __syncthreads();
+  for (int x = wid; x < n_pieces; x += all_warps) {
+    int b = 0;
+    for (int hi = a.n_slots, step = hi; step > 1;) {  // the row of piece x, 32 ways at a time
+      step = (hi - b + 31) / 32;
+      const int f = __ffs(__ballot_sync(0xffffffffu, pieces[min(b + (lane + 1) * step, hi) - 1] > x)) - 1;
+      b += f * step;
+      hi = min(hi, b + step);
+    }
+    const int need = plan.pages_of(a.lens[b]), i0 = (x - (b ? pieces[b - 1] : 0)) * kPiece32 + lane;
+    const int32_t *row = a.table + static_cast<int64_t>(b) * a.max_pages;
+    int p[kPiece32 / 32];
+#pragma unroll
+    for (int j = 0; j < kPiece32 / 32; ++j) p[j] = i0 + 32 * j < need ? row[i0 + 32 * j] : 0;
+#pragma unroll
+    for (int j = 0; j < kPiece32 / 32; ++j) {
+      if (i0 + 32 * j >= need) continue;
+      if (p[j] >= 0 && p[j] < a.n_pages) atomicOr(&bits[p[j] >> 5], 1u << (p[j] & 31));
+      else bad = 1;
     }
   }
 
-  // 2. this CTA's share of all marks, and the unused pages before it
+  // Forks i0 ..: their ranks in s_rank, `before` and what they want themselves in front of the next ones.
+  auto fork_ranks = [&](int i0, int before) {
+    const int i = i0 + tid;
+    const bool made = i < a.m && plan.fork_made(i), tail = made && plan.fork_tail(i);
+    int all;
+    const int at = block_scan(tail, all);
+    s_rank[tid] = tail ? before + at : made ? -1 : -2;
+    if (i < a.m && !made) bad = 1;
+    __syncthreads();
+    return all;
+  };
+  if (OP == kPagesFork)
+    for (int i0 = 0; i0 < a.m; i0 += kPThreads) want += fork_ranks(i0, want);
+
+  // 2. this CTA's share of all marks, and the unused pages before each word
   cluster_sync();
-  const int each = (share + kPThreads - 1) / kPThreads;  // words of a thread, one after another
-  const int w0 = min(rank * share + tid * each, words), w1 = min(min(w0 + each, (rank + 1) * share), words);
-  int unused = 0;
-  for (int w = w0; w < w1; ++w) {
-    uint32_t v = 0;
+  {
+    const int w = rank * share + 4 * tid;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    const bool some = 4 * tid < share;
+    if (some) {
 #pragma unroll
-    for (unsigned q = 0; q < kPRanks; ++q) v |= remote(bits + w, q);
-    bits[w] = v;  // (nobody else reads this CTA's share of this CTA's bitmap)
-    unused += 32 - __popc(v);
+      for (unsigned q = 0; q < kPRanks; ++q) {
+        const uint4 x = remote4(bits + w, q);
+        v.x |= x.x, v.y |= x.y, v.z |= x.z, v.w |= x.w;
+      }
+      // (nobody else reads this CTA's share of this CTA's bitmap before the barrier)
+      *reinterpret_cast<uint4 *>(bits + w) = v;
+    }
+    const int x = __popc(~v.x), y = __popc(~v.y), z = __popc(~v.z);
+    int total;
+    const int first = block_scan(some ? x + y + z + __popc(~v.w) : 0, total);
+    if (some) *reinterpret_cast<int4 *>(counts + 4 * tid) = make_int4(first, first + x, first + x + y, first + x + y + z);
+    if (tid == 0) s_total = total;
   }
-  int total, first = block_scan(unused, total);
-  if (tid == 0) s_total = total;
   cluster_sync();
-  int left = 0;
+  int base[kPRanks], left = 0;  // unused pages in front of each share, and all
 #pragma unroll
   for (int q = 0; q < kPRanks; ++q) {
-    const int n = static_cast<int>(remote(&s_total, q));
-    if (q < rank) first += n;
-    left += n;
+    base[q] = left;
+    left += static_cast<int>(remote(&s_total, q));
   }
+  // A word of the marks, and the unused pages before it.
+  auto word = [&](int w, int &before) -> uint32_t {
+    const int q = w / share;
+    before = static_cast<int>(remote(counts + (w - q * share), q));
+#pragma unroll
+    for (int r = 1; r < kPRanks; ++r)
+      if (r == q) before += base[r];
+    return remote(bits + w, q);
+  };
+  // Calls each(page, whether it is unused, unused pages before it) for a lane's pages, in ascending order,
+  // until a word has `end` unused pages before it.  A warp has eight words in a row, and reads those of four
+  // rounds at once, one in each lane: lanes that ask for the same remote word are served one after another.
+  auto each_page = [&](int end, auto &&each) {
+    for (int w0 = wid * 8; w0 < words; w0 += 32 * all_warps) {
+      int k = end;
+      const int mine = w0 + (lane / 8) * 8 * all_warps + lane % 8;
+      const uint32_t v = mine < words ? ~word(mine, k) : 0u;
+      for (int s = 0; s < 32; ++s) {
+        const uint32_t u = __shfl_sync(0xffffffffu, v, s);
+        const int before = __shfl_sync(0xffffffffu, k, s), w = __shfl_sync(0xffffffffu, mine, s);
+        if (before >= end) {
+          if (s % 8 == 0) return;  // (so have the words of later rounds)
+          s |= 7;
+          continue;
+        }
+        each(w * 32 + lane, u >> lane & 1, before + __popc(u & ((1u << lane) - 1)));
+      }
+    }
+  };
 
   if (OP == kPagesGrow) {
-    int64_t carry = 0;
-    for (int b0 = 0; b0 < a.n_slots; b0 += kPThreads) {
-      const int b = b0 + tid;
-      int more = 0;
-      if (b < a.n_slots) {
-        const int have = plan.pages_of(a.lens[b]), want = plan.pages_of(a.want[b]);
-        if (want < 0) bad = 1;
-        if (have >= 0 && want > have) more = want - have;
-      }
-      int all, before = block_scan(more, all);
-      if (b < a.n_slots) rows[b] = static_cast<int>(min(carry + before + more, int64_t(1) << 30));
-      carry += all;
-    }
-    __syncthreads();
-    const int n = a.n_slots;
-    for (int w = w0; w < w1; ++w)
-      for (uint32_t v = ~bits[w]; v; v &= v - 1, ++first) {
-        if (n == 0 || first >= rows[n - 1]) break;
+    const int n = a.n_slots, given = n ? rows[n - 1] : 0;
+    int begin = 0, end = 0;  // the ranks that the row of the warp's last page takes, and where
+    int32_t *to = nullptr;
+    each_page(given, [&](int p, bool unused, int k) {
+      const bool mine = unused && k < given;
+      if (__any_sync(0xffffffffu, mine && k >= end)) {
         int lo = 0, hi = n - 1;  // the first row whose demands end behind this rank
         while (lo < hi) {
           const int mid = (lo + hi) / 2;
-          if (rows[mid] > first) hi = mid;
+          if (rows[mid] > k) hi = mid;
           else lo = mid + 1;
         }
-        if (rows[lo] <= left)
-          a.table[static_cast<int64_t>(lo) * a.max_pages + plan.pages_of(a.lens[lo]) + first -
-                  (lo ? rows[lo - 1] : 0)] = w * 32 + __ffs(v) - 1;
+        begin = lo ? rows[lo - 1] : 0;
+        end = rows[lo];
+        to = a.table + static_cast<int64_t>(lo) * a.max_pages + plan.pages_of(a.lens[lo]);
       }
-    for (int b = rank * 32 + warp; b < n; b += kPRanks * 32) {
-      if (rows[b] <= left) continue;  // all of its pages, or none
-      const int have = plan.pages_of(a.lens[b]), want = plan.pages_of(a.want[b]);
-      if (have < 0) continue;
-      for (int i = have + lane; i < want; i += 32)
-        a.table[static_cast<int64_t>(b) * a.max_pages + i] = -1;
-    }
+      if (mine && end <= left) to[k - begin] = p;
+      // ranks only rise: the last lane's row is where the next word goes on
+      begin = __shfl_sync(0xffffffffu, begin, 31);
+      end = __shfl_sync(0xffffffffu, end, 31);
+      to = reinterpret_cast<int32_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), 31));
+    });
+    if (given > left)  // a row gets all of its pages or none
+      for (int b = wid; b < n; b += all_warps) {
+        if (rows[b] <= left) continue;
+        const int have = plan.pages_of(a.lens[b]), need = plan.pages_of(a.want[b]);
+        if (have < 0) continue;
+        for (int i = have + lane; i < need; i += 32)
+          a.table[static_cast<int64_t>(b) * a.max_pages + i] = -1;
+      }
     if (rank == 0 && tid == 0)
-      *a.count = static_cast<int>(max(left - carry, -static_cast<int64_t>(kNone)));
+      *a.count = static_cast<int>(max(left - demand, -static_cast<int64_t>(kNone)));
   }
 
   if (OP == kPagesFork) {
     int32_t *src = a.ws + kPagesWsHead, *dst = src + a.ws_n, *len = dst + a.ws_n,
             *fresh = len + a.ws_n;
-    int want = 0;  // forks with a partial last page
-    for (int i0 = 0; i0 < a.m; i0 += kPThreads) {
-      const int i = i0 + tid;
-      want += __syncthreads_count(i < a.m && plan.fork_made(i) && plan.fork_tail(i));
-    }
-    for (int w = w0; w < w1; ++w)
-      for (uint32_t v = ~bits[w]; v && first < want; v &= v - 1, ++first)
-        fresh[first] = w * 32 + __ffs(v) - 1;
+    each_page(want, [&](int p, bool unused, int k) {
+      if (unused && k < want) fresh[k] = p;
+    });
     cluster_sync();
-    __shared__ int s_rank[kPThreads];  // of the fork's fresh page; -1: needs none, -2: not made
     int before = 0;
     for (int i0 = 0; i0 < a.m; i0 += kPThreads) {
-      const int i = i0 + tid;
-      const bool made = i < a.m && plan.fork_made(i), tail = made && plan.fork_tail(i);
-      int all;
-      const int at = block_scan(tail, all);
-      s_rank[tid] = tail ? before + at : made ? -1 : -2;
-      if (i < a.m && !made) bad = 1;
-      before += all;
-      __syncthreads();
-      for (int j = rank * 32 + warp; j < min(kPThreads, a.m - i0); j += kPRanks * 32) {
+      if (a.m > kPThreads) before += fork_ranks(i0, before);  // (else they are there)
+      const int across = max((a.max_pages + kPiece32 - 1) / kPiece32, 1);
+      const int64_t all = static_cast<int64_t>(min(kPThreads, a.m - i0)) * across;
+      for (int64_t x = wid; x < all; x += all_warps) {
+        const int j = static_cast<int>(x / across), e0 = static_cast<int>(x - static_cast<int64_t>(j) * across) * kPiece32 + lane;
         const int r = s_rank[j];
         if (r == -2) continue;
         const int s = a.src[i0 + j], d = a.dst[i0 + j], tokens = a.lens[s];
@@ -231,17 +323,15 @@ __global__ void __launch_bounds__(kPThreads, 1) pages_plan_kernel(const PagesArg
         int32_t *to = a.table + static_cast<int64_t>(d) * a.max_pages;
         const bool none = r >= left;  // no page is left for it: an empty row
         const int need = none ? 0 : plan.pages_of(tokens);
-        const int whole = need - (r >= 0 && !none);
-        for (int e = lane; e < a.max_pages; e += 32) {
-          if (e < whole) to[e] = from[e];
-          else if (e >= need) to[e] = -1;
-        }
-        if (lane == 0) {
+        const int whole = need - (r >= 0 && !none), page = whole < need ? __ldcg(fresh + r) : -1;
+#pragma unroll
+        for (int e = e0; e < e0 + kPiece32; e += 32)
+          if (e < a.max_pages) to[e] = e < whole ? from[e] : e < need ? page : -1;
+        if (e0 == 0) {
           a.lens[d] = none ? 0 : tokens;
           if (whole < need) {
-            const int old = from[whole], page = __ldcg(fresh + r);
+            const int old = from[whole];
             const bool ok = old >= 0 && old < a.n_pages;
-            to[whole] = page;
             src[r] = ok ? old : -1;
             dst[r] = page;
             len[r] = plan.fork_tail(i0 + j);
@@ -258,57 +348,43 @@ __global__ void __launch_bounds__(kPThreads, 1) pages_plan_kernel(const PagesArg
   }
 
   if (OP == kPagesCompact) {
-    int32_t *src = a.ws + kPagesWsHead, *dst = src + a.ws_n, *now = dst + a.ws_n;
+    int32_t *src = a.ws + kPagesWsHead, *dst = src + a.ws_n;
     const int used = a.n_pages - left;
-    // rank of an unused page: those before it; of a used one from `used` on: the used ones before
-    // it, less the used ones below `used`, which are as many as the unused ones from there on
-    // fewer than `left`.  Holes are the unused pages below `used`.
-    __shared__ int s_below;  // unused pages below `used`, in this CTA's share
-    if (tid == 0) s_below = 0;
-    __syncthreads();
-    int below = 0;
-    for (int w = w0; w < w1; ++w) {
-      const int n = used - w * 32;  // pages of this word below `used`
-      if (n > 0) below += __popc(~bits[w] & (n >= 32 ? ~0u : (1u << n) - 1));
+    // the unused pages below `used`: as many as used ones lie from there on
+    int holes = left;
+    if (used < a.n_pages) {
+      const uint32_t v = ~word(used / 32, holes);
+      holes += __popc(v & ((1u << (used % 32)) - 1));
     }
-    if (below) atomicAdd(&s_below, below);
-    cluster_sync();
-    int holes = 0;
-#pragma unroll
-    for (int q = 0; q < kPRanks; ++q) holes += static_cast<int>(remote(&s_below, q));
-    // the used pages before this thread's words: the words' pages less the unused ones
-    int k = first, u = w0 * 32 - first - (used - holes);
-    for (int w = w0; w < w1; ++w)
-      for (int j = 0; j < 32; ++j) {
-        const int p = w * 32 + j;
-        if (p >= a.n_pages) break;
-        if (bits[w] >> j & 1) {
-          if (p >= used) src[u] = p;
-          ++u;
-        } else {
-          if (p < used) dst[k] = p;
-          ++k;
-        }
+    // rank of a used page among those from `used` on: the pages before it, less the unused ones and
+    // the used ones below `used`
+    each_page(kNone, [&](int p, bool unused, int k) {
+      if (unused) {
+        if (p < used) dst[k] = p;
+      } else if (p >= used && p < a.n_pages) {
+        src[p - k - (used - holes)] = p;
       }
+    });
     cluster_sync();
-    u = w0 * 32 - first - (used - holes);
-    for (int w = w0; w < w1; ++w)
-      for (uint32_t v = bits[w]; v; v &= v - 1, ++u) {
-        const int p = w * 32 + __ffs(v) - 1;
-        if (p >= used && p < a.n_pages) now[p] = __ldcg(dst + u);
-      }
-    cluster_sync();
-    for (int b = rank * 32 + warp; b < a.n_slots; b += kPRanks * 32) {
+    const int across = (a.max_pages + kPiece32 - 1) / kPiece32;
+    const int64_t all = static_cast<int64_t>(a.n_slots) * across;
+    for (int64_t x = wid; x < all; x += all_warps) {
+      const int b = static_cast<int>(x / across), i0 = static_cast<int>(x - static_cast<int64_t>(b) * across) * kPiece32 + lane;
       const int need = plan.pages_of(a.lens[b]);
       const int32_t *row = a.table + static_cast<int64_t>(b) * a.max_pages;
       int32_t *out = a.table_out + static_cast<int64_t>(b) * a.max_pages;
-      for (int i = lane; i < a.max_pages; i += 32) {
-        int p = -1;
-        if (i < need) {
-          p = row[i];
-          if (p >= used && p < a.n_pages) p = __ldcg(now + p);
+      int p[kPiece32 / 32];
+#pragma unroll
+      for (int j = 0; j < kPiece32 / 32; ++j) p[j] = i0 + 32 * j < need ? row[i0 + 32 * j] : -1;
+#pragma unroll
+      for (int j = 0; j < kPiece32 / 32; ++j) {
+        if (p[j] >= used && p[j] < a.n_pages) {
+          int k;
+          const uint32_t v = ~word(p[j] / 32, k);
+          k += __popc(v & ((1u << (p[j] % 32)) - 1));
+          p[j] = __ldcg(dst + (p[j] - k - (used - holes)));
         }
-        out[i] = p;
+        if (i0 + 32 * j < a.max_pages) out[i0 + 32 * j] = p[j];
       }
     }
     if (rank == 0 && tid == 0) {
@@ -359,11 +435,11 @@ __global__ void __launch_bounds__(kMThreads) pages_move_kernel(const PagesArgs a
 
 template <PagesOp OP>
 cudaError_t plan(const PagesArgs &a, cudaStream_t st) {
-  const size_t bytes = 4 * (static_cast<size_t>(a.n_pages + 31) / 32 + (OP == kPagesCompact ? 0 : a.n_slots));
+  const size_t bytes = 4 * (static_cast<size_t>(share_of(a.n_pages)) * (kPRanks + 1) + (OP == kPagesCompact ? 1 : 2) * static_cast<size_t>(a.n_slots));
   if (bytes > 40 * 1024)  // (with the static arrays, more than any kernel gets unasked)
     if (cudaError_t e = cudaFuncSetAttribute(pages_plan_kernel<OP>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             4 * (kMaxPages / 32 + kMaxSlots)))
+                                             4 * (kMaxPages / 32 / kPRanks * (kPRanks + 1) + 2 * kMaxSlots)))
       return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kPRanks);

@@ -203,6 +203,8 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
     tmem_relinquish();
   }
 
+  grid_dependency_wait();
+
   // This CTA's share: all units, then the run in which the share begins.
   int64_t *const plan = reinterpret_cast<int64_t *>(smem + M::PLAN);
   bool bad = false;
@@ -235,7 +237,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
   auto found = [&](int b) {
     if (before <= start && start < before + mine) {
       plan[0] = before;
-      plan[1] = mine / a.H;
+      plan[1] = attn::quotient(mine, a.H);
       plan[2] = b;
     }
   };
@@ -308,7 +310,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
                   Run{__shfl_sync(0xffffffffu, lot.run.before, from), __shfl_sync(0xffffffffu, lot.run.len, from), a.G, a.window}};
       };
       take();
-      const int64_t whole = plan[1], x0 = start - plan[0], h0 = x0 / whole, x = x0 - h0 * whole;
+      const int64_t whole = plan[1], x0 = start - plan[0], h0 = attn::quotient(x0, whole), x = x0 - h0 * whole;
       int h = static_cast<int>(h0), i = 0;
       for (int hi = r.run.items(); hi - i > 1;) {  // the item of the first unit, 32 ways at a time
         const int step = (hi - i + 31) / 32, c = i + lane * step;
@@ -567,11 +569,11 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
     const uint32_t ts = tmem + w * 128 + lanes, to = tmem + 256 + w * 128 + lanes;
     float2 *const stats = reinterpret_cast<float2 *>(smem + M::STAT);
     uint32_t taken = 0, s_n = 0, o_n = 0, m_n = 0;
-    auto next_item = [&](Item &it) -> bool {
+    // (an item stays in shared memory until its results are out: its fields would take registers)
+    auto next_item = [&](const Item *&it) -> bool {
       const uint32_t is = taken % kItems;
       if (!wait(sb + M::IFULL + 8 * is, taken / kItems)) return false;
-      it = items[is];
-      arrive(sb + M::IEMPTY + 8 * is);
+      it = items + is;
       ++taken;
       return true;
     };
@@ -586,12 +588,11 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       const kda_bf16 *const q = a.q + static_cast<int64_t>(it.token0) * a.ldq + static_cast<int64_t>(it.head) * a.G * D + c * 8;
       const int i0 = (tid & 127) / kAcross, step_t = kAtOnce / a.G, step_g = kAtOnce - step_t * a.G;
       int t = (it.row0 + row_of + i0) / a.G, g = it.row0 + row_of + i0 - t * a.G;
+      const int rows = min(it.rows - row_of, 128);
 #pragma unroll 4
-      for (int i = i0; i < 128; i += kAtOnce) {
-        if (row_of + i < it.rows) {
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(col + i * 128 + (((c & 7) ^ (i & 7)) << 4)),
-                       "l"(__cvta_generic_to_global(q + t * a.ldq + g * D)) : "memory");
-        }
+      for (int i = i0; i < rows; i += kAtOnce) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(col + i * 128 + (((c & 7) ^ (i & 7)) << 4)),
+                     "l"(__cvta_generic_to_global(q + t * a.ldq + g * D)) : "memory");
         t += step_t;
         if ((g += step_g) >= a.G) {
           g -= a.G;
@@ -610,9 +611,10 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       const bool both = it.rows > 128;
       const int row_of = both ? w * 128 : 0, row = it.row0 + row_of + r, tok = row / a.G;
       const bool live = row_of + quad * 32 < it.rows, valid = row_of + r < it.rows;
-      float *const part = it.part < 0 ? nullptr
-                                      : reinterpret_cast<float *>(a.ws + kCutBytes + kStatBytes) +
-                                            (static_cast<int64_t>(it.part) * kRows + row_of + r) * D;
+      // parts: four columns of all rows, then the next four (a warp stores 512 bytes in a row)
+      float4 *const part = it.part < 0 ? nullptr
+                                       : reinterpret_cast<float4 *>(a.ws + kCutBytes + kStatBytes) +
+                                             static_cast<int64_t>(it.part) * kRows * (D / 4) + row_of + r;
       kda_bf16 *const out = a.o + (static_cast<int64_t>(it.token0) + tok) * a.ldo +
                             (static_cast<int64_t>(it.head) * a.G + (row - tok * a.G)) * D;
       auto put = [&](const float (&o)[32], int c, float f) {  // columns [32 c, 32 c + 32) of this row
@@ -620,7 +622,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
         if (part) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4 *>(part + 32 * c + 4 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            part[(8 * c + i) * kRows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -638,7 +640,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       if (both || it.n == 1) {
         const float f = l == 0.f ? 0.f : 1.f / l;
         if (live) {
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             float o[32];
             tmem_ld32(to + 32 * c, o);
@@ -651,20 +653,21 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
         return true;
       }
       // two chains of the same rows: the second one's sums come through shared memory, 64 columns at a
-      // time, 16-byte words of a row XORed with the row
+      // time, or all where 64 rows are enough, 16-byte words of a row XORed with the row
+      const int across = it.rows <= 64 ? D / 32 : 2;
+      const uint32_t at = sb + M::MERGE + r * across * 128;
       float mine = 1.f, other = 0.f, inv = 0.f;
-#pragma unroll
-      for (int half = 0; half < D / 64; ++half) {
-        const uint32_t at = sb + M::MERGE + r * 256;
+#pragma unroll 1
+      for (int c0 = 0; c0 < D / 32; c0 += across) {
         if (w == 1) {
           if (!wait(sb + M::MEMPTY, m_n + 1)) return false;
           ++m_n;
           if (live) {
-            if (half == 0) stats[r] = make_float2(m, l);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            if (c0 == 0) stats[r] = make_float2(m, l);
+#pragma unroll 1
+            for (int c = 0; c < across; ++c) {
               float o[32];
-              tmem_ld32(to + 64 * half + 32 * c, o);
+              tmem_ld32(to + 32 * (c0 + c), o);
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 8; ++i)
@@ -676,7 +679,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
           if (!wait(sb + M::MFULL, m_n)) return false;
           ++m_n;
           if (live) {
-            if (half == 0) {
+            if (c0 == 0) {
               const float2 t = stats[r];
               const float top = fmaxf(m, t.x), base = top == -INFINITY ? 0.f : top;
               mine = ex2(m - base);
@@ -684,11 +687,12 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
               l = l * mine + t.y * other;
               m = top;
               inv = l == 0.f ? 0.f : 1.f / l;
+              put_stats();
             }
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
+#pragma unroll 1
+            for (int c = 0; c < across; ++c) {
               float o[32];
-              tmem_ld32(to + 64 * half + 32 * c, o);
+              tmem_ld32(to + 32 * (c0 + c), o);
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
@@ -697,9 +701,8 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[4 * i + e] = o[4 * i + e] * mine + x[e] * other;
               }
-              put(o, 2 * half + c, inv);
+              put(o, c0 + c, inv);
             }
-            if (half == 0) put_stats();
           }
           arrive(sb + M::MEMPTY);
         }
@@ -708,13 +711,14 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       return true;
     };
     auto run = [&]() {
-      Item it;
-      if (!next_item(it)) return;
-      if (has_q(it)) {
-        if (!fetch_q(it)) return;
+      const Item *at, *next;
+      if (!next_item(at)) return;
+      if (has_q(*at)) {
+        if (!fetch_q(*at)) return;
         give_q();
       }
-      for (Item next; it.rows >= 0; it = next) {
+      for (; at->rows >= 0; at = next) {
+        const Item &it = *at;
         const bool both = it.rows > 128;
         const int steps = both ? it.n : (it.n + 1 - w) >> 1;
         const int row_of = both ? w * 128 : 0;  // of the tile, in the item
@@ -793,21 +797,22 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
         // else the other's may still be on their way, and are not when its last sum is there.  The second
         // tile's place takes sums below.
         if (!next_item(next)) return;
-        const bool q = has_q(next), q_later = q && !both && w == 1;
-        if (q && both && !fetch_q(next)) return;
+        const bool q = has_q(*next), q_later = q && !both && w == 1;
+        if (q && both && !fetch_q(*next)) return;
         if (steps > 0) {
           if (!wait(sb + M::OFULL + 8 * w, o_n++)) return;
           tc_fence_after();
         }
         if (q && !q_later) {
-          if (!both && !fetch_q(next)) return;
+          if (!both && !fetch_q(*next)) return;
           give_q();
         }
         if (steps > 0 && !results(it, m, l)) return;
         if (q_later) {
-          if (!fetch_q(next)) return;
+          if (!fetch_q(*next)) return;
           give_q();
         }
+        arrive(sb + M::IEMPTY + 8 * static_cast<uint32_t>(at - items));
       }
     };
     run();
@@ -821,51 +826,57 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
   }
 }
 
-// Joins the parts of each item that was cut: a warp takes a row, o = sum 2^(m_p - m) o_p / sum 2^(m_p - m) l_p.
+// Joins the parts of each item that was cut, o = sum 2^(m_p - m) o_p / sum 2^(m_p - m) l_p.  A lane takes a
+// row, a warp an eighth of the columns: what it reads lies in a row of memory.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinBlocks = 16;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
   grid_dependency_wait();
-  const int cta = blockIdx.x, lane = threadIdx.x & 31;
+  grid_launch_dependents();  // (the next call's start, which waits for this kernel's end)
+  const int cta = blockIdx.x, r = blockIdx.y * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
   const Cut cut = reinterpret_cast<const Cut *>(a.ws)[cta];
-  const float2 *stats = reinterpret_cast<const float2 *>(a.ws + kCutBytes);
-  const float *parts = reinterpret_cast<const float *>(a.ws + kCutBytes + kStatBytes);
+  if (r >= cut.rows) return;
+  constexpr int kFours = D / 4 / 8;  // of a lane
+  const float2 *stats = reinterpret_cast<const float2 *>(a.ws + kCutBytes) + r;
+  const float4 *parts = reinterpret_cast<const float4 *>(a.ws + kCutBytes + kStatBytes) + warp * kFours * kRows + r;
   const int n = cut.last - cta + 1;  // the first is 2 cta + 1, the others 2 c
-  auto place = [&](int p, int r) { return static_cast<int64_t>(p ? 2 * (cta + p) : 2 * cta + 1) * kRows + r; };
-  for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < cut.rows;
-       r += kJoinBlocks * (kJoinThreads / 32)) {
-    float top = -INFINITY;
-    for (int p = lane; p < n; p += 32) top = fmaxf(top, stats[place(p, r)].x);
+  auto place = [&](int p) { return static_cast<int64_t>(p ? 2 * (cta + p) : 2 * cta + 1); };
+  float4 o[kFours];
+  float top = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if (top == -INFINITY) top = 0.f;
-    constexpr int kCols = D / 32;
-    float o[kCols] = {}, l = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < n; ++p) {
-      const float2 s = stats[place(p, r)];
-      const float f = ex2(s.x - top);
-      l += s.y * f;
-      const float *x = parts + place(p, r) * D + lane * kCols;
-      if constexpr (kCols == 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(x);
-        o[0] += v.x * f, o[1] += v.y * f, o[2] += v.z * f, o[3] += v.w * f;
-      } else {
-        const float2 v = *reinterpret_cast<const float2 *>(x);
-        o[0] += v.x * f, o[1] += v.y * f;
+  for (int c = 0; c < kFours; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p0 = 0; p0 < n; p0 += 4) {  // four parts on their way at once
+    float2 s[4];
+    float4 v[4][kFours];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t at = place(min(p0 + i, n - 1));
+      s[i] = stats[at * kRows];
+#pragma unroll
+      for (int c = 0; c < kFours; ++c) v[i][c] = parts[(at * (D / 4) + c) * kRows];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (p0 + i >= n) break;
+      const float m = fmaxf(top, s[i].x), base = m == -INFINITY ? 0.f : m;
+      const float mine = ex2(top - base), f = ex2(s[i].x - base);
+      top = m;
+      l = l * mine + s[i].y * f;
+#pragma unroll
+      for (int c = 0; c < kFours; ++c) {
+        o[c].x = o[c].x * mine + v[i][c].x * f, o[c].y = o[c].y * mine + v[i][c].y * f;
+        o[c].z = o[c].z * mine + v[i][c].z * f, o[c].w = o[c].w * mine + v[i][c].w * f;
       }
     }
-    const float f = l == 0.f ? 0.f : 1.f / l;
-    const int row = cut.row0 + r, t = row / a.G, g = row - t * a.G;
-    kda_bf16 *out = a.o + (static_cast<int64_t>(cut.token0) + t) * a.ldo + (static_cast<int64_t>(cut.head) * a.G + g) * D + lane * kCols;
-    uint32_t x[kCols / 2];
-#pragma unroll
-    for (int e = 0; e < kCols / 2; ++e) x[e] = pack(o[2 * e] * f, o[2 * e + 1] * f);
-    if constexpr (kCols == 4) *reinterpret_cast<uint2 *>(out) = make_uint2(x[0], x[1]);
-    else *reinterpret_cast<uint32_t *>(out) = x[0];
   }
+  const float f = l == 0.f ? 0.f : 1.f / l;
+  const int row = cut.row0 + r, t = row / a.G, g = row - t * a.G;
+  kda_bf16 *out = a.o + (static_cast<int64_t>(cut.token0) + t) * a.ldo + (static_cast<int64_t>(cut.head) * a.G + g) * D + warp * kFours * 4;
+#pragma unroll
+  for (int c = 0; c < kFours; c += 2)
+    *reinterpret_cast<uint4 *>(out + 4 * c) = make_uint4(pack(o[c].x * f, o[c].y * f), pack(o[c].z * f, o[c].w * f),
+                                                         pack(o[c + 1].x * f, o[c + 1].y * f), pack(o[c + 1].z * f, o[c + 1].w * f));
 }
 
 template <int D>
@@ -886,10 +897,9 @@ cudaError_t run(const AttnArgs &a, const kda_bf16 *cache, cudaStream_t st) {
   const auto kernel = attn_kernel<D>;
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::BYTES))
     return e;
-  kernel<<<kCtas, kThreads, Smem<D>::BYTES, st>>>(map, a);
-  if (cudaError_t e = cudaGetLastError()) return e;
+  if (cudaError_t e = launch_pdl(kernel, dim3(kCtas), dim3(kThreads), Smem<D>::BYTES, st, map, a)) return e;
   if (!a.ws) return cudaSuccess;
-  return launch_pdl(attn_join_kernel<D>, dim3(kCtas, kJoinBlocks), dim3(kJoinThreads), 0, st, a);
+  return launch_pdl(attn_join_kernel<D>, dim3(kCtas, kRows / 32), dim3(kJoinThreads), 0, st, a);
 }
 
 }  // namespace

@@ -19,7 +19,12 @@ constexpr int kItemUnits = 5;  // what an item costs beside its tiles, in tiles
 constexpr int kCtas = 152;     // one on each SM
 constexpr int kLeastUnits = 4;
 
-KDA_HD int64_t floor_div(int64_t a, int64_t b) { return a >= 0 ? a / b : -((b - 1 - a) / b); }
+// a / b for a >= 0, b > 0: 64-bit division takes several times as long.
+KDA_HD int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+KDA_HD int64_t floor_div(int64_t a, int64_t b) { return a >= 0 ? quotient(a, b) : -quotient(b - 1 - a, b); }
 
 // Sum of floor((2 k + b) / G) over k in [0, n), b >= 0.
 //
@@ -27,10 +32,11 @@ KDA_HD int64_t floor_div(int64_t a, int64_t b) { return a >= 0 ? a / b : -((b - 
 // is the last term: n m less, for each y, the ceil((y G - b) / 2) values of k that do not reach it.
 KDA_HD int64_t floor_sum(int64_t n, int64_t G, int64_t b) {
   if (n <= 0) return 0;
-  int64_t sum = n * (b / G);
-  b %= G;
+  const int64_t q = quotient(b, G);
+  int64_t sum = n * q;
+  b -= q * G;
   if (G == 1) return sum + n * (n - 1);
-  const int64_t m = (2 * (n - 1) + b) / G, odd = G & 1;
+  const int64_t m = quotient(2 * (n - 1) + b, G), odd = G & 1;
   // the sum of ceil(x / 2), x = y G - b: (x + 1) / 2 where x is odd
   const int64_t n_odd = odd ? (b & 1 ? m / 2 : (m + 1) / 2) : (b & 1 ? m : 0);
   return sum + n * m - (G * (m * (m + 1) / 2) - m * b + n_odd) / 2;

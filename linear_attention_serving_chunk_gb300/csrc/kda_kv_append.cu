@@ -4,6 +4,7 @@
 // vectors a thread of consecutive tokens; the run, slot and page of each of its tokens are looked up
 // once, by one thread each, and the vectors are all in flight before the first is stored.
 #include "kda_paged.cuh"
+#include "kda_pdl.cuh"
 
 namespace kda {
 
@@ -55,6 +56,7 @@ __device__ int64_t place(const AppendArgs &a, int64_t t) {
 
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a, int per_token, int per_head) {
   __shared__ int64_t where[kTokens];
+  grid_launch_dependents();  // (the attention's start, which waits for this kernel's end)
   // vectors of a token: k's heads, then v's
   const int64_t v0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kVectors), t0 = v0 / per_token;
   const int first = static_cast<int>(v0 - t0 * per_token);

@@ -216,6 +216,7 @@ int kda_pages_compact(kda_bf16 *cache, int layers, int n_pages, int H, int page,
                       kda_stream_t stream) {
   if (int e = check_table(table, lens, max_pages, n_slots, n_pages, page)) return e;
   if (int e = check_layers(cache, layers, n_pages, H, page, D)) return e;
+  if (n_slots > kMaxSlots) return KDA_ERR_UNSUPPORTED;
   if (!used || (n_slots > 0 && max_pages > 0 && !table_out)) return KDA_ERR_NULL;
   if (!aligned4(table_out) || !aligned4(used) || !aligned16(workspace)) return KDA_ERR_ALIGN;
   const int64_t need = pages_ws_bytes(n_pages), rows = 4LL * n_slots, all = rows * max_pages;

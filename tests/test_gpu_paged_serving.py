@@ -1,0 +1,158 @@
+"""The paged cache's operators together, as a serving loop uses them: prompts in chunks, forked
+sequences, drafted runs that draft verification cuts, compaction in between, all lengths on the GPU;
+eagerly and with the step captured into a graph."""
+import pytest
+import torch
+
+import linear_attention_serving_chunk_gb300 as kda
+import paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+PAGE, H, Hq, D, LAYERS, VOCAB, SLOTS, PAGES, MOST, DRAFTS = 16, 2, 6, 64, 2, 40, 6, 90, 12, 3
+
+
+class Model:
+    """Queries, keys, values of a token are rows of tables, so what the cache has to hold is known exactly."""
+
+    def __init__(self, seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+        self.q = rnd(LAYERS, VOCAB, Hq, D).bfloat16()
+        self.kv = rnd(2, LAYERS, VOCAB, H, D).bfloat16()
+        self.head = (rnd(LAYERS * Hq * D, VOCAB) / (LAYERS * Hq * D) ** 0.5 * 6).bfloat16()
+        self.cache = torch.full((LAYERS, PAGES, 2, H, PAGE, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+        self.table = torch.full((SLOTS, MOST), -1, dtype=torch.int32, device="cuda")
+        self.lens = torch.zeros(SLOTS, dtype=torch.int32, device="cuda")
+
+    def forward(self, tokens, slots, cu):
+        """Probabilities after each token of the runs; their keys and values are in the cache then."""
+        want = self.lens.clone()
+        want[slots.long()] += cu[1:] - cu[:-1]
+        left = kda.pages_grow(self.table, self.lens, want, PAGE, PAGES)
+        out = []
+        for i in range(LAYERS):
+            t = tokens.long()
+            kda.kv_append(self.kv[0, i][t], self.kv[1, i][t], self.cache[i], self.table, self.lens, slots, cu)
+            out.append(kda.attn_paged(self.q[i][t], self.cache[i], self.table, self.lens, slots, cu))
+        self.out = torch.cat([o.flatten(1) for o in out], 1)
+        return torch.softmax((self.out @ self.head).float(), 1), left
+
+    def step(self, tokens, slots, cu, u):
+        """One run of a token and its drafts for each sequence: (emitted tokens, how many), lens moved on."""
+        p, left = self.forward(tokens, slots, cu)
+        out, n_out = kda.verify_draft(p, tokens, u, cu)
+        self.lens[slots.long()] += n_out
+        return out, n_out, left
+
+    def check_cache(self, texts):
+        """The pages of every sequence hold the keys and values of its tokens."""
+        for s, text in texts.items():
+            assert int(self.lens[s]) == len(text)
+            t = torch.tensor(text, device="cuda")
+            for i in range(LAYERS):
+                held = ref.gathered(self.cache[i].cpu(), self.table.cpu(), s, len(text))
+                assert torch.equal(held, self.kv[:, i][:, t].transpose(1, 2).double().cpu())
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def serve(graph):
+    g = torch.Generator().manual_seed(5)
+    m = Model(1)
+    # three prompts in two chunks, the second one's first chunk all of it
+    texts = {s: torch.randint(0, VOCAB, (n,), generator=g).tolist() for s, n in ((4, 37), (0, 16), (3, 50))}
+    done = {s: 0 for s in texts}
+    for cut in (16, 100):
+        runs = {s: t[done[s]:cut] for s, t in texts.items()}
+        cu = ints(ref.offsets([len(r) for r in runs.values()]))
+        slots = ints(list(runs))
+        m.forward(ints(sum(runs.values(), [])), slots, cu)
+        m.lens[slots.long()] += cu[1:] - cu[:-1]
+        for s, r in runs.items():
+            done[s] += len(r)
+    m.check_cache(texts)
+    # two of them go on twice; what they share stays shared
+    left = kda.pages_fork(m.cache, m.table, m.lens, ints([4, 3]), ints([1, 5]))
+    texts[1], texts[5] = list(texts[4]), list(texts[3])
+    m.check_cache(texts)
+    # unused: all but 3 + 1 + 4 pages of the prompts and two copies of last ones
+    assert left.tolist() == [PAGES - 10] and kda.device_status() == 0
+    live = list(texts)
+    slots, cu = ints(live), ints(ref.offsets([1 + DRAFTS] * len(live)))
+    tokens, u = ints([0] * (len(live) * (1 + DRAFTS))), torch.zeros(len(live) * (1 + DRAFTS), device="cuda")
+    replay = None
+    if graph:
+        lens = m.lens.clone()
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        replay = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(replay, stream=stream):
+            outs = m.step(tokens, slots, cu, u)
+        m.lens.copy_(lens)
+    last = {s: int(torch.randint(0, VOCAB, (1,), generator=g)) for s in live}
+    seen = []
+    for turn in range(7):
+        # drafts: the text's own words, so that some are accepted
+        batch = [[last[s]] + torch.randint(0, VOCAB, (DRAFTS,), generator=g).tolist() for s in live]
+        tokens.copy_(ints(sum(batch, [])))
+        u.copy_(torch.rand(len(u), generator=g) * 0.05)  # (low: certain drafts pass at the rate of their weight)
+        if graph:
+            replay.replay()
+        else:
+            before = m.lens.clone()
+            outs = m.step(tokens, slots, cu, u)
+            for i in range(LAYERS):  # the attention of this step, against the plain form
+                o, size = ref.attention(m.q[i][tokens.long()].cpu(), m.cache[i].cpu(), m.table.cpu(), before.cpu(), live, cu.tolist())
+                err = (m.out[:, i * Hq * D:(i + 1) * Hq * D].view(-1, Hq, D).double().cpu() - o).abs()
+                assert float((err - 2.0 ** -8 * o.abs() - (2.0 ** -8 + 2.0 ** -14) * size).max()) <= 0
+        emitted, count = outs[0].view(len(live), -1).tolist(), outs[1].tolist()
+        seen.append((emitted, count, outs[2].tolist()))
+        for s, row, e, n in zip(live, batch, emitted, count):
+            texts[s] += row[:1] + e[:n - 1]
+            last[s] = e[n - 1]
+        m.check_cache(texts)
+        if turn == 3:
+            table, used = kda.pages_compact(m.cache, m.table, m.lens)
+            m.table.copy_(table)
+            assert int(m.table.max()) == int(used) - 1
+            m.check_cache(texts)
+    assert kda.device_status() == 0
+    return texts, seen
+
+
+def test_serving_loop_eager_and_captured():
+    """The same tokens either way; at least one draft in the run is accepted, at least one refused."""
+    texts, seen = serve(False)
+    counts = sum((c for _, c, _ in seen), [])
+    assert min(counts) == 1 and max(counts) > 1
+    again, seen_again = serve(True)
+    assert again == texts and seen_again == seen
+
+
+def test_two_captured_calls_with_workspaces_of_their_own():
+    """Attention captured twice, on two streams, replayed at once: each as it is alone."""
+    outs, graphs, want = [], [], []
+    for seed in (1, 2):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        q = torch.randn(3, 8, 128, generator=g, device="cuda").bfloat16()
+        cache = torch.randn(200, 2, 1, 64, 128, generator=g, device="cuda").bfloat16()
+        table, lens = torch.randperm(200, generator=g, device="cuda").int().view(2, 100), ints([6000, 3000])
+        args = (q, cache, table, lens, None, ints([0, 1, 3]))
+        want.append(kda.attn_paged(*args))
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            outs.append(kda.attn_paged(*args))
+        graphs.append((graph, s, args))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, s, _ in graphs:
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+    assert kda.device_status() == 0

@@ -320,11 +320,9 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       }
       int64_t at = plan[0] + h * whole + r.run.units_before(i);  // where it begins
       while (at < stop) {
-        const int lo = r.run.first(i), n = r.run.end(i) - lo;
+        const int lo = r.run.first(i), n = r.run.end(i) - lo, weight = r.run.weight(i);
         // this share's part of the item, in tiles
-        const int64_t skip = at + attn::kItemUnits;
-        int from = start > skip ? static_cast<int>(start - skip) : 0;
-        int to = static_cast<int>(min(stop - skip, static_cast<int64_t>(n)));
+        int from = attn::tiles_before(start - at, n, weight), to = attn::tiles_before(stop - at, n, weight);
         if (!a.ws) {  // an item belongs to the share in which it begins
           from = 0;
           to = at >= start ? n : 0;
@@ -332,7 +330,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
         if (from < to) {
           Item it;
           it.row0 = i * kRows;
-          it.rows = min(r.run.rows() - it.row0, kRows);
+          it.rows = r.run.rows_of(i);
           it.token0 = r.begin;
           it.head = h;
           it.before = r.run.before;
@@ -342,10 +340,10 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
           it.slot = r.slot;
           it.part = from > 0 ? 2 * cta : to < n ? 2 * cta + 1 : -1;
           if (from == 0 && to < n && lane == 0)
-            reinterpret_cast<Cut *>(a.ws)[cta] = Cut{it.rows, it.row0, it.token0, h, static_cast<int>((skip + n - 1) / each), {}};
+            reinterpret_cast<Cut *>(a.ws)[cta] = Cut{it.rows, it.row0, it.token0, h, static_cast<int>(attn::quotient(at + attn::kItemUnits + static_cast<int64_t>(n - 1) * weight, each)), {}};
           if (!give(it)) break;
         }
-        at = skip + n;
+        at += attn::kItemUnits + static_cast<int64_t>(n) * weight;
         if (++i < r.run.items()) continue;
         i = 0;
         if (++h < a.H) continue;

@@ -15,9 +15,12 @@ namespace attn {
 
 constexpr int kRows = 256;     // rows (token, head of the group) of an item, two tiles of 128
 constexpr int kTile = 128;     // positions of a tile of keys
-constexpr int kItemUnits = 5;  // what an item costs beside its tiles, in tiles
 constexpr int kCtas = 152;     // one on each SM
-constexpr int kLeastUnits = 4;
+
+// What things cost, in tiles of an item of at most 128 rows (each of its two chains takes every other tile).
+constexpr int kWideTile = 2;   // a tile of an item with more rows
+constexpr int kItemUnits = 7;  // an item, beside its tiles
+constexpr int kLeastUnits = 4; // the least share of a CTA
 
 // a / b for a >= 0, b > 0: 64-bit division takes several times as long.
 KDA_HD int64_t quotient(int64_t a, int64_t b) {
@@ -59,23 +62,34 @@ struct Run {
     const int last = static_cast<int>((static_cast<unsigned>(i + 1) * kRows - 1) / G);
     return (before + (last < len - 1 ? last : len - 1) + kTile) / kTile;
   }
+  KDA_HD int rows_of(int i) const { return rows() - i * kRows < kRows ? rows() - i * kRows : kRows; }
+  KDA_HD int weight(int i) const { return rows_of(i) > 128 ? kWideTile : 1; }
   // Units of the items in front of item i: both ends grow by 256 / (128 G) tiles an item, rounded down.
   KDA_HD int64_t units_before(int i) const {
     const int n = items();
     const int64_t k = i < n ? i : n - 1;
     if (n == 0 || i == 0) return 0;
-    if (n == 1) return kItemUnits + end(0) - first(0);
-    int64_t sum = k * kItemUnits + floor_sum(k, G, (static_cast<int64_t>(G) * (before + kTile) + kRows - 1) / kTile);
+    const int64_t last = kItemUnits + static_cast<int64_t>(weight(n - 1)) * (end(n - 1) - first(n - 1));
+    if (n == 1) return last;
+    int64_t tiles = floor_sum(k, G, (static_cast<int64_t>(G) * (before + kTile) + kRows - 1) / kTile);
     if (window) {
       const int64_t b = floor_div(static_cast<int64_t>(G) * (before - window + 1), kTile), skip = b < 0 ? (1 - b) / 2 : 0;
-      if (k > skip) sum -= floor_sum(k - skip, G, 2 * skip + b);
+      if (k > skip) tiles -= floor_sum(k - skip, G, 2 * skip + b);
     }
-    return i < n ? sum : sum + kItemUnits + end(n - 1) - first(n - 1);
+    return k * kItemUnits + tiles * kWideTile + (i < n ? 0 : last);
   }
   KDA_HD int64_t units() const { return units_before(items()); }
 };
 
-// Units of a CTA.
+// Tiles of an item that lie in front of unit u behind its beginning; a tile belongs to the share in which it
+// begins.
+KDA_HD int tiles_before(int64_t u, int n, int weight) {
+  u -= kItemUnits;
+  return u <= 0 ? 0 : u >= static_cast<int64_t>(n) * weight ? n : static_cast<int>((u + weight - 1) / weight);
+}
+
+// Units of a CTA, at least two of the widest tiles, so that no share within an item is empty.
+static_assert(kLeastUnits >= 2 * kWideTile, "shares");
 KDA_HD int64_t share(int64_t units) {
   const int64_t each = (units + kCtas - 1) / kCtas;
   return each > kLeastUnits ? each : kLeastUnits;

@@ -188,13 +188,28 @@ int main() {
         if (p / kTile + 1 > hi) hi = p / kTile + 1;
       }
       if (lo != r.first(i) || hi != r.end(i)) return printf("tiles G %d before %d len %d window %d item %d\n", r.G, r.before, r.len, r.window, i), 1;
-      sum += kItemUnits + hi - lo;
+      sum += kItemUnits + (hi - lo) * ((r.rows() - i * kRows > 128) ? kWideTile : 1);
     }
   }
   Run far{(1 << 27) - 70000, 70000, 128, 0};  // the largest positions
   long long sum = 0;
-  for (int i = 0; i < far.items(); ++i) sum += kItemUnits + far.end(i);
-  return sum == far.units() ? 0 : (printf("far\n"), 1);
+  for (int i = 0; i < far.items(); ++i) sum += kItemUnits + static_cast<long long>(far.end(i)) * (far.rows() - i * kRows > 128 ? kWideTile : 1);
+  if (sum != far.units()) return printf("far\n"), 1;
+  // an item cut at any units: parts follow one another, none in the middle is empty, and the last one is known
+  for (int turn = 0; turn < 20000; ++turn) {
+    const int n = 1 + rand() % 60, weight = 1 + turn % kWideTile;
+    const long long at = rand() % 500, units = kItemUnits + n * weight, each = kLeastUnits + rand() % 40;
+    int done = 0;
+    long long last = -1;
+    for (long long c = at / each; c * each < at + units; ++c) {
+      const int from = tiles_before(c * each - at, n, weight), to = tiles_before((c + 1) * each - at, n, weight);
+      if (from != done || (from > 0 && from < n && to == from)) return printf("part\n"), 1;
+      if (to > from) last = c;
+      done = to;
+    }
+    if (done != n || last != quotient(at + kItemUnits + static_cast<long long>(n - 1) * weight, each)) return printf("parts\n"), 1;
+  }
+  return 0;
 }
 """
 

@@ -32,6 +32,8 @@
 // rows of V behind the sequence are zeroed, for 0 times what lies there might not be 0.
 #include <string.h>
 
+#include <type_traits>
+
 #include "kda_attn_plan.cuh"
 #include "kda_paged.cuh"
 #include "kda_pdl.cuh"
@@ -96,13 +98,17 @@ struct Smem {
   static constexpr uint32_t kRegion = kTile * 128;              // 64 columns of a tile
   static constexpr uint32_t kTileBytes = D / 64 * kRegion;
   static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kScores = D == 128 ? 2 : 3;              // places of scores and weights in TMEM
+  static constexpr uint32_t kO = kScores * 128;                 // sums behind them
+  // Of scores s of an item behind `turn` others: the warpgroup's own, or a third one in turn.
+  __device__ static uint32_t place(uint32_t turn, uint32_t s) { return kScores == 2 ? s & 1 : (turn + s) % kScores; }
   static constexpr uint32_t Q = 0;
   static constexpr uint32_t MERGE = kTileBytes;                 // second Q tile, or 128 x 64 fp32
   static constexpr uint32_t STAGE = MERGE + 32 * 1024;
   static constexpr uint32_t BAR = STAGE + kStages * kTileBytes;
   static constexpr uint32_t FULL = BAR, EMPTY = FULL + 8 * kStages, SFULL = EMPTY + 8 * kStages,
-                            PREADY = SFULL + 16, QREADY = PREADY + 16, OFULL = QREADY + 16,
-                            IFULL = OFULL + 16, IEMPTY = IFULL + 8 * kItems,
+                            PREADY = SFULL + 32, QREADY = PREADY + 8 * kScores, OFULL = QREADY + 16,
+                            ODONE = OFULL + 16, IFULL = ODONE + 16, IEMPTY = IFULL + 8 * kItems,
                             MFULL = IEMPTY + 8 * kItems, MEMPTY = MFULL + 8, FIN = MEMPTY + 8;
   static constexpr uint32_t TMEM = FIN + 8;
   static constexpr uint32_t PLAN = TMEM + 8;                    // int64: units, position, run's first unit; run
@@ -174,6 +180,8 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, cta = blockIdx.x;
   grid_launch_dependents();
   if ((sb & 1023u) != 0) {  // the swizzled tiles need it
+    grid_dependency_wait();
+    if (a.ws && tid < 8) reinterpret_cast<int *>(a.ws)[cta * 8 + tid] = 0;
     if (tid == 0) atomicOr(a.status, KDA_ERR_UNSUPPORTED);
     return;
   }
@@ -182,11 +190,12 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       mbar_init(sb + M::FULL + 8 * i, 1);
       mbar_init(sb + M::EMPTY + 8 * i, 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(sb + M::SFULL + 8 * i, 1);
+    for (int i = 0; i < M::kScores; ++i) mbar_init(sb + M::PREADY + 8 * i, 4);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(sb + M::SFULL + 8 * i, 1);
-      mbar_init(sb + M::PREADY + 8 * i, 4);
       mbar_init(sb + M::QREADY + 8 * i, 4);
       mbar_init(sb + M::OFULL + 8 * i, 1);
+      mbar_init(sb + M::ODONE + 8 * i, 1);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(sb + M::IFULL + 8 * i, 1);
@@ -204,6 +213,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
   }
 
   grid_dependency_wait();
+  if (a.ws && tid < 8) reinterpret_cast<int *>(a.ws)[cta * 8 + tid] = 0;  // no item is cut yet
 
   // This CTA's share: all units, then the run in which the share begins.
   int64_t *const plan = reinterpret_cast<int64_t *>(smem + M::PLAN);
@@ -293,8 +303,6 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       ++given;
       return true;
     };
-    if (a.ws && lane < 8) reinterpret_cast<int *>(a.ws)[cta * 8 + lane] = 0;
-    __syncwarp();
     if (start < stop) {
       // 32 runs at a time, one in each lane
       int b = static_cast<int>(plan[2]), held = b;
@@ -410,19 +418,13 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
     auto load_item = [&](const Item &it) -> bool {
       const int first = a.window ? max(it.before + it.row0 / a.G - a.window + 1, 0) : 0;
       const int n = it.n, lo = it.lo;
-      if (!load(it, lo, 0, first)) return false;
-      if (it.rows > 128) {
-        for (int j = 0; j < n; ++j) {
-          if (!load(it, lo + j, 1, first)) return false;
-          if (j + 1 < n && !load(it, lo + j + 1, 0, first)) return false;
-        }
-        return true;
-      }
-      // in the order in which the MMAs want them: K of two tiles ahead behind each V
-      if (n > 1 && !load(it, lo + 1, 0, first)) return false;
+      // in the order in which the MMAs want them: the scores run ahead of the sums
+      const int ahead = it.rows > 128 ? (M::kScores + 1) / 2 : M::kScores;
+      for (int j = 0; j < min(ahead, n); ++j)
+        if (!load(it, lo + j, 0, first)) return false;
       for (int j = 0; j < n; ++j) {
         if (!load(it, lo + j, 1, first)) return false;
-        if (j + 2 < n && !load(it, lo + j + 2, 0, first)) return false;
+        if (j + ahead < n && !load(it, lo + j + ahead, 0, first)) return false;
       }
       return true;
     };
@@ -445,10 +447,20 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
     // ---- MMAs ------------------------------------------------------------------------------
     constexpr uint32_t ID_S = idesc_mma(128, kTile, kFmtBF16, kFmtBF16, 0, 0);
     constexpr uint32_t ID_O = idesc_mma(128, D, kFmtBF16, kFmtBF16, 0, 1);
-    uint32_t used = 0, stage = 0, taken = 0, q_n[2] = {0, 0}, p_n[2] = {0, 0};
+    uint32_t used = 0, stage = 0, taken = 0, q_n[2] = {0, 0}, p_bits = 0;
+    auto p_phase = [&](uint32_t place) {  // each place's phases of P, one after another
+      const uint32_t phase = p_bits >> place;
+      p_bits ^= 1u << place;
+      return phase;
+    };
     // (descriptors from an address that the compiler cannot see through: hoisted out of the loop, the
     // sums of all steps would take most of this warp's registers)
-    auto scores = [&](int w, int q, uint32_t k) {
+    // Scores are announced to each warpgroup in turn on two barriers of its own: it waits for each of its
+    // scores, and for no other's, and at most one more is there before it has taken the last.
+    uint32_t announced[2] = {0, 0};
+    auto scores = [&](int place, int w, int q, uint32_t k) {
+      const uint32_t full = sb + M::SFULL + 16 * w + 8 * (announced[w] & 1);
+      ++announced[w];
       if (elect()) {
         uint32_t qa = sb + M::Q + q * M::kTileBytes;
         asm volatile("" : "+r"(qa), "+r"(k));
@@ -456,25 +468,22 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
           const uint32_t off = ((s >> 2) * M::kRegion + (s & 3) * 32) >> 4;
-          mma_f16(tmem + w * 128, qd + off, kd + off, ID_S, s > 0);
+          mma_f16(tmem + place * 128, qd + off, kd + off, ID_S, s > 0);
         }
-        mma_commit(sb + M::SFULL + 8 * w);
+        mma_commit(full);
       }
       __syncwarp();
     };
-    auto weighted = [&](int w, uint32_t v, bool add) -> bool {
-      if (!wait(sb + M::PREADY + 8 * w, p_n[w]++)) return false;
-      tc_fence_after();
+    auto weighted = [&](int place, int w, uint32_t v, bool add) {
       if (elect()) {
-        uint32_t p = tmem + w * 128;
+        uint32_t p = tmem + place * 128, o = tmem + M::kO + w * D;
         asm volatile("" : "+r"(p), "+r"(v));
         const uint64_t vd = sw128_desc(v, M::kRegion, 1024);
 #pragma unroll
         for (int s = 0; s < kTile / 16; ++s)
-          mma_ta(p + 256, p + 8 * s, vd + ((s * 2048) >> 4), ID_O, add || s > 0);
+          mma_ta(o, p + 8 * s, vd + ((s * 2048) >> 4), ID_O, add || s > 0);
       }
       __syncwarp();
-      return true;
     };
     auto commit = [&](uint32_t bar) {
       if (elect()) mma_commit(bar);
@@ -489,7 +498,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       return ok;
     };
     auto run = [&]() {
-      for (;;) {
+      for (uint32_t turn = 0;;) {  // scores of the items before
         const uint32_t s = taken % kItems;
         if (!wait(sb + M::IFULL + 8 * s, taken / kItems)) return;
         const Item it = items[s];
@@ -509,50 +518,47 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
           fence_proxy_async();
           __syncwarp();
         };
-        uint32_t k, v, k_free, v_free;
+        // Scores s = 0, 1, ... of the item go to the warpgroups in turn, and to the places in TMEM: scores
+        // s + kScores follow the sum that has read the weights s (MMAs are done in order).
+        const int all = both ? 2 * n : n;
+        uint32_t k = 0, v = 0, k_free = 0, v_free = 0;
         if (!wait(sb + M::QREADY, q_n[0]++)) return;
         if (both && !wait(sb + M::QREADY + 8, q_n[1]++)) return;
         tc_fence_after();
-        if (!tile(k, k_free)) return;
-        scores(0, 0, k);
-        if (both) scores(1, 1, k);
-        commit(k_free);
-        if (both) {
-          for (int j = 0; j < n; ++j) {
-            const bool more = j + 1 < n;
-            if (!tile(v, v_free)) return;
-            if (j == zero_tile) clear(v);
-            if (more && !tile(k, k_free)) return;
-            for (int w = 0; w < 2; ++w) {
-              if (!weighted(w, v, j > 0)) return;
-              if (w == 1) commit(v_free);
-              if (more) scores(w, w, k);
-              else commit(sb + M::OFULL + 8 * w);
+        // (twice in the code, for what it tests to be known, and two steps at a time, for the same reason)
+        auto steps = [&](auto wide) -> bool {
+          constexpr bool two = decltype(wide)::value;  // the tiles serve both warpgroups
+          auto next_keys = [&](int s) -> bool { return (two && (s & 1)) || tile(k, k_free); };
+          auto next_scores = [&](int s) {
+            const bool second = s & 1;
+            scores(M::place(turn, s), second, two && second, k);
+            if (!two || second) commit(k_free);
+          };
+          for (int s = 0; s < min(M::kScores, all); ++s) {
+            if (!next_keys(s)) return false;
+            next_scores(s);
+          }
+#pragma unroll 2
+          for (int s = 0; s < all; ++s) {
+            const int w = s & 1, place = M::place(turn, s);
+            if (!(two && w)) {
+              if (!tile(v, v_free)) return false;
+              if ((two ? s >> 1 : s) == zero_tile) clear(v);
             }
-            if (more) commit(k_free);
+            const bool more = s + M::kScores < all;
+            if (more && !next_keys(s + M::kScores)) return false;
+            if (!wait(sb + M::PREADY + 8 * place, p_phase(place))) return false;
+            tc_fence_after();
+            weighted(place, w, v, s > 1);
+            if (!two || w) commit(v_free);
+            if (M::kScores > 2) commit(sb + M::ODONE + 8 * w);
+            if (s + 2 >= all) commit(sb + M::OFULL + 8 * w);
+            if (more) next_scores(s + M::kScores);
           }
-        } else {
-          if (n > 1) {
-            if (!tile(k, k_free)) return;
-            scores(1, 0, k);
-            commit(k_free);
-          }
-          for (int j = 0; j < n; ++j) {
-            const int w = j & 1;
-            const bool more = j + 2 < n;
-            if (!tile(v, v_free)) return;
-            if (j == zero_tile) clear(v);
-            if (!weighted(w, v, j > 1)) return;
-            commit(v_free);
-            if (more) {
-              if (!tile(k, k_free)) return;
-              scores(w, 0, k);
-              commit(k_free);
-            } else {
-              commit(sb + M::OFULL + 8 * w);
-            }
-          }
-        }
+          return true;
+        };
+        if (!(both ? steps(std::true_type{}) : steps(std::false_type{}))) return;
+        turn += all;
       }
     };
     run();
@@ -564,9 +570,9 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
     // ---- weights and results ---------------------------------------------------------------
     const int w = warp >> 2, quad = warp & 3, r = quad * 32 + lane;  // row of the warpgroup's tile
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t ts = tmem + w * 128 + lanes, to = tmem + 256 + w * 128 + lanes;
+    const uint32_t to = tmem + M::kO + w * D + lanes;
     float2 *const stats = reinterpret_cast<float2 *>(smem + M::STAT);
-    uint32_t taken = 0, s_n = 0, o_n = 0, m_n = 0;
+    uint32_t taken = 0, turn = 0, s_n = 0, o_n = 0, m_n = 0;  // turn: scores of the items before
     // (an item stays in shared memory until its results are out: its fields would take registers)
     auto next_item = [&](const Item *&it) -> bool {
       const uint32_t is = taken % kItems;
@@ -726,7 +732,9 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
         const int see1 = it.before + tok + 1, see0 = a.window ? max(see1 - a.window, 0) : 0;
         float m = -INFINITY, l = 0.f;  // log2
         for (int j = 0; j < steps; ++j) {
-          if (!wait(sb + M::SFULL + 8 * w, s_n++)) return;
+          const uint32_t place = M::place(turn, 2 * j + w), ts = tmem + place * 128 + lanes;
+          if (!wait(sb + M::SFULL + 16 * w + 8 * (s_n & 1), s_n >> 1)) return;
+          ++s_n;
           if (live) {
             tc_fence_after();
             float s[4][32];
@@ -751,12 +759,18 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
               for (int i = 1; i < 32; ++i) mx[c] = fmaxf(mx[c], s[c][i]);
             }
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
-            const bool higher = top > m + kKeep;  // (the first finite score is: m is -inf)
+            const bool higher = valid && top > m + kKeep;  // (the first finite score is: m is -inf)
             if (__any_sync(0xffffffffu, higher)) {
               const float f = higher ? ex2(m - top) : 1.f;
               if (higher) m = top;
               l *= f;
-              if (j > 0) {  // O of the tiles before: their MMAs are done, the next one waits for P
+              if (j > 0) {  // O of the tiles before: the next MMA waits for P
+                // With two places, these scores came behind the last sum; with three, behind the one before it,
+                // so that the barrier of the sums is in the last one's phase or behind it.
+                if (M::kScores > 2) {
+                  if (!wait(sb + M::ODONE + 8 * w, s_n - 2)) return;
+                  tc_fence_after();
+                }
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                   float o[32];
@@ -789,8 +803,9 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
             tmem_wait_st();
             tc_fence_before();
           }
-          arrive(sb + M::PREADY + 8 * w);
+          arrive(sb + M::PREADY + 8 * place);
         }
+        turn += both ? 2 * it.n : it.n;
         // The next item's Q.  With 128 rows of its own the warpgroup has seen the last scores of this one;
         // else the other's may still be on their way, and are not when its last sum is there.  The second
         // tile's place takes sums below.

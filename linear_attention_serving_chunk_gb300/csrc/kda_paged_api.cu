@@ -108,8 +108,8 @@ int kda_attn_paged(const kda_bf16 *q, int64_t ldq, const int32_t *cu_seqlens, in
   if (int e = check_heads(H, D, cache, n_pages)) return e;
   if (Hq <= 0 || Hq % H != 0 || Hq > 65535 || window < 0) return KDA_ERR_SHAPE;
   if (!slots && n > n_slots) return KDA_ERR_SHAPE;
-  // (also refuses NaN)
-  if (!(scale > 0.f && scale <= 3e38f)) return KDA_ERR_UNSUPPORTED;
+  // (also refuses NaN; the kernel multiplies it by log2(e))
+  if (!(scale > 0.f && scale <= 1e38f)) return KDA_ERR_UNSUPPORTED;
   const int64_t cols = static_cast<int64_t>(Hq) * D;
   if (total_tokens > 1 && (ldq < cols || ldo < cols)) return KDA_ERR_SHAPE;
   if (total_tokens > 0 && (!q || !o)) return KDA_ERR_NULL;

@@ -42,6 +42,13 @@ def _table(table, lens, dev):
             _dense(lens, "lens", _I32, (n_slots,), dev), n_slots)
 
 
+def _int32(v, name):
+    """v, which the C call takes as an int: others would be cut to 32 bits without a word."""
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} must be a 32-bit integer, got {v}")
+    return v
+
+
 def _scratch(workspace, size, dev, stream):
     """(the workspace, its address, its bytes)"""
     if workspace is None:
@@ -105,7 +112,7 @@ def attn_paged(q, cache, table, lens, slots=None, cu_seqlens=None, scale=None, w
         workspace, L.kda_attn_paged_workspace_bytes(n, total, Hq, H, D), dev, stream)
     st = L.kda_attn_paged(*_rows(q, "q", (total, Hq, D), dev), cu, n, total, Hq, H, D, at, n_pages,
                           page, tp, most, lp, n_slots, _dense(slots, "slots", _I32, (n,), dev),
-                          D ** -0.5 if scale is None else scale, window, op, ldo, wp, size,
+                          D ** -0.5 if scale is None else scale, _int32(window, "window"), op, ldo, wp, size,
                           _on(stream, dev))
     if st != KDA_OK:
         raise KDAError("kda_attn_paged", st)
@@ -128,7 +135,7 @@ def pages_grow(table, lens, want, page, n_pages, left=None, stream=None):
         raise TypeError("want must be a torch.Tensor")
     left, cp = _count(left, "left", dev, stream)
     st = lib().kda_pages_grow(tp, most, lp, _dense(want, "want", _I32, (n_slots,), dev), n_slots,
-                              n_pages, page, cp, _on(stream, dev))
+                              _int32(n_pages, "n_pages"), _int32(page, "page"), cp, _on(stream, dev))
     if st != KDA_OK:
         raise KDAError("kda_pages_grow", st)
     return left

@@ -224,6 +224,20 @@ def test_compact(n_slots, most, page, n_pages, layers, in_place):
     assert torch.equal(t.cpu(), renamed if in_place else table)
 
 
+def test_compact_leaves_what_is_malformed():
+    """Entries outside the pool stay as they are; a row with a bad length holds no pages."""
+    table = torch.tensor([[9, 12], [-4, 6], [7, 8], [1, 1]], dtype=torch.int32)
+    lens = torch.tensor([20, 32, -1, 33], dtype=torch.int32)
+    cache = noise(1, 10, 2, 1, 16, 64)
+    want, renamed, used = ref.compact(cache, table, lens, 16)
+    c = cache.cuda()
+    out, n = kda.pages_compact(c, table.cuda(), lens.cuda())
+    assert kda.device_status() == kda.KDA_ERR_SHAPE
+    assert n.tolist() == [used] == [2] and torch.equal(out.cpu(), renamed) and same(c, want)
+    with pytest.raises(ValueError):
+        kda.pages_grow(table.cuda(), lens.cuda(), lens.cuda(), 16, 1 << 32)
+
+
 def test_compact_of_a_large_pool():
     """2^20 pages of 4 KB: every third is in use, and each keeps its contents."""
     n_pages = 1 << 20

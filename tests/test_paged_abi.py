@@ -61,7 +61,7 @@ ATTN = dict(q=at(GB), ldq=256, cu=at(0x1000), n=2, total=8, Hq=4, H=2, D=64, cac
     (dict(ldq=248), SHAPE), (dict(ldo=255), SHAPE), (dict(ldq=260), ALIGN), (dict(ldo=258), ALIGN),
     (dict(Hq=3), SHAPE), (dict(Hq=0), SHAPE), (dict(Hq=65536), SHAPE), (dict(window=-1), SHAPE), (dict(n_pages=0), SHAPE),
     (dict(scale=0.0), UNSUPPORTED), (dict(scale=-1.0), UNSUPPORTED), (dict(scale=float("nan")), UNSUPPORTED),
-    (dict(scale=float("inf")), UNSUPPORTED), (dict(ws=at(0x10008)), ALIGN),
+    (dict(scale=float("inf")), UNSUPPORTED), (dict(scale=3e38), UNSUPPORTED), (dict(ws=at(0x10008)), ALIGN),
     # o beside q but not over it, and in the cache
     (dict(o=at(GB + 16)), SHAPE), (dict(o=at(GB), ldo=264), SHAPE), (dict(o=at(4 * GB + 32)), SHAPE)])
 def test_attention_refuses(L, kw, status):

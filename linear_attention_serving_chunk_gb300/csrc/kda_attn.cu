@@ -319,14 +319,25 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       };
       take();
       const int64_t whole = plan[1], x0 = start - plan[0], h0 = attn::quotient(x0, whole), x = x0 - h0 * whole;
-      int h = static_cast<int>(h0), i = 0;
-      for (int hi = r.run.items(); hi - i > 1;) {  // the item of the first unit, 32 ways at a time
+      int h = static_cast<int>(h0), i = 0, hi = r.run.items();
+      while (hi - i > 32) {  // the items around unit x, 32 ways at a time
         const int step = (hi - i + 31) / 32, c = i + lane * step;
         const unsigned some = __ballot_sync(0xffffffffu, c < hi && r.run.units_before(c) <= x);
         i += (31 - __clz(some)) * step;
         hi = min(hi, i + step);
       }
-      int64_t at = plan[0] + h * whole + r.run.units_before(i);  // where it begins
+      // and of these, each in a lane, the one that unit x is in
+      const int64_t front = i ? r.run.units_before(i) : 0;
+      const int mine = i + lane < hi ? static_cast<int>(r.run.units_of(i + lane)) : 0;
+      int ends = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int y = __shfl_up_sync(0xffffffffu, ends, d);
+        if (lane >= d) ends += y;
+      }
+      const int in = __ffs(__ballot_sync(0xffffffffu, front + ends > x)) - 1;
+      i += in;
+      int64_t at = plan[0] + h * whole + front + __shfl_sync(0xffffffffu, ends - mine, in);  // where it begins
       while (at < stop) {
         const int lo = r.run.first(i), n = r.run.end(i) - lo, weight = r.run.weight(i);
         // this share's part of the item, in tiles
@@ -912,7 +923,9 @@ cudaError_t run(const AttnArgs &a, const kda_bf16 *cache, cudaStream_t st) {
     return e;
   if (cudaError_t e = launch_pdl(kernel, dim3(kCtas), dim3(kThreads), Smem<D>::BYTES, st, map, a)) return e;
   if (!a.ws) return cudaSuccess;
-  return launch_pdl(attn_join_kernel<D>, dim3(kCtas, kRows / 32), dim3(kJoinThreads), 0, st, a);
+  // (of runs of one length the host knows how many rows an item has at most)
+  const int64_t rows = a.runs.cu ? kRows : a.runs.fixed_len * a.G < kRows ? a.runs.fixed_len * a.G : kRows;
+  return launch_pdl(attn_join_kernel<D>, dim3(kCtas, static_cast<unsigned>((rows + 31) / 32)), dim3(kJoinThreads), 0, st, a);
 }
 
 }  // namespace

@@ -64,12 +64,13 @@ struct Run {
   }
   KDA_HD int rows_of(int i) const { return rows() - i * kRows < kRows ? rows() - i * kRows : kRows; }
   KDA_HD int weight(int i) const { return rows_of(i) > 128 ? kWideTile : 1; }
+  KDA_HD int64_t units_of(int i) const { return kItemUnits + static_cast<int64_t>(weight(i)) * (end(i) - first(i)); }
   // Units of the items in front of item i: both ends grow by 256 / (128 G) tiles an item, rounded down.
   KDA_HD int64_t units_before(int i) const {
     const int n = items();
     const int64_t k = i < n ? i : n - 1;
     if (n == 0 || i == 0) return 0;
-    const int64_t last = kItemUnits + static_cast<int64_t>(weight(n - 1)) * (end(n - 1) - first(n - 1));
+    const int64_t last = units_of(n - 1);
     if (n == 1) return last;
     int64_t tiles = floor_sum(k, G, (static_cast<int64_t>(G) * (before + kTile) + kRows - 1) / kTile);
     if (window) {

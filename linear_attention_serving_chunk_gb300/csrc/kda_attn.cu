@@ -851,44 +851,45 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
 }
 
 // Joins the parts of each item that was cut, o = sum 2^(m_p - m) o_p / sum 2^(m_p - m) l_p.  A lane takes a
-// row, a warp an eighth of the columns: what it reads lies in a row of memory.
-constexpr int kJoinThreads = 256;
+// row and FOURS times four columns: what a warp reads lies in a row of memory.  Bound by latency, so the
+// fewer rows an item has, the fewer columns a lane takes and the more parts are on their way at once: a
+// sequence of a million keys in 152 parts.
+constexpr int kJoinThreads = 512;
+constexpr int kJoinWarps = kJoinThreads / 32;
 
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
-  grid_dependency_wait();
-  grid_launch_dependents();  // (the next call's start, which waits for this kernel's end)
-  const int cta = blockIdx.x, r = blockIdx.y * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
-  const Cut cut = reinterpret_cast<const Cut *>(a.ws)[cta];
-  if (r >= cut.rows) return;
-  constexpr int kFours = D / 4 / 8;  // of a lane
+template <int D, int FOURS, int kAtOnce>
+__device__ void join_row(const AttnArgs &a, const Cut &cut, int r, int four) {
+  const int cta = blockIdx.x, n = cut.last - cta + 1;  // parts: the first is 2 cta + 1, the others 2 c
   const float2 *stats = reinterpret_cast<const float2 *>(a.ws + kCutBytes) + r;
-  const float4 *parts = reinterpret_cast<const float4 *>(a.ws + kCutBytes + kStatBytes) + warp * kFours * kRows + r;
-  const int n = cut.last - cta + 1;  // the first is 2 cta + 1, the others 2 c
-  auto place = [&](int p) { return static_cast<int64_t>(p ? 2 * (cta + p) : 2 * cta + 1); };
-  float4 o[kFours];
+  const float4 *parts = reinterpret_cast<const float4 *>(a.ws + kCutBytes + kStatBytes) + four * kRows + r;
+  float4 o[FOURS];
   float top = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int c = 0; c < kFours; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p0 = 0; p0 < n; p0 += 4) {  // four parts on their way at once
-    float2 s[4];
-    float4 v[4][kFours];
+  for (int c = 0; c < FOURS; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p0 = 0; p0 < n; p0 += kAtOnce) {
+    float2 s[kAtOnce];
+    float4 v[kAtOnce][FOURS];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t at = place(min(p0 + i, n - 1));
-      s[i] = stats[at * kRows];
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int p = min(p0 + i, n - 1);  // (behind the last one: the same again, without weight)
+      const int64_t at = p ? 2 * (cta + p) : 2 * cta + 1;
+      // (in this order, so that all are on their way before the first is used)
+      asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(s[i].x), "=f"(s[i].y) : "l"(stats + at * kRows));
 #pragma unroll
-      for (int c = 0; c < kFours; ++c) v[i][c] = parts[(at * (D / 4) + c) * kRows];
+      for (int c = 0; c < FOURS; ++c)
+        asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[i][c].x), "=f"(v[i][c].y), "=f"(v[i][c].z), "=f"(v[i][c].w) : "l"(parts + (at * (D / 4) + c) * kRows));
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (p0 + i >= n) break;
+    for (int i = 0; i < kAtOnce; ++i)
+      if (p0 + i >= n) s[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
       const float m = fmaxf(top, s[i].x), base = m == -INFINITY ? 0.f : m;
       const float mine = ex2(top - base), f = ex2(s[i].x - base);
       top = m;
       l = l * mine + s[i].y * f;
 #pragma unroll
-      for (int c = 0; c < kFours; ++c) {
+      for (int c = 0; c < FOURS; ++c) {
         o[c].x = o[c].x * mine + v[i][c].x * f, o[c].y = o[c].y * mine + v[i][c].y * f;
         o[c].z = o[c].z * mine + v[i][c].z * f, o[c].w = o[c].w * mine + v[i][c].w * f;
       }
@@ -896,11 +897,31 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   }
   const float f = l == 0.f ? 0.f : 1.f / l;
   const int row = cut.row0 + r, t = row / a.G, g = row - t * a.G;
-  kda_bf16 *out = a.o + (static_cast<int64_t>(cut.token0) + t) * a.ldo + (static_cast<int64_t>(cut.head) * a.G + g) * D + warp * kFours * 4;
+  kda_bf16 *out = a.o + (static_cast<int64_t>(cut.token0) + t) * a.ldo + (static_cast<int64_t>(cut.head) * a.G + g) * D + four * 4;
 #pragma unroll
-  for (int c = 0; c < kFours; c += 2)
-    *reinterpret_cast<uint4 *>(out + 4 * c) = make_uint4(pack(o[c].x * f, o[c].y * f), pack(o[c].z * f, o[c].w * f),
-                                                         pack(o[c + 1].x * f, o[c + 1].y * f), pack(o[c + 1].z * f, o[c + 1].w * f));
+  for (int c = 0; c < FOURS; ++c)
+    *reinterpret_cast<uint2 *>(out + 4 * c) = make_uint2(pack(o[c].x * f, o[c].y * f), pack(o[c].z * f, o[c].w * f));
+}
+
+// Block (cta, y): half y % 2 of the columns of every other 32 rows, from rows 32 (y / 2) on.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads, 1) attn_join_kernel(const AttnArgs a) {
+  grid_dependency_wait();
+  grid_launch_dependents();  // (the next call's start, which waits for this kernel's end)
+  const Cut cut = reinterpret_cast<const Cut *>(a.ws)[blockIdx.x];
+  constexpr int kHalf = D / 8;  // columns in fours
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int half = blockIdx.y & 1, first = blockIdx.y >> 1, lots = ((cut.rows + 31) / 32 - first + 1) / 2;
+  if (lots <= 0) return;
+  const int each = lots == 1 ? kJoinWarps : lots == 2 ? kJoinWarps / 2 : kJoinWarps / 4;  // warps of 32 rows
+  const int fours = kHalf > each ? kHalf / each : 1, lot = warp / each, four = (warp - lot * each) * fours;
+  const int r = (first + 2 * lot) * 32 + lane;
+  if (r >= cut.rows || four >= kHalf) return;
+  const int at = half * kHalf + four;
+  if (fours == 1 && cut.last - static_cast<int>(blockIdx.x) >= 4) join_row<D, 1, 16>(a, cut, r, at);
+  else if (fours == 1) join_row<D, 1, 4>(a, cut, r, at);
+  else if (fours == 2) join_row<D, 2, 4>(a, cut, r, at);
+  else if constexpr (kHalf >= kJoinWarps) join_row<D, 4, 2>(a, cut, r, at);
 }
 
 template <int D>
@@ -924,8 +945,8 @@ cudaError_t run(const AttnArgs &a, const kda_bf16 *cache, cudaStream_t st) {
   if (cudaError_t e = launch_pdl(kernel, dim3(kCtas), dim3(kThreads), Smem<D>::BYTES, st, map, a)) return e;
   if (!a.ws) return cudaSuccess;
   // (of runs of one length the host knows how many rows an item has at most)
-  const int64_t rows = a.runs.cu ? kRows : a.runs.fixed_len * a.G < kRows ? a.runs.fixed_len * a.G : kRows;
-  return launch_pdl(attn_join_kernel<D>, dim3(kCtas, static_cast<unsigned>((rows + 31) / 32)), dim3(kJoinThreads), 0, st, a);
+  const int64_t rows = a.runs.cu ? kRows : a.runs.fixed_len * a.G;
+  return launch_pdl(attn_join_kernel<D>, dim3(kCtas, rows > 32 ? 4 : 2), dim3(kJoinThreads), 0, st, a);
 }
 
 }  // namespace

@@ -102,6 +102,14 @@ def test_shared_out(cached, new, D):
     near(b.call(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), want)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,new", [(16, 1), (5, 7), (16, 6), (16, 11), (3, 60)])
+def test_many_parts(G, new, D):
+    """One head of keys over 110,000 positions: 152 shares for the rows of one item (16 to 180 of them)."""
+    b = Batch([110000 - new], [new], G, 1, D, 128, seed=G)
+    near(b.call(), b.want())
+
+
 @pytest.mark.parametrize("H", [1, 3, 8])
 def test_more_runs_than_threads(H):
     new = [(7 * i) % 4 for i in range(1000)]

@@ -54,10 +54,11 @@ __device__ int64_t place(const AppendArgs &a, int64_t t) {
   return (((static_cast<int64_t>(page) * 2 * a.H) << s.page_shift) + (at & ((1 << s.page_shift) - 1))) * a.D;
 }
 
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a, int per_token, int per_head) {
+// per_token: vectors of a token, k's heads and then v's; inverse: 1 / per_token.
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a, int per_token, float inverse) {
   __shared__ int64_t where[kTokens];
   grid_launch_dependents();  // (the attention's start, which waits for this kernel's end)
-  // vectors of a token: k's heads, then v's
   const int64_t v0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kVectors), t0 = v0 / per_token;
   const int first = static_cast<int>(v0 - t0 * per_token);
   const int tokens = (first + kThreads * kVectors + per_token - 1) / per_token;
@@ -68,13 +69,17 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a,
   int token[kVectors];
   int64_t off[kVectors];
   const int half = per_token / 2;
-  const int64_t plane = static_cast<int64_t>(a.D) << a.seqs.page_shift;
+  const int64_t plane = static_cast<int64_t>(D) << a.seqs.page_shift;
 #pragma unroll
   for (int j = 0; j < kVectors; ++j) {
     const int x = first + j * kThreads + threadIdx.x;
-    token[j] = x / per_token;
-    const int in = x - token[j] * per_token, is_v = in >= half, row = in - (is_v ? half : 0);
-    const int h = row / per_head, e = (row - h * per_head) * 8;
+    // x / per_token, by a product that is off by one at most (integer division takes a third of all instructions)
+    int n = static_cast<int>(static_cast<float>(x) * inverse);
+    n -= n * per_token > x;
+    n += (n + 1) * per_token <= x;
+    token[j] = n;
+    const int in = x - n * per_token, is_v = in >= half, row = in - (is_v ? half : 0);
+    const int h = row / (D / 8), e = row % (D / 8) * 8;
     const int64_t t = t0 + token[j];
     off[j] = (static_cast<int64_t>(is_v ? a.H : 0) + h) * plane + e;
     if (t < a.runs.total)
@@ -93,7 +98,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a,
 cudaError_t kv_append_launch(const AppendArgs &a, cudaStream_t st) {
   const int per_token = 2 * a.H * a.D / 8;
   const int64_t blocks = (a.runs.total * per_token + kThreads * kVectors - 1) / (kThreads * kVectors);
-  kv_append_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(a, per_token, a.D / 8);
+  const dim3 grid(static_cast<unsigned>(blocks));
+  if (a.D == 64) kv_append_kernel<64><<<grid, kThreads, 0, st>>>(a, per_token, 1.f / per_token);
+  else kv_append_kernel<128><<<grid, kThreads, 0, st>>>(a, per_token, 1.f / per_token);
   return cudaGetLastError();
 }
 

@@ -13,23 +13,40 @@
 // Nothing is taken in turn, so the same call gives the same bits.
 //
 // One CTA: two warpgroups, each with its 128 rows' scores, weights and sums in TMEM, a warp that
-// issues the MMAs, and one that looks up pages and loads tiles by TMA.
+// issues the MMAs, one that works out the items, and two that look up pages and load tiles of K and of
+// V by TMA into a ring of 160 KB.
 //   S_w = Q_w K^T         128 x 128 x D, K-major tiles
 //   P_w = exp(..) bf16    in the columns of S_w, read from there by the MMA
 //   O_w += P_w V          128 x D x 128, V as it lies in the cache
 // While one warpgroup turns its scores into weights the tensor core works for the other.  Items of
 // more than 128 rows give each warpgroup 128 of them, with the same tiles.  Those of at most 128
 // (tokens, drafted runs) give both the same rows and every other tile: then the keys are what counts,
-// and two chains hide each other's latency; their sums meet in shared memory at the end.
+// and two chains hide each other's latency; their sums meet in shared memory at the end.  With heads
+// of 64 the sums leave room in TMEM for a third place of scores, which run ahead by one: their MMAs
+// take half as long, and with two places a warpgroup waits for them (955 against 770 us for 4096 tokens
+// behind 28,672, 32 heads of 64).
 //
 // Scores, maxima, sums and O are fp32.  The weights are rounded to bf16 for their product with V,
-// which a row's sum does not see: 2^-9 of each weight, in either direction.  A maximum is kept until
-// a score is more than 2^8 above it in the exponent's base: weights up to 256 lose nothing, and most
-// tiles then need no scaling of O.
+// which a row's sum does not see: by at most 2^-8 of each weight, in either direction.  A maximum is
+// kept until a score is more than 2^8 above it in the exponent's base: weights up to 256 lose nothing, and
+// most tiles then need no scaling of O.
 //
 // A warp whose rows are all beyond the item (three of four in a step of single tokens) computes
 // nothing.  Keys behind a row's position, or behind the window, weigh nothing whatever they are; the
 // rows of V behind the sequence are zeroed, for 0 times what lies there might not be 0.
+//
+// Prompt chunks are bound by the tensor core: 1160 to 1190 us for 4096 tokens behind 28,672, 32 heads of 128
+// over 8 of keys, 1.75 PFLOP/s where a large product of the library reaches 1.93 (1370 us back to back for
+// seconds, at the clock that the power limit leaves).  Single tokens are bound by memory: 645 us for 128
+// sequences of 1000 to 16,000 tokens, 4.49 GB.  Short calls are bound by latency: about 5 us until the
+// first scores, 1 us a tile, 3 us for the join.
+//
+// What it took, us for those chunks / those tokens: the MMAs issued by lane 0 1694 / 675 (each waits for its
+// operands to come into uniform registers); by an elected thread, with the warp's number and TMEM's address
+// uniform for all 1172 / 661; one warp that loads and one that works out items 1163 / 652; two that load
+// 1150 / 641 (heads of 64 in pages of 16: 526 to 357).  Not kept: the weights given in two halves, each as
+// soon as it is there (1804); rows of o through a transposition between lanes, 64 bytes in a row, which makes
+// the compiler spill registers in the loop over the keys (1350); 32-byte stores (no change).
 #include <string.h>
 
 #include <type_traits>
@@ -101,7 +118,9 @@ struct Smem {
   static constexpr int kScores = D == 128 ? 2 : 3;              // places of scores and weights in TMEM
   static constexpr uint32_t kO = kScores * 128;                 // sums behind them
   // Of scores s of an item behind `turn` others: the warpgroup's own, or a third one in turn.
-  __device__ static uint32_t place(uint32_t turn, uint32_t s) { return kScores == 2 ? s & 1 : (turn + s) % kScores; }
+  __device__ static uint32_t place(uint32_t turn, uint32_t s) {
+    return kScores == 2 ? s & 1 : (turn + s) % kScores;
+  }
   static constexpr uint32_t Q = 0;
   static constexpr uint32_t MERGE = kTileBytes;                 // second Q tile, or 128 x 64 fp32
   static constexpr uint32_t STAGE = MERGE + 32 * 1024;
@@ -111,11 +130,14 @@ struct Smem {
                             ODONE = OFULL + 16, IFULL = ODONE + 16, IEMPTY = IFULL + 8 * kItems,
                             MFULL = IEMPTY + 8 * kItems, MEMPTY = MFULL + 8, FIN = MEMPTY + 8;
   static constexpr uint32_t TMEM = FIN + 8;
-  static constexpr uint32_t PLAN = TMEM + 8;                    // int64: units, position, run's first unit; run
+  // int64: the first unit of the share's first run, the run's units for a head, its number; partial sums
+  static constexpr uint32_t PLAN = TMEM + 8;
   static constexpr uint32_t ITEM = PLAN + 8 * 16;
   static constexpr uint32_t STAT = ITEM + sizeof(Item) * kItems;
   static constexpr uint32_t BYTES = STAT + 128 * sizeof(float2);
-  static_assert(BYTES <= 232448 && STAGE % 1024 == 0 && MERGE % 1024 == 0 && STAT % 8 == 0 && TMEM % 8 == 0, "shared memory");
+  static_assert(BYTES <= 232448 && STAGE % 1024 == 0 && MERGE % 1024 == 0 && STAT % 8 == 0 &&
+                    TMEM % 8 == 0,
+                "shared memory");
 };
 
 template <int REGS, bool MORE>
@@ -128,6 +150,28 @@ __device__ __forceinline__ void set_registers() {
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void st_shared4(uint32_t at, float x, float y, float z, float w) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(x), "f"(y), "f"(z), "f"(w)
+               : "memory");
+}
+__device__ __forceinline__ float4 ld_shared4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+// Loads that stay in the order in which they stand.
+__device__ __forceinline__ void ld_in_turn(float2 &v, const float2 *p) {
+  asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p));
+}
+__device__ __forceinline__ void ld_in_turn(float4 &v, const float4 *p) {
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p));
 }
 
 __device__ __forceinline__ bool elect() {
@@ -168,7 +212,8 @@ __device__ __forceinline__ RunAt run_at(const AttnArgs &a, int b, bool &bad) {
     bad = true;
     return RunAt{0, 0, Run{0, 0, a.G, a.window}};
   }
-  return RunAt{static_cast<int>(begin), slot, Run{static_cast<int>(before), static_cast<int>(len), a.G, a.window}};
+  return RunAt{static_cast<int>(begin), slot,
+               Run{static_cast<int>(before), static_cast<int>(len), a.G, a.window}};
 }
 
 template <int D>
@@ -291,291 +336,296 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
   };
 
   if (warp >= 8) {
-  set_registers<kOtherRegs, false>();
-  if (warp == kItemWarp) {
-    // ---- items -----------------------------------------------------------------------------
-    uint32_t given = 0;
-    auto give = [&](const Item &it) -> bool {
-      const uint32_t s = given % kItems;
-      if (!wait(sb + M::IEMPTY + 8 * s, given / kItems + 1)) return false;
-      if (lane == 0) items[s] = it;
-      arrive(sb + M::IFULL + 8 * s);
-      ++given;
-      return true;
-    };
-    if (start < stop) {
-      // 32 runs at a time, one in each lane
-      int b = static_cast<int>(plan[2]), held = b;
-      bool none = false;
-      RunAt lot = run_at(a, min(b + lane, a.runs.n - 1), none), r;
-      auto take = [&]() {
-        if (b >= held + 32) {
-          held = b;
-          lot = run_at(a, min(b + lane, a.runs.n - 1), none);
-        }
-        const int from = b - held;
-        r = RunAt{__shfl_sync(0xffffffffu, lot.begin, from), __shfl_sync(0xffffffffu, lot.slot, from),
-                  Run{__shfl_sync(0xffffffffu, lot.run.before, from), __shfl_sync(0xffffffffu, lot.run.len, from), a.G, a.window}};
+    set_registers<kOtherRegs, false>();
+    if (warp == kItemWarp) {
+      // ---- items -----------------------------------------------------------------------------
+      uint32_t given = 0;
+      auto give = [&](const Item &it) -> bool {
+        const uint32_t s = given % kItems;
+        if (!wait(sb + M::IEMPTY + 8 * s, given / kItems + 1)) return false;
+        if (lane == 0) items[s] = it;
+        arrive(sb + M::IFULL + 8 * s);
+        ++given;
+        return true;
       };
-      take();
-      const int64_t whole = plan[1], x0 = start - plan[0], h0 = attn::quotient(x0, whole), x = x0 - h0 * whole;
-      int h = static_cast<int>(h0), i = 0, hi = r.run.items();
-      while (hi - i > 32) {  // the items around unit x, 32 ways at a time
-        const int step = (hi - i + 31) / 32, c = i + lane * step;
-        const unsigned some = __ballot_sync(0xffffffffu, c < hi && r.run.units_before(c) <= x);
-        i += (31 - __clz(some)) * step;
-        hi = min(hi, i + step);
-      }
-      // and of these, each in a lane, the one that unit x is in
-      const int64_t front = i ? r.run.units_before(i) : 0;
-      const int mine = i + lane < hi ? static_cast<int>(r.run.units_of(i + lane)) : 0;
-      int ends = mine;
+      if (start < stop) {
+        // 32 runs at a time, one in each lane
+        int b = static_cast<int>(plan[2]), held = b;
+        bool none = false;
+        RunAt lot = run_at(a, min(b + lane, a.runs.n - 1), none), r;
+        auto take = [&]() {
+          if (b >= held + 32) {
+            held = b;
+            lot = run_at(a, min(b + lane, a.runs.n - 1), none);
+          }
+          const int from = b - held;
+          auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, from); };
+          r = RunAt{of(lot.begin), of(lot.slot), Run{of(lot.run.before), of(lot.run.len), a.G, a.window}};
+        };
+        take();
+        const int64_t whole = plan[1], x0 = start - plan[0], h0 = attn::quotient(x0, whole);
+        const int64_t x = x0 - h0 * whole;
+        int h = static_cast<int>(h0), i = 0, hi = r.run.items();
+        while (hi - i > 32) {  // the items around unit x, 32 ways at a time
+          const int step = (hi - i + 31) / 32, c = i + lane * step;
+          const unsigned some = __ballot_sync(0xffffffffu, c < hi && r.run.units_before(c) <= x);
+          i += (31 - __clz(some)) * step;
+          hi = min(hi, i + step);
+        }
+        // and of these, each in a lane, the one that unit x is in
+        const int64_t front = i ? r.run.units_before(i) : 0;
+        const int mine = i + lane < hi ? static_cast<int>(r.run.units_of(i + lane)) : 0;
+        int ends = mine;
 #pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const int y = __shfl_up_sync(0xffffffffu, ends, d);
-        if (lane >= d) ends += y;
-      }
-      const int in = __ffs(__ballot_sync(0xffffffffu, front + ends > x)) - 1;
-      i += in;
-      int64_t at = plan[0] + h * whole + front + __shfl_sync(0xffffffffu, ends - mine, in);  // where it begins
-      while (at < stop) {
-        const int lo = r.run.first(i), n = r.run.end(i) - lo, weight = r.run.weight(i);
-        // this share's part of the item, in tiles
-        int from = attn::tiles_before(start - at, n, weight), to = attn::tiles_before(stop - at, n, weight);
-        if (!a.ws) {  // an item belongs to the share in which it begins
-          from = 0;
-          to = at >= start ? n : 0;
+        for (int d = 1; d < 32; d *= 2) {
+          const int y = __shfl_up_sync(0xffffffffu, ends, d);
+          if (lane >= d) ends += y;
         }
-        if (from < to) {
-          Item it;
-          it.row0 = i * kRows;
-          it.rows = r.run.rows_of(i);
-          it.token0 = r.begin;
-          it.head = h;
-          it.before = r.run.before;
-          it.reach = r.run.before + r.run.len;
-          it.lo = lo + from;
-          it.n = to - from;
-          it.slot = r.slot;
-          it.part = from > 0 ? 2 * cta : to < n ? 2 * cta + 1 : -1;
-          if (from == 0 && to < n && lane == 0)
-            reinterpret_cast<Cut *>(a.ws)[cta] = Cut{it.rows, it.row0, it.token0, h, static_cast<int>(attn::quotient(at + attn::kItemUnits + static_cast<int64_t>(n - 1) * weight, each)), {}};
-          if (!give(it)) break;
+        const int in = __ffs(__ballot_sync(0xffffffffu, front + ends > x)) - 1;
+        i += in;
+        int64_t at = plan[0] + h * whole + front + __shfl_sync(0xffffffffu, ends - mine, in);  // where it begins
+        while (at < stop) {
+          const int lo = r.run.first(i), n = r.run.end(i) - lo, weight = r.run.weight(i);
+          // this share's part of the item, in tiles
+          int from = attn::tiles_before(start - at, n, weight), to = attn::tiles_before(stop - at, n, weight);
+          if (!a.ws) {  // an item belongs to the share in which it begins
+            from = 0;
+            to = at >= start ? n : 0;
+          }
+          if (from < to) {
+            Item it;
+            it.row0 = i * kRows;
+            it.rows = r.run.rows_of(i);
+            it.token0 = r.begin;
+            it.head = h;
+            it.before = r.run.before;
+            it.reach = r.run.before + r.run.len;
+            it.lo = lo + from;
+            it.n = to - from;
+            it.slot = r.slot;
+            it.part = from > 0 ? 2 * cta : to < n ? 2 * cta + 1 : -1;
+            if (from == 0 && to < n && lane == 0) {
+              const int64_t last = at + attn::kItemUnits + static_cast<int64_t>(n - 1) * weight;
+              reinterpret_cast<Cut *>(a.ws)[cta] =
+                  Cut{it.rows, it.row0, it.token0, h, static_cast<int>(attn::quotient(last, each)), {}};
+            }
+            if (!give(it)) break;
+          }
+          at += attn::kItemUnits + static_cast<int64_t>(n) * weight;
+          if (++i < r.run.items()) continue;
+          i = 0;
+          if (++h < a.H) continue;
+          h = 0;
+          do {
+            if (++b == a.runs.n) break;
+            take();
+          } while (r.run.len == 0);
+          if (b == a.runs.n) break;
         }
-        at += attn::kItemUnits + static_cast<int64_t>(n) * weight;
-        if (++i < r.run.items()) continue;
-        i = 0;
-        if (++h < a.H) continue;
-        h = 0;
-        do {
-          if (++b == a.runs.n) break;
-          take();
-        } while (r.run.len == 0);
-        if (b == a.runs.n) break;
       }
-    }
-    Item end{};
-    end.rows = -1;
-    if (!gave_up) give(end);
-  } else if (warp != kMmaWarp) {
-    // ---- pages and tiles: one warp loads the keys' and one the values' ------------------------
-    const bool mine_is_v = warp == kLoadVWarp;
-    uint32_t fills = 0, stage = 0, taken = 0;
-    bool wrong = false;
-    const int per_tile = kTile >> a.seqs.page_shift; constexpr int halves = D / 64;
-    // Tile t of keys (or values): pages that no row needs, and those outside the pool, come as zeros.
-    auto load = [&](const Item &it, int t, int values, int first) -> bool {
-      if ((values != 0) != mine_is_v) {  // the other's place in the ring
+      Item end{};
+      end.rows = -1;
+      if (!gave_up) give(end);
+    } else if (warp != kMmaWarp) {
+      // ---- pages and tiles: one warp loads the keys' and one the values' ------------------------
+      const bool mine_is_v = warp == kLoadVWarp;
+      uint32_t fills = 0, stage = 0, taken = 0;
+      bool wrong = false;
+      const int per_tile = kTile >> a.seqs.page_shift;
+      constexpr int halves = D / 64;
+      // Tile t of keys (or values): pages that no row needs, and those outside the pool, come as zeros.
+      auto load = [&](const Item &it, int t, int values, int first) -> bool {
+        if ((values != 0) != mine_is_v) {  // the other's place in the ring
+          ++fills;
+          if (++stage == M::kStages) stage = 0;
+          return true;
+        }
+        if (!wait(sb + M::EMPTY + 8 * stage, fills / M::kStages + 1)) return false;
+        const uint32_t bar = sb + M::FULL + 8 * stage, to = sb + M::STAGE + stage * M::kTileBytes;
+        const int32_t *const row = a.seqs.table + static_cast<int64_t>(it.slot) * a.seqs.max_pages;
+        if (lane == 0) {
+          mbar_expect_tx(bar, M::kTileBytes);
+          const int ahead = (t + 1) * per_tile + 31;  // the table's next line
+          if (ahead < a.seqs.max_pages) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + ahead));
+        }
+        __syncwarp();
+        int plane = 0;
+        if (lane < per_tile) {
+          const int p = lane;
+          const int i = t * per_tile + p, at = i << a.seqs.page_shift;
+          int page = -1;
+          if (at < it.reach && at + (1 << a.seqs.page_shift) > first) {
+            page = row[i];
+            if (page < 0 || page >= a.seqs.n_pages) {
+              page = -1;
+              wrong = true;
+            }
+          }
+          plane = page < 0 ? a.seqs.n_pages * 2 * a.H : (page * 2 + values) * a.H + it.head;
+        }
+        for (int p = 0; p < per_tile; ++p) {
+          const int at = __shfl_sync(0xffffffffu, plane, p);
+          if (elect()) {
+#pragma unroll
+            for (int c = 0; c < halves; ++c)
+              tma_load_3d(to + c * M::kRegion + (p << a.seqs.page_shift) * 128, &map, c * 64, 0, at, bar);
+          }
+        }
+        __syncwarp();
         ++fills;
         if (++stage == M::kStages) stage = 0;
         return true;
-      }
-      if (!wait(sb + M::EMPTY + 8 * stage, fills / M::kStages + 1)) return false;
-      const uint32_t bar = sb + M::FULL + 8 * stage, to = sb + M::STAGE + stage * M::kTileBytes;
-      if (lane == 0) {
-        mbar_expect_tx(bar, M::kTileBytes);
-        const int ahead = (t + 1) * per_tile + 31;  // the table's next line
-        if (ahead < a.seqs.max_pages)
-          asm volatile("prefetch.global.L1 [%0];" ::"l"(a.seqs.table + static_cast<int64_t>(it.slot) * a.seqs.max_pages + ahead));
-      }
-      __syncwarp();
-      int plane = 0;
-      if (lane < per_tile) {
-        const int p = lane;
-        const int i = t * per_tile + p, at = i << a.seqs.page_shift;
-        int page = -1;
-        if (at < it.reach && at + (1 << a.seqs.page_shift) > first) {
-          page = a.seqs.table[static_cast<int64_t>(it.slot) * a.seqs.max_pages + i];
-          if (page < 0 || page >= a.seqs.n_pages) {
-            page = -1;
-            wrong = true;
-          }
+      };
+      auto load_item = [&](const Item &it) -> bool {
+        const int first = a.window ? max(it.before + it.row0 / a.G - a.window + 1, 0) : 0;
+        const int n = it.n, lo = it.lo;
+        // in the order in which the MMAs want them: the scores run ahead of the sums
+        const int ahead = it.rows > 128 ? (M::kScores + 1) / 2 : M::kScores;
+        for (int j = 0; j < min(ahead, n); ++j)
+          if (!load(it, lo + j, 0, first)) return false;
+        for (int j = 0; j < n; ++j) {
+          if (!load(it, lo + j, 1, first)) return false;
+          if (j + ahead < n && !load(it, lo + j + ahead, 0, first)) return false;
         }
-        plane = page < 0 ? a.seqs.n_pages * 2 * a.H : (page * 2 + values) * a.H + it.head;
-      }
-      for (int p = 0; p < per_tile; ++p) {
-        const int at = __shfl_sync(0xffffffffu, plane, p);
-        if (elect()) {
-#pragma unroll
-          for (int c = 0; c < halves; ++c)
-            tma_load_3d(to + c * M::kRegion + (p << a.seqs.page_shift) * 128, &map, c * 64, 0, at, bar);
-        }
-      }
-      __syncwarp();
-      ++fills;
-      if (++stage == M::kStages) stage = 0;
-      return true;
-    };
-    auto load_item = [&](const Item &it) -> bool {
-      const int first = a.window ? max(it.before + it.row0 / a.G - a.window + 1, 0) : 0;
-      const int n = it.n, lo = it.lo;
-      // in the order in which the MMAs want them: the scores run ahead of the sums
-      const int ahead = it.rows > 128 ? (M::kScores + 1) / 2 : M::kScores;
-      for (int j = 0; j < min(ahead, n); ++j)
-        if (!load(it, lo + j, 0, first)) return false;
-      for (int j = 0; j < n; ++j) {
-        if (!load(it, lo + j, 1, first)) return false;
-        if (j + ahead < n && !load(it, lo + j + ahead, 0, first)) return false;
-      }
-      return true;
-    };
+        return true;
+      };
 
-    for (;;) {
-      const uint32_t s = taken % kItems;
-      if (!wait(sb + M::IFULL + 8 * s, taken / kItems)) break;
-      const Item it = items[s];
-      arrive(sb + M::IEMPTY + 8 * s);
-      ++taken;
-      if (it.rows < 0 || !load_item(it)) break;
-    }
-    if (__any_sync(0xffffffffu, wrong) && lane == 0) atomicOr(a.status, KDA_ERR_SHAPE);
-    if (gave_up) {  // the tiles on their way
-      const uint32_t n = min(fills, static_cast<uint32_t>(M::kStages));
-      for (uint32_t f = fills - n; f < fills; ++f)
-        mbar_wait_bounded(sb + M::FULL + 8 * (f % M::kStages), (f / M::kStages) & 1u, kPolls);
-    }
-  } else {
-    // ---- MMAs ------------------------------------------------------------------------------
-    constexpr uint32_t ID_S = idesc_mma(128, kTile, kFmtBF16, kFmtBF16, 0, 0);
-    constexpr uint32_t ID_O = idesc_mma(128, D, kFmtBF16, kFmtBF16, 0, 1);
-    uint32_t used = 0, stage = 0, taken = 0, q_n[2] = {0, 0}, p_bits = 0;
-    auto p_phase = [&](uint32_t place) {  // each place's phases of P, one after another
-      const uint32_t phase = p_bits >> place;
-      p_bits ^= 1u << place;
-      return phase;
-    };
-    // (descriptors from an address that the compiler cannot see through: hoisted out of the loop, the
-    // sums of all steps would take most of this warp's registers)
-    // Scores are announced to each warpgroup in turn on two barriers of its own: it waits for each of its
-    // scores, and for no other's, and at most one more is there before it has taken the last.
-    uint32_t announced[2] = {0, 0};
-    auto scores = [&](int place, int w, int q, uint32_t k) {
-      const uint32_t full = sb + M::SFULL + 16 * w + 8 * (announced[w] & 1);
-      ++announced[w];
-      if (elect()) {
-        uint32_t qa = sb + M::Q + q * M::kTileBytes;
-        asm volatile("" : "+r"(qa), "+r"(k));
-        const uint64_t qd = sw128_desc(qa, 16, 1024), kd = sw128_desc(k, 16, 1024);
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const uint32_t off = ((s >> 2) * M::kRegion + (s & 3) * 32) >> 4;
-          mma_f16(tmem + place * 128, qd + off, kd + off, ID_S, s > 0);
-        }
-        mma_commit(full);
-      }
-      __syncwarp();
-    };
-    auto weighted = [&](int place, int w, uint32_t v, bool add) {
-      if (elect()) {
-        uint32_t p = tmem + place * 128, o = tmem + M::kO + w * D;
-        asm volatile("" : "+r"(p), "+r"(v));
-        const uint64_t vd = sw128_desc(v, M::kRegion, 1024);
-#pragma unroll
-        for (int s = 0; s < kTile / 16; ++s)
-          mma_ta(o, p + 8 * s, vd + ((s * 2048) >> 4), ID_O, add || s > 0);
-      }
-      __syncwarp();
-    };
-    auto commit = [&](uint32_t bar) {
-      if (elect()) mma_commit(bar);
-      __syncwarp();
-    };
-    auto tile = [&](uint32_t &at, uint32_t &free) -> bool {  // the next one in the ring
-      at = sb + M::STAGE + stage * M::kTileBytes;
-      free = sb + M::EMPTY + 8 * stage;
-      const bool ok = wait(sb + M::FULL + 8 * stage, used / M::kStages);
-      ++used;
-      if (++stage == M::kStages) stage = 0;
-      return ok;
-    };
-    auto run = [&]() {
-      for (uint32_t turn = 0;;) {  // scores of the items before
+      for (;;) {
         const uint32_t s = taken % kItems;
-        if (!wait(sb + M::IFULL + 8 * s, taken / kItems)) return;
+        if (!wait(sb + M::IFULL + 8 * s, taken / kItems)) break;
         const Item it = items[s];
         arrive(sb + M::IEMPTY + 8 * s);
         ++taken;
-        if (it.rows < 0) return;
-        const bool both = it.rows > 128;  // both warpgroups take every tile
-        const int n = it.n;
-        // the tile in which the sequence ends inside a page: V's rows from there on
-        const int zero_tile = (it.reach & ((1 << a.seqs.page_shift) - 1)) ? it.reach / kTile - it.lo : -1;
-        auto clear = [&](uint32_t v) {
-          const int r0 = it.reach % kTile, r1 = (r0 | ((1 << a.seqs.page_shift) - 1)) + 1;
-          for (int x = lane; x < (r1 - r0) * (D / 8); x += 32) {
-            const int r = r0 + x / (D / 8), c = x % (D / 8);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + (c >> 3) * M::kRegion + r * 128 + (c & 7) * 16), "r"(0) : "memory");
-          }
-          fence_proxy_async();
-          __syncwarp();
-        };
-        // Scores s = 0, 1, ... of the item go to the warpgroups in turn, and to the places in TMEM: scores
-        // s + kScores follow the sum that has read the weights s (MMAs are done in order).
-        const int all = both ? 2 * n : n;
-        uint32_t k = 0, v = 0, k_free = 0, v_free = 0;
-        if (!wait(sb + M::QREADY, q_n[0]++)) return;
-        if (both && !wait(sb + M::QREADY + 8, q_n[1]++)) return;
-        tc_fence_after();
-        // (twice in the code, for what it tests to be known, and two steps at a time, for the same reason)
-        auto steps = [&](auto wide) -> bool {
-          constexpr bool two = decltype(wide)::value;  // the tiles serve both warpgroups
-          auto next_keys = [&](int s) -> bool { return (two && (s & 1)) || tile(k, k_free); };
-          auto next_scores = [&](int s) {
-            const bool second = s & 1;
-            scores(M::place(turn, s), second, two && second, k);
-            if (!two || second) commit(k_free);
-          };
-          for (int s = 0; s < min(M::kScores, all); ++s) {
-            if (!next_keys(s)) return false;
-            next_scores(s);
-          }
-#pragma unroll 2
-          for (int s = 0; s < all; ++s) {
-            const int w = s & 1, place = M::place(turn, s);
-            if (!(two && w)) {
-              if (!tile(v, v_free)) return false;
-              if ((two ? s >> 1 : s) == zero_tile) clear(v);
-            }
-            const bool more = s + M::kScores < all;
-            if (more && !next_keys(s + M::kScores)) return false;
-            if (!wait(sb + M::PREADY + 8 * place, p_phase(place))) return false;
-            tc_fence_after();
-            weighted(place, w, v, s > 1);
-            if (!two || w) commit(v_free);
-            if (M::kScores > 2) commit(sb + M::ODONE + 8 * w);
-            if (s + 2 >= all) commit(sb + M::OFULL + 8 * w);
-            if (more) next_scores(s + M::kScores);
-          }
-          return true;
-        };
-        if (!(both ? steps(std::true_type{}) : steps(std::false_type{}))) return;
-        turn += all;
+        if (it.rows < 0 || !load_item(it)) break;
       }
-    };
-    run();
-    commit(sb + M::FIN);
-    mbar_wait_bounded(sb + M::FIN, 0, kPolls);
-  }
+      if (__any_sync(0xffffffffu, wrong) && lane == 0) atomicOr(a.status, KDA_ERR_SHAPE);
+      if (gave_up) {  // the tiles on their way
+        const uint32_t n = min(fills, static_cast<uint32_t>(M::kStages));
+        for (uint32_t f = fills - n; f < fills; ++f)
+          mbar_wait_bounded(sb + M::FULL + 8 * (f % M::kStages), (f / M::kStages) & 1u, kPolls);
+      }
+    } else {
+      // ---- MMAs ------------------------------------------------------------------------------
+      constexpr uint32_t ID_S = idesc_mma(128, kTile, kFmtBF16, kFmtBF16, 0, 0);
+      constexpr uint32_t ID_O = idesc_mma(128, D, kFmtBF16, kFmtBF16, 0, 1);
+      uint32_t used = 0, stage = 0, taken = 0, q_n[2] = {0, 0}, p_bits = 0;
+      auto p_phase = [&](uint32_t place) {  // each place's phases of P, one after another
+        const uint32_t phase = p_bits >> place;
+        p_bits ^= 1u << place;
+        return phase;
+      };
+      // Scores are announced to each warpgroup in turn on two barriers of its own: it waits for each of its
+      // scores, and for no other's, and at most one more is there before it has taken the last.  (Descriptors
+      // from an address that the compiler cannot see through: hoisted out of the loop, the sums of all steps
+      // would take most of this warp's registers.)
+      uint32_t announced[2] = {0, 0};
+      auto scores = [&](int place, int w, int q, uint32_t k) {
+        const uint32_t full = sb + M::SFULL + 16 * w + 8 * (announced[w] & 1);
+        ++announced[w];
+        if (elect()) {
+          uint32_t qa = sb + M::Q + q * M::kTileBytes;
+          asm volatile("" : "+r"(qa), "+r"(k));
+          const uint64_t qd = sw128_desc(qa, 16, 1024), kd = sw128_desc(k, 16, 1024);
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t off = ((s >> 2) * M::kRegion + (s & 3) * 32) >> 4;
+            mma_f16(tmem + place * 128, qd + off, kd + off, ID_S, s > 0);
+          }
+          mma_commit(full);
+        }
+        __syncwarp();
+      };
+      auto weighted = [&](int place, int w, uint32_t v, bool add) {
+        if (elect()) {
+          uint32_t p = tmem + place * 128, o = tmem + M::kO + w * D;
+          asm volatile("" : "+r"(p), "+r"(v));
+          const uint64_t vd = sw128_desc(v, M::kRegion, 1024);
+#pragma unroll
+          for (int s = 0; s < kTile / 16; ++s)
+            mma_ta(o, p + 8 * s, vd + ((s * 2048) >> 4), ID_O, add || s > 0);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint32_t bar) {
+        if (elect()) mma_commit(bar);
+        __syncwarp();
+      };
+      auto tile = [&](uint32_t &at, uint32_t &free) -> bool {  // the next one in the ring
+        at = sb + M::STAGE + stage * M::kTileBytes;
+        free = sb + M::EMPTY + 8 * stage;
+        const bool ok = wait(sb + M::FULL + 8 * stage, used / M::kStages);
+        ++used;
+        if (++stage == M::kStages) stage = 0;
+        return ok;
+      };
+      auto run = [&]() {
+        for (uint32_t turn = 0;;) {  // scores of the items before
+          const uint32_t s = taken % kItems;
+          if (!wait(sb + M::IFULL + 8 * s, taken / kItems)) return;
+          const Item it = items[s];
+          arrive(sb + M::IEMPTY + 8 * s);
+          ++taken;
+          if (it.rows < 0) return;
+          const bool both = it.rows > 128;  // both warpgroups take every tile
+          const int n = it.n;
+          // the tile in which the sequence ends inside a page: V's rows from there on
+          const int zero_tile = (it.reach & ((1 << a.seqs.page_shift) - 1)) ? it.reach / kTile - it.lo : -1;
+          auto clear = [&](uint32_t v) {
+            const int r0 = it.reach % kTile, r1 = (r0 | ((1 << a.seqs.page_shift) - 1)) + 1;
+            for (int x = lane; x < (r1 - r0) * (D / 8); x += 32) {
+              const int r = r0 + x / (D / 8), c = x % (D / 8);
+              st_shared4(v + (c >> 3) * M::kRegion + r * 128 + (c & 7) * 16, 0.f, 0.f, 0.f, 0.f);
+            }
+            fence_proxy_async();
+            __syncwarp();
+          };
+          // Scores s = 0, 1, ... of the item go to the warpgroups in turn, and to the places in TMEM: scores
+          // s + kScores follow the sum that has read the weights s (MMAs are done in order).
+          const int all = both ? 2 * n : n;
+          uint32_t k = 0, v = 0, k_free = 0, v_free = 0;
+          if (!wait(sb + M::QREADY, q_n[0]++)) return;
+          if (both && !wait(sb + M::QREADY + 8, q_n[1]++)) return;
+          tc_fence_after();
+          // (twice in the code, for what it tests to be known, and two steps at a time, for the same reason)
+          auto steps = [&](auto wide) -> bool {
+            constexpr bool two = decltype(wide)::value;  // the tiles serve both warpgroups
+            auto next_keys = [&](int s) -> bool { return (two && (s & 1)) || tile(k, k_free); };
+            auto next_scores = [&](int s) {
+              const bool second = s & 1;
+              scores(M::place(turn, s), second, two && second, k);
+              if (!two || second) commit(k_free);
+            };
+            for (int s = 0; s < min(M::kScores, all); ++s) {
+              if (!next_keys(s)) return false;
+              next_scores(s);
+            }
+#pragma unroll 2
+            for (int s = 0; s < all; ++s) {
+              const int w = s & 1, place = M::place(turn, s);
+              if (!(two && w)) {
+                if (!tile(v, v_free)) return false;
+                if ((two ? s >> 1 : s) == zero_tile) clear(v);
+              }
+              const bool more = s + M::kScores < all;
+              if (more && !next_keys(s + M::kScores)) return false;
+              if (!wait(sb + M::PREADY + 8 * place, p_phase(place))) return false;
+              tc_fence_after();
+              weighted(place, w, v, s > 1);
+              if (!two || w) commit(v_free);
+              if (M::kScores > 2) commit(sb + M::ODONE + 8 * w);
+              if (s + 2 >= all) commit(sb + M::OFULL + 8 * w);
+              if (more) next_scores(s + M::kScores);
+            }
+            return true;
+          };
+          if (!(both ? steps(std::true_type{}) : steps(std::false_type{}))) return;
+          turn += all;
+        }
+      };
+      run();
+      commit(sb + M::FIN);
+      mbar_wait_bounded(sb + M::FIN, 0, kPolls);
+    }
   } else {
     set_registers<kRowRegs, true>();
     // ---- weights and results ---------------------------------------------------------------
@@ -600,14 +650,17 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       constexpr int kAcross = D / 8, kAtOnce = 128 / kAcross;
       const int c = (tid & 127) % kAcross, row_of = it.rows > 128 ? w * 128 : 0;
       const uint32_t col = sb + M::Q + w * M::kTileBytes + (c >> 3) * M::kRegion;
-      const kda_bf16 *const q = a.q + static_cast<int64_t>(it.token0) * a.ldq + static_cast<int64_t>(it.head) * a.G * D + c * 8;
+      const kda_bf16 *const q = a.q + static_cast<int64_t>(it.token0) * a.ldq +
+                                static_cast<int64_t>(it.head) * a.G * D + c * 8;
       const int i0 = (tid & 127) / kAcross, step_t = kAtOnce / a.G, step_g = kAtOnce - step_t * a.G;
       int t = (it.row0 + row_of + i0) / a.G, g = it.row0 + row_of + i0 - t * a.G;
       const int rows = min(it.rows - row_of, 128);
 #pragma unroll 4
       for (int i = i0; i < rows; i += kAtOnce) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(col + i * 128 + (((c & 7) ^ (i & 7)) << 4)),
-                     "l"(__cvta_generic_to_global(q + t * a.ldq + g * D)) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         col + i * 128 + (((c & 7) ^ (i & 7)) << 4)),
+                     "l"(__cvta_generic_to_global(q + t * a.ldq + g * D))
+                     : "memory");
         t += step_t;
         if ((g += step_g) >= a.G) {
           g -= a.G;
@@ -650,7 +703,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       };
       auto put_stats = [&]() {
         if (part && valid)
-          reinterpret_cast<float2 *>(a.ws + kCutBytes)[static_cast<int64_t>(it.part) * kRows + row_of + r] = make_float2(m, l);
+          reinterpret_cast<float2 *>(a.ws + kCutBytes)[it.part * kRows + row_of + r] = make_float2(m, l);
       };
       if (both || it.n == 1) {
         const float f = l == 0.f ? 0.f : 1.f / l;
@@ -686,7 +739,8 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((c * 8 + i) ^ (r & 15)) << 4)), "f"(o[4 * i]), "f"(o[4 * i + 1]), "f"(o[4 * i + 2]), "f"(o[4 * i + 3]) : "memory");
+                st_shared4(at + (((c * 8 + i) ^ (r & 15)) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2],
+                           o[4 * i + 3]);
             }
           }
           arrive(sb + M::MFULL);
@@ -711,10 +765,11 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                float x[4];
-                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(at + (((c * 8 + i) ^ (r & 15)) << 4)) : "memory");
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[4 * i + e] = o[4 * i + e] * mine + x[e] * other;
+                const float4 x = ld_shared4(at + (((c * 8 + i) ^ (r & 15)) << 4));
+                o[4 * i] = o[4 * i] * mine + x.x * other;
+                o[4 * i + 1] = o[4 * i + 1] * mine + x.y * other;
+                o[4 * i + 2] = o[4 * i + 2] * mine + x.z * other;
+                o[4 * i + 3] = o[4 * i + 3] * mine + x.w * other;
               }
               put(o, c0 + c, inv);
             }
@@ -874,10 +929,9 @@ __device__ void join_row(const AttnArgs &a, const Cut &cut, int r, int four) {
       const int p = min(p0 + i, n - 1);  // (behind the last one: the same again, without weight)
       const int64_t at = p ? 2 * (cta + p) : 2 * cta + 1;
       // (in this order, so that all are on their way before the first is used)
-      asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(s[i].x), "=f"(s[i].y) : "l"(stats + at * kRows));
+      ld_in_turn(s[i], stats + at * kRows);
 #pragma unroll
-      for (int c = 0; c < FOURS; ++c)
-        asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[i][c].x), "=f"(v[i][c].y), "=f"(v[i][c].z), "=f"(v[i][c].w) : "l"(parts + (at * (D / 4) + c) * kRows));
+      for (int c = 0; c < FOURS; ++c) ld_in_turn(v[i][c], parts + (at * (D / 4) + c) * kRows);
     }
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i)
@@ -897,10 +951,12 @@ __device__ void join_row(const AttnArgs &a, const Cut &cut, int r, int four) {
   }
   const float f = l == 0.f ? 0.f : 1.f / l;
   const int row = cut.row0 + r, t = row / a.G, g = row - t * a.G;
-  kda_bf16 *out = a.o + (static_cast<int64_t>(cut.token0) + t) * a.ldo + (static_cast<int64_t>(cut.head) * a.G + g) * D + four * 4;
+  kda_bf16 *out = a.o + (static_cast<int64_t>(cut.token0) + t) * a.ldo +
+                  (static_cast<int64_t>(cut.head) * a.G + g) * D + four * 4;
 #pragma unroll
   for (int c = 0; c < FOURS; ++c)
-    *reinterpret_cast<uint2 *>(out + 4 * c) = make_uint2(pack(o[c].x * f, o[c].y * f), pack(o[c].z * f, o[c].w * f));
+    *reinterpret_cast<uint2 *>(out + 4 * c) =
+        make_uint2(pack(o[c].x * f, o[c].y * f), pack(o[c].z * f, o[c].w * f));
 }
 
 // Block (cta, y): half y % 2 of the columns of every other 32 rows, from rows 32 (y / 2) on.
@@ -931,7 +987,8 @@ cudaError_t run(const AttnArgs &a, const kda_bf16 *cache, cudaStream_t st) {
   CUtensorMap map;
   memset(&map, 0, sizeof(map));
   const int page = 1 << a.seqs.page_shift;
-  const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(a.seqs.n_pages) * 2 * a.H};
+  const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(page),
+                              static_cast<cuuint64_t>(a.seqs.n_pages) * 2 * a.H};
   const cuuint64_t strides[2] = {2 * D, static_cast<cuuint64_t>(2) * D * page};
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(page), 1};
   const cuuint32_t step[3] = {1, 1, 1};

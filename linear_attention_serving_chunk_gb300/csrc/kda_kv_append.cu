@@ -2,7 +2,9 @@
 //
 // Bound by memory: each row of k and v is read once and written once.  A block takes kVectors 16-byte
 // vectors a thread of consecutive tokens; the run, slot and page of each of its tokens are looked up
-// once, by one thread each, and the vectors are all in flight before the first is stored.
+// once, by one thread each, and the vectors are all in flight before the first is stored.  44 us for 32,768
+// packed tokens of 8 heads of 128 (268 MB, 6.1 TB/s); with 8 vectors a thread 47, with 2 47, with blocks
+// of 512 threads 51, with streaming loads or stores no change.
 #include "kda_paged.cuh"
 #include "kda_pdl.cuh"
 
@@ -73,7 +75,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a,
 #pragma unroll
   for (int j = 0; j < kVectors; ++j) {
     const int x = first + j * kThreads + threadIdx.x;
-    // x / per_token, by a product that is off by one at most (integer division takes a third of all instructions)
+    // x / per_token, by a product that is off by one at most (the integer division took 1.4 of 45 us)
     int n = static_cast<int>(static_cast<float>(x) * inverse);
     n -= n * per_token > x;
     n += (n + 1) * per_token <= x;

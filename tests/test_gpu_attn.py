@@ -1,4 +1,6 @@
 """Attention over a paged cache on the GPU, against the plain form in 64 bits (tests/paged_ref.py)."""
+import random
+
 import pytest
 import torch
 
@@ -189,6 +191,22 @@ def test_bad_entries():
     o = b.call()
     assert kda.device_status() == kda.KDA_ERR_SHAPE
     assert torch.equal(o[:2], good[:2]) and torch.equal(o[9:], good[9:])
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_drawn_batches(seed):
+    """Random heads, pages, windows, contexts and runs, with and without a workspace."""
+    rng = random.Random(seed)
+    H, D, page = rng.choice([1, 2, 3, 5]), rng.choice([64, 128]), rng.choice([16, 32, 64, 128])
+    n, G = rng.randint(1, 12), rng.choice([1, 2, 3, 4, 6, 8, 13, 33])
+    new = [rng.choice([0, 1, 1, rng.randint(2, 8), rng.randint(1, 400)]) for _ in range(n)]
+    cached = [rng.choice([0, rng.randint(1, 130), rng.randint(1, 3000)]) for _ in range(n)]
+    if rng.random() < 0.3:
+        new = [rng.randint(1, 3)] * n
+    window = rng.choice([0, 0, 1, rng.randint(2, 300), rng.randint(100, 4000)])
+    b = Batch(cached, new, G * H, H, D, page, seed=seed, wide=rng.choice([0, 8, 24]))
+    kw = dict(workspace=torch.empty(0, dtype=torch.uint8, device="cuda")) if rng.random() < 0.3 else {}
+    near(b.call(window=window, **kw), b.want(window))
 
 
 def test_rows_outside_all_runs_and_in_place():

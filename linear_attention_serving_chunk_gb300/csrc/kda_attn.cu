@@ -204,16 +204,21 @@ struct RunAt {
   Run run;
 };
 __device__ __forceinline__ RunAt run_at(const AttnArgs &a, int b, bool &bad) {
-  int64_t begin, len, used, before;
-  int slot;
-  bool ok = run_range(a.runs, b, begin, len, used) && run_slot(a.seqs, b, slot, before);
-  if (ok && before + len > (static_cast<int64_t>(a.seqs.max_pages) << a.seqs.page_shift)) ok = false;
+  int64_t begin = b * a.runs.fixed_len, end = begin + a.runs.fixed_len;
+  // (the offsets and the slot are on their way at once: this is on every call's way to its first tile)
+  const int slot = a.seqs.slots ? a.seqs.slots[b] : b;
+  bool ok = true;
+  if (a.runs.cu) ok = seq_range(a.runs.cu, b, a.runs.total, begin, end);
+  const int64_t len = end - begin;
+  int before = -1;
+  if (slot >= 0 && slot < a.seqs.n_slots) before = a.seqs.lens[slot];
+  ok = ok && before >= 0 &&
+       before + len <= (static_cast<int64_t>(a.seqs.max_pages) << a.seqs.page_shift);
   if (!ok) {
     bad = true;
     return RunAt{0, 0, Run{0, 0, a.G, a.window}};
   }
-  return RunAt{static_cast<int>(begin), slot,
-               Run{static_cast<int>(before), static_cast<int>(len), a.G, a.window}};
+  return RunAt{static_cast<int>(begin), slot, Run{before, static_cast<int>(len), a.G, a.window}};
 }
 
 template <int D>

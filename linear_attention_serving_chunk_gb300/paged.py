@@ -12,6 +12,8 @@ A step of a batch of runs (prompt chunks, single tokens, drafted runs)::
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import KDA_OK, KDAError, lib
@@ -86,8 +88,14 @@ def kv_append(k, v, cache, table, lens, slots=None, cu_seqlens=None, stream=None
         raise KDAError("kda_kv_append", st)
 
 
+@functools.lru_cache(maxsize=256)  # (a tenth of a call's checks for the same sizes again)
 def attn_workspace_bytes(n, total_tokens, Hq, H, D):
     return int(lib().kda_attn_paged_workspace_bytes(n, total_tokens, Hq, H, D))
+
+
+@functools.lru_cache(maxsize=256)
+def _pages_workspace_bytes(n):
+    return int(lib().kda_pages_workspace_bytes(n))
 
 
 def attn_paged(q, cache, table, lens, slots=None, cu_seqlens=None, scale=None, window=0, o=None,
@@ -107,10 +115,9 @@ def attn_paged(q, cache, table, lens, slots=None, cu_seqlens=None, scale=None, w
         raise ValueError(f"cache has heads of {D_c}, q of {D}")
     tp, most, lp, n_slots = _table(table, lens, dev)
     o, op, ldo = _result(o, (total, Hq, D), dev, stream)
-    L = lib()
     workspace, wp, size = _scratch(
-        workspace, L.kda_attn_paged_workspace_bytes(n, total, Hq, H, D), dev, stream)
-    st = L.kda_attn_paged(*_rows(q, "q", (total, Hq, D), dev), cu, n, total, Hq, H, D, at, n_pages,
+        workspace, attn_workspace_bytes(n, total, Hq, H, D), dev, stream)
+    st = lib().kda_attn_paged(*_rows(q, "q", (total, Hq, D), dev), cu, n, total, Hq, H, D, at, n_pages,
                           page, tp, most, lp, n_slots, _dense(slots, "slots", _I32, (n,), dev),
                           D ** -0.5 if scale is None else scale, _int32(window, "window"), op, ldo, wp, size,
                           _on(stream, dev))
@@ -152,9 +159,8 @@ def pages_fork(cache, table, lens, src, dst, left=None, workspace=None, stream=N
         raise TypeError("src and dst must be int32 tensors")
     n = src.numel()
     left, cp = _count(left, "left", dev, stream)
-    L = lib()
-    workspace, wp, size = _scratch(workspace, L.kda_pages_workspace_bytes(n), dev, stream)
-    st = L.kda_pages_fork(at, layers, n_pages, H, page, D, tp, most, lp, n_slots,
+    workspace, wp, size = _scratch(workspace, _pages_workspace_bytes(n), dev, stream)
+    st = lib().kda_pages_fork(at, layers, n_pages, H, page, D, tp, most, lp, n_slots,
                           _dense(src, "src", _I32, (n,), dev), _dense(dst, "dst", _I32, (n,), dev),
                           n, cp, wp, size, _on(stream, dev))
     if st != KDA_OK:
@@ -172,9 +178,8 @@ def pages_compact(cache, table, lens, table_out=None, used=None, workspace=None,
     if table_out is None:
         table_out = _empty((n_slots, most), _I32, dev, stream)
     used, cp = _count(used, "used", dev, stream)
-    L = lib()
-    workspace, wp, size = _scratch(workspace, L.kda_pages_workspace_bytes(n_pages), dev, stream)
-    st = L.kda_pages_compact(at, layers, n_pages, H, page, D, tp, most, lp, n_slots,
+    workspace, wp, size = _scratch(workspace, _pages_workspace_bytes(n_pages), dev, stream)
+    st = lib().kda_pages_compact(at, layers, n_pages, H, page, D, tp, most, lp, n_slots,
                              _dense(table_out, "table_out", _I32, (n_slots, most), dev), cp, wp,
                              size, _on(stream, dev))
     if st != KDA_OK:

@@ -443,8 +443,8 @@ int kda_verify_draft(const void *target, const void *draft, int prob_bytes, int 
 /*
  * The paged cache: what the full attention layers of a hybrid model keep of
  * their sequences, beside the recurrent layers' states, on the same kind of
- * batch.  These operators are additions of this library; the pages have no
- * counterpart.
+ * batch.  These operators are additions of this library; the report and the
+ * summary have no counterpart.
  *
  *   cache   bf16 [n_pages, 2, H, page, D] of one layer: for each page the keys
  *           and then the values of H heads, `page` tokens each.  The operators

@@ -35,7 +35,8 @@
 // nothing.  Keys behind a row's position, or behind the window, weigh nothing whatever they are; the
 // rows of V behind the sequence are zeroed, for 0 times what lies there might not be 0.
 //
-// Prompt chunks are bound by the tensor core: 1160 to 1190 us for 4096 tokens behind 28,672, 32 heads of 128
+// Prompt chunks are bound by the products, and those by shared memory: the scores of two tiles read 128 KB in
+// their 1024 cycles while 64 KB of K and V are written.  1160 to 1190 us for 4096 tokens behind 28,672, 32 heads of 128
 // over 8 of keys, 1.75 PFLOP/s where a large product of the library reaches 1.93 (1370 us back to back for
 // seconds, at the clock that the power limit leaves).  Single tokens are bound by memory: 645 us for 128
 // sequences of 1000 to 16,000 tokens, 4.49 GB.  Short calls are bound by latency: about 5 us until the

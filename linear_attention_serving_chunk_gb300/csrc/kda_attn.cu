@@ -133,7 +133,8 @@ struct Smem {
   static constexpr uint32_t TMEM = FIN + 8;
   // int64: the first unit of the share's first run, the run's units for a head, its number; partial sums
   static constexpr uint32_t PLAN = TMEM + 8;
-  static constexpr uint32_t ITEM = PLAN + 8 * 16;
+  static constexpr uint32_t FIRST = PLAN + 8 * 16;                // that run
+  static constexpr uint32_t ITEM = FIRST + 32;
   static constexpr uint32_t STAT = ITEM + sizeof(Item) * kItems;
   static constexpr uint32_t BYTES = STAT + 128 * sizeof(float2);
   static_assert(BYTES <= 232448 && STAGE % 1024 == 0 && MERGE % 1024 == 0 && STAT % 8 == 0 &&
@@ -204,6 +205,7 @@ struct RunAt {
   int begin, slot;
   Run run;
 };
+static_assert(sizeof(RunAt) <= 32, "Smem::FIRST");
 __device__ __forceinline__ RunAt run_at(const AttnArgs &a, int b, bool &bad) {
   int64_t begin = b * a.runs.fixed_len, end = begin + a.runs.fixed_len;
   // (the offsets and the slot are on their way at once: this is on every call's way to its first tile)
@@ -269,10 +271,12 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
   // This CTA's share: all units, then the run in which the share begins.
   int64_t *const plan = reinterpret_cast<int64_t *>(smem + M::PLAN);
   bool bad = false;
-  int64_t units = 0, mine = 0;
+  int64_t units = 0, whole = 0;  // whole: those of one head of this thread's run
+  RunAt run{};
   for (int b = tid; b < a.runs.n; b += kThreads) {
-    mine = run_at(a, b, bad).run.units() * a.H;
-    units += mine;
+    run = run_at(a, b, bad);
+    whole = run.run.units();
+    units += whole * a.H;
   }
   auto sum_up = [&](int64_t v, int64_t &before) {  // over the block; `before`: over the threads before
     int64_t x = v;
@@ -296,10 +300,11 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
   units = sum_up(units, before);
   const int64_t each = attn::share(units), start = each * cta, stop = min(start + each, units);
   auto found = [&](int b) {
-    if (before <= start && start < before + mine) {
+    if (before <= start && start < before + whole * a.H) {
       plan[0] = before;
-      plan[1] = attn::quotient(mine, a.H);
+      plan[1] = whole;
       plan[2] = b;
+      *reinterpret_cast<RunAt *>(smem + M::FIRST) = run;
     }
   };
   if (a.runs.n <= kThreads) {
@@ -308,8 +313,12 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
     int64_t carry = 0;
     for (int b0 = 0; b0 < a.runs.n && carry <= start; b0 += kThreads) {
       const int b = b0 + tid;
-      mine = b < a.runs.n ? run_at(a, b, bad).run.units() * a.H : 0;
-      const int64_t all = sum_up(mine, before);
+      whole = 0;
+      if (b < a.runs.n) {
+        run = run_at(a, b, bad);
+        whole = run.run.units();
+      }
+      const int64_t all = sum_up(whole * a.H, before);
       before += carry;
       carry += all;
       found(b);
@@ -355,11 +364,10 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
         return true;
       };
       if (start < stop) {
-        // 32 runs at a time, one in each lane
-        int b = static_cast<int>(plan[2]), held = b;
+        int b = static_cast<int>(plan[2]), held = -32;
         bool none = false;
-        RunAt lot = run_at(a, min(b + lane, a.runs.n - 1), none), r;
-        auto take = [&]() {
+        RunAt r = *reinterpret_cast<const RunAt *>(smem + M::FIRST), lot{};
+        auto take = [&]() {  // of 32 runs at a time, one in each lane
           if (b >= held + 32) {
             held = b;
             lot = run_at(a, min(b + lane, a.runs.n - 1), none);
@@ -368,7 +376,6 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
           auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, from); };
           r = RunAt{of(lot.begin), of(lot.slot), Run{of(lot.run.before), of(lot.run.len), a.G, a.window}};
         };
-        take();
         const int64_t whole = plan[1], x0 = start - plan[0], h0 = attn::quotient(x0, whole);
         const int64_t x = x0 - h0 * whole;
         int h = static_cast<int>(h0), i = 0, hi = r.run.items();

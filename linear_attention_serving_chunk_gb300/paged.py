@@ -88,7 +88,7 @@ def kv_append(k, v, cache, table, lens, slots=None, cu_seqlens=None, stream=None
         raise KDAError("kda_kv_append", st)
 
 
-@functools.lru_cache(maxsize=256)  # (a tenth of a call's checks for the same sizes again)
+@functools.lru_cache(maxsize=256)  # (a function of the sizes alone, and 0.7 us of a call)
 def attn_workspace_bytes(n, total_tokens, Hq, H, D):
     return int(lib().kda_attn_paged_workspace_bytes(n, total_tokens, Hq, H, D))
 

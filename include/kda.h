@@ -478,7 +478,7 @@ int kda_verify_draft(const void *target, const void *draft, int prob_bytes, int 
  *          (ldk, ldv multiples of 8).  They do not lie in the cache.
  * The pages are there before (kda_pages_grow).  A token without a valid page
  * is not written and recorded.  Slots are distinct.  Tokens of k and v
- * outside all runs are not read.
+ * outside all runs (in front of the first, behind the last) are not written.
  *   Errors: KDA_ERR_NULL, _SHAPE, _ALIGN, _UNSUPPORTED, _CUDA.
  */
 int kda_kv_append(const kda_bf16 *k, int64_t ldk, const kda_bf16 *v, int64_t ldv,

@@ -33,8 +33,9 @@ __device__ int64_t place(const AppendArgs &a, int64_t t) {
       if (r.cu[b] > t || r.cu[b] < 0) atomicOr(a.status, KDA_ERR_SHAPE);
       return -1;
     }
-    if (!seq_range(r.cu, b, r.total, begin, end) || t < begin || t >= end) {
-      atomicOr(a.status, KDA_ERR_SHAPE);
+    const bool ok = seq_range(r.cu, b, r.total, begin, end);
+    if (!ok || t < begin || t >= end) {
+      if (!(ok && b == 0 && t < begin)) atomicOr(a.status, KDA_ERR_SHAPE);  // (else: in front of the first run)
       return -1;
     }
   } else {

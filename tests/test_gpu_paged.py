@@ -87,6 +87,27 @@ def test_append_leaves_what_it_cannot_place():
         assert same(c, cache)
 
 
+def test_append_of_runs_inside_the_rows():
+    """Rows in front of the first run and behind the last are left out, and are no fault; so they are for
+    the attention that follows."""
+    page, H, D = 16, 2, 64
+    cu, total, cached = [5, 8, 8, 45], 50, [3, 40, 0]
+    table = torch.tensor([[4, 0, -1], [-1, -1, -1], [2, 5, 1]], dtype=torch.int32)
+    table[1] = torch.tensor([3, 6, 7])
+    k, v = torch.randn(total, H, D).bfloat16(), torch.randn(total, H, D).bfloat16()
+    cache = torch.randn(8, 2, H, page, D).bfloat16()
+    want = ref.append(k, v, cache, table, torch.tensor(cached), [0, 1, 2], cu, page)
+    c = cache.cuda()
+    kda.kv_append(k.cuda(), v.cuda(), c, table.cuda(), ints(cached), cu_seqlens=ints(cu))
+    assert kda.device_status() == 0
+    assert same(c, want)
+    o = noise(total, H, D, seed=4)
+    got = kda.attn_paged(k.cuda(), c, table.cuda(), ints(cached), cu_seqlens=ints(cu), o=o.cuda())
+    assert kda.device_status() == 0
+    assert same(got[:5], o[:5]) and same(got[45:], o[45:])
+    assert bool(torch.isfinite(got[5:45].float()).all())
+
+
 def test_append_beyond_32_bits():
     """Pages whose offsets pass 2^32 elements."""
     H, page, D = 8, 128, 128

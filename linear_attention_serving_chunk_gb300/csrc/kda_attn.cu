@@ -200,6 +200,13 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   return r;
 }
 
+// Ones from bit n on: all for n <= 0, none for n >= 32.
+__device__ __forceinline__ uint32_t ones_from(int n) {
+  uint32_t r;
+  asm("shl.b32 %0, %1, %2;" : "=r"(r) : "r"(~0u), "r"(max(n, 0)));  // (a shift by 32 or more leaves nothing)
+  return r;
+}
+
 // Run b as this call takes it: empty where an entry is malformed.
 struct RunAt {
   int begin, slot;
@@ -823,12 +830,12 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
             const int p0 = (it.lo + (both ? j : 2 * j + w)) * kTile;
             const int c1 = min(max(see1 - p0, 0), kTile), c0 = min(max(see0 - p0, 0), kTile);
             if (__any_sync(0xffffffffu, valid && (c0 > 0 || c1 < kTile))) {
-              const unsigned seen = c1 > c0 ? c1 - c0 : 0;
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t seen = ones_from(c0 - 32 * c) & ~ones_from(c1 - 32 * c);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  s[c][i] = static_cast<unsigned>(c * 32 + i - c0) < seen ? s[c][i] : -INFINITY;
+                for (int i = 0; i < 32; ++i) s[c][i] = (seen >> i) & 1u ? s[c][i] : -INFINITY;
+              }
             }
             float mx[4];
 #pragma unroll

@@ -37,10 +37,10 @@
 //
 // Prompt chunks are bound by the products, and those by shared memory: the scores of two tiles read 128 KB in
 // their 1024 cycles while 64 KB of K and V are written.  1160 to 1190 us for 4096 tokens behind 28,672, 32 heads of 128
-// over 8 of keys, 1.75 PFLOP/s where a large product of the library reaches 1.93 (1370 us back to back for
+// over 8 of keys, 1.75 PFLOP/s where a large product of the library reaches 1.93 (1340 us back to back for
 // seconds, at the clock that the power limit leaves).  Single tokens are bound by memory: 645 us for 128
 // sequences of 1000 to 16,000 tokens, 4.49 GB.  Short calls are bound by latency: about 5 us until the
-// first scores, 1 us a tile, 3 us for the join.
+// first scores, 1 us a tile (2 the first time, while its code comes), 3 us for the join.
 //
 // What it took, us for those chunks / those tokens: the MMAs issued by lane 0 1694 / 675 (each waits for its
 // operands to come into uniform registers); by an elected thread, with the warp's number and TMEM's address
@@ -200,7 +200,8 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   return r;
 }
 
-// Ones from bit n on: all for n <= 0, none for n >= 32.
+// Ones from bit n on: all for n <= 0, none for n >= 32.  (A mask's bit a score: two instructions, three with the
+// bounds compared, which is 1.5 us of a mixed batch's 28.)
 __device__ __forceinline__ uint32_t ones_from(int n) {
   uint32_t r;
   asm("shl.b32 %0, %1, %2;" : "=r"(r) : "r"(~0u), "r"(max(n, 0)));  // (a shift by 32 or more leaves nothing)

@@ -66,7 +66,9 @@ using namespace sm100;
 using attn::kCtas;
 using attn::kRows;
 using attn::kTile;
+using attn::phase_of;
 using attn::Run;
+using attn::turn_of;
 
 constexpr int kThreads = 384;
 // Registers a thread: a launch of 384 threads gives 168 to each, 3 x 168 = 2 x 208 + 88.
@@ -128,7 +130,7 @@ struct Smem {
   static constexpr uint32_t BAR = STAGE + kStages * kTileBytes;
   static constexpr uint32_t FULL = BAR, EMPTY = FULL + 8 * kStages, SFULL = EMPTY + 8 * kStages,
                             PREADY = SFULL + 32, QREADY = PREADY + 8 * kScores, OFULL = QREADY + 16,
-                            ODONE = OFULL + 16, IFULL = ODONE + 16, IEMPTY = IFULL + 8 * kItems,
+                            ODONE = OFULL + 16, IFULL = ODONE + 32, IEMPTY = IFULL + 8 * kItems,
                             MFULL = IEMPTY + 8 * kItems, MEMPTY = MFULL + 8, FIN = MEMPTY + 8;
   static constexpr uint32_t TMEM = FIN + 8;
   // int64: the first unit of the share's first run, the run's units for a head, its number; partial sums
@@ -251,12 +253,14 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       mbar_init(sb + M::FULL + 8 * i, 1);
       mbar_init(sb + M::EMPTY + 8 * i, 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(sb + M::SFULL + 8 * i, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(sb + M::SFULL + 8 * i, 1);
+      mbar_init(sb + M::ODONE + 8 * i, 1);
+    }
     for (int i = 0; i < M::kScores; ++i) mbar_init(sb + M::PREADY + 8 * i, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(sb + M::QREADY + 8 * i, 4);
       mbar_init(sb + M::OFULL + 8 * i, 1);
-      mbar_init(sb + M::ODONE + 8 * i, 1);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(sb + M::IFULL + 8 * i, 1);
@@ -539,10 +543,9 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       // scores, and for no other's, and at most one more is there before it has taken the last.  (Descriptors
       // from an address that the compiler cannot see through: hoisted out of the loop, the sums of all steps
       // would take most of this warp's registers.)
-      uint32_t announced[2] = {0, 0};
+      uint32_t announced[2] = {0, 0}, summed[2] = {0, 0};
       auto scores = [&](int place, int w, int q, uint32_t k) {
-        const uint32_t full = sb + M::SFULL + 16 * w + 8 * (announced[w] & 1);
-        ++announced[w];
+        const uint32_t full = sb + M::SFULL + 16 * w + 8 * turn_of(announced[w]++);
         if (elect()) {
           uint32_t qa = sb + M::Q + q * M::kTileBytes;
           asm volatile("" : "+r"(qa), "+r"(k));
@@ -633,7 +636,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
               tc_fence_after();
               weighted(place, w, v, s > 1);
               if (!two || w) commit(v_free);
-              if (M::kScores > 2) commit(sb + M::ODONE + 8 * w);
+              if (M::kScores > 2) commit(sb + M::ODONE + 16 * w + 8 * turn_of(summed[w]++));
               if (s + 2 >= all) commit(sb + M::OFULL + 8 * w);
               if (more) next_scores(s + M::kScores);
             }
@@ -820,8 +823,12 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
         float m = -INFINITY, l = 0.f;  // log2
         for (int j = 0; j < steps; ++j) {
           const uint32_t place = M::place(turn, 2 * j + w), ts = tmem + place * 128 + lanes;
-          if (!wait(sb + M::SFULL + 16 * w + 8 * (s_n & 1), s_n >> 1)) return;
+          if (!wait(sb + M::SFULL + 16 * w + 8 * turn_of(s_n), phase_of(s_n))) return;
           ++s_n;
+          // With two places, these scores came behind this warpgroup's last sum.  With three, behind the one before
+          // it, which is waited for here so that each barrier of the sums is seen in all of its phases.
+          auto summed = [&](uint32_t k) { return wait(sb + M::ODONE + 16 * w + 8 * turn_of(k), phase_of(k)); };
+          if (M::kScores > 2 && s_n > 2 && !summed(s_n - 3)) return;
           if (live) {
             tc_fence_after();
             float s[4][32];
@@ -852,10 +859,8 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
               if (higher) m = top;
               l *= f;
               if (j > 0) {  // O of the tiles before: the next MMA waits for P
-                // With two places, these scores came behind the last sum; with three, behind the one before it,
-                // so that the barrier of the sums is in the last one's phase or behind it.
                 if (M::kScores > 2) {
-                  if (!wait(sb + M::ODONE + 8 * w, s_n - 2)) return;
+                  if (!summed(s_n - 2)) return;
                   tc_fence_after();
                 }
 #pragma unroll

@@ -89,6 +89,12 @@ KDA_HD int tiles_before(int64_t u, int n, int weight) {
   return u <= 0 ? 0 : u >= static_cast<int64_t>(n) * weight ? n : static_cast<int>((u + weight - 1) / weight);
 }
 
+// What happens k-th and is announced on two barriers in turn: the barrier, and the phase that it completes there.
+// A wait tells a phase from the one before by its parity alone.  So who waits for the k-th has waited for the (k - 2)nd,
+// and waits before the (k + 2)nd can happen: barriers are not signalled in the order of what completes them.
+KDA_HD constexpr uint32_t turn_of(uint32_t k) { return k & 1; }
+KDA_HD constexpr uint32_t phase_of(uint32_t k) { return k >> 1; }
+
 // Units of a CTA, at least two of the widest tiles, so that no share within an item is empty.
 static_assert(kLeastUnits >= 2 * kWideTile, "shares");
 KDA_HD int64_t share(int64_t units) {

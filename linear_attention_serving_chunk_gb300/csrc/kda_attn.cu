@@ -67,6 +67,7 @@ using attn::kCtas;
 using attn::kRows;
 using attn::kTile;
 using attn::phase_of;
+using attn::RingAt;
 using attn::Run;
 using attn::turn_of;
 
@@ -128,7 +129,7 @@ struct Smem {
   static constexpr uint32_t MERGE = kTileBytes;                 // second Q tile, or 128 x 64 fp32
   static constexpr uint32_t STAGE = MERGE + 32 * 1024;
   static constexpr uint32_t BAR = STAGE + kStages * kTileBytes;
-  static constexpr uint32_t FULL = BAR, EMPTY = FULL + 8 * kStages, SFULL = EMPTY + 8 * kStages,
+  static constexpr uint32_t FULL = BAR, EMPTY = FULL + 8 * kStages, SFULL = EMPTY + 16 * kStages,
                             PREADY = SFULL + 32, QREADY = PREADY + 8 * kScores, OFULL = QREADY + 16,
                             ODONE = OFULL + 16, IFULL = ODONE + 32, IEMPTY = IFULL + 8 * kItems,
                             MFULL = IEMPTY + 8 * kItems, MEMPTY = MFULL + 8, FIN = MEMPTY + 8;
@@ -251,7 +252,8 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
   if (tid == 0) {
     for (int i = 0; i < M::kStages; ++i) {
       mbar_init(sb + M::FULL + 8 * i, 1);
-      mbar_init(sb + M::EMPTY + 8 * i, 1);
+      mbar_init(sb + M::EMPTY + 16 * i, 1);
+      mbar_init(sb + M::EMPTY + 16 * i + 8, 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(sb + M::SFULL + 8 * i, 1);
@@ -454,19 +456,19 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
     } else if (warp != kMmaWarp) {
       // ---- pages and tiles: one warp loads the keys' and one the values' ------------------------
       const bool mine_is_v = warp == kLoadVWarp;
-      uint32_t fills = 0, stage = 0, taken = 0;
+      RingAt ring;
+      uint32_t taken = 0;
       bool wrong = false;
       const int per_tile = kTile >> a.seqs.page_shift;
       constexpr int halves = D / 64;
       // Tile t of keys (or values): pages that no row needs, and those outside the pool, come as zeros.
       auto load = [&](const Item &it, int t, int values, int first) -> bool {
         if ((values != 0) != mine_is_v) {  // the other's place in the ring
-          ++fills;
-          if (++stage == M::kStages) stage = 0;
+          ring.next(M::kStages);
           return true;
         }
-        if (!wait(sb + M::EMPTY + 8 * stage, fills / M::kStages + 1)) return false;
-        const uint32_t bar = sb + M::FULL + 8 * stage, to = sb + M::STAGE + stage * M::kTileBytes;
+        if (!wait(sb + M::EMPTY + 16 * ring.stage + 8 * ring.free(), ring.free_phase())) return false;
+        const uint32_t bar = sb + M::FULL + 8 * ring.stage, to = sb + M::STAGE + ring.stage * M::kTileBytes;
         const int32_t *const row = a.seqs.table + static_cast<int64_t>(it.slot) * a.seqs.max_pages;
         if (lane == 0) {
           mbar_expect_tx(bar, M::kTileBytes);
@@ -497,8 +499,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
           }
         }
         __syncwarp();
-        ++fills;
-        if (++stage == M::kStages) stage = 0;
+        ring.next(M::kStages);
         return true;
       };
       auto load_item = [&](const Item &it) -> bool {
@@ -525,7 +526,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       }
       if (__any_sync(0xffffffffu, wrong) && lane == 0) atomicOr(a.status, KDA_ERR_SHAPE);
       if (gave_up) {  // the tiles on their way
-        const uint32_t n = min(fills, static_cast<uint32_t>(M::kStages));
+        const uint32_t fills = ring.round * M::kStages + ring.stage, n = min(fills, static_cast<uint32_t>(M::kStages));
         for (uint32_t f = fills - n; f < fills; ++f)
           mbar_wait_bounded(sb + M::FULL + 8 * (f % M::kStages), (f / M::kStages) & 1u, kPolls);
       }
@@ -533,7 +534,8 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       // ---- MMAs ------------------------------------------------------------------------------
       constexpr uint32_t ID_S = idesc_mma(128, kTile, kFmtBF16, kFmtBF16, 0, 0);
       constexpr uint32_t ID_O = idesc_mma(128, D, kFmtBF16, kFmtBF16, 0, 1);
-      uint32_t used = 0, stage = 0, taken = 0, q_n[2] = {0, 0}, p_bits = 0;
+      RingAt ring;
+      uint32_t taken = 0, q_n[2] = {0, 0}, p_bits = 0;
       auto p_phase = [&](uint32_t place) {  // each place's phases of P, one after another
         const uint32_t phase = p_bits >> place;
         p_bits ^= 1u << place;
@@ -575,11 +577,10 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
         __syncwarp();
       };
       auto tile = [&](uint32_t &at, uint32_t &free) -> bool {  // the next one in the ring
-        at = sb + M::STAGE + stage * M::kTileBytes;
-        free = sb + M::EMPTY + 8 * stage;
-        const bool ok = wait(sb + M::FULL + 8 * stage, used / M::kStages);
-        ++used;
-        if (++stage == M::kStages) stage = 0;
+        at = sb + M::STAGE + ring.stage * M::kTileBytes;
+        free = sb + M::EMPTY + 16 * ring.stage + 8 * ring.release();
+        const bool ok = wait(sb + M::FULL + 8 * ring.stage, ring.round);
+        ring.next(M::kStages);
         return ok;
       };
       auto run = [&]() {

@@ -95,6 +95,21 @@ KDA_HD int tiles_before(int64_t u, int n, int weight) {
 KDA_HD constexpr uint32_t turn_of(uint32_t k) { return k & 1; }
 KDA_HD constexpr uint32_t phase_of(uint32_t k) { return k >> 1; }
 
+// A place of a ring of `stages`, as a warp goes through them.  Two warps fill it, each the places of its own tiles, so
+// neither waits for every release of a place: with one barrier for a place, a release that arrives late could be
+// taken for the one two rounds before.  With two in turn, that would need one from four rounds before, whose
+// place has not been filled again then.
+struct RingAt {
+  uint32_t stage = 0, round = 0;
+  KDA_HD void next(uint32_t stages) {
+    if (++stage == stages) stage = 0, ++round;
+  }
+  KDA_HD uint32_t release() const { return turn_of(round); }  // the barrier of this round's release
+  // The release of the round before, which a fill waits for (in front of the first: the phase before a new barrier's).
+  KDA_HD uint32_t free() const { return turn_of(round - 1); }
+  KDA_HD uint32_t free_phase() const { return phase_of(round - 1); }
+};
+
 // Units of a CTA, at least two of the widest tiles, so that no share within an item is empty.
 static_assert(kLeastUnits >= 2 * kWideTile, "shares");
 KDA_HD int64_t share(int64_t units) {

@@ -117,6 +117,64 @@ int main() {
 }
 """
 
+RING = MODEL + r"""
+// Two warps that fill a ring with keys and values, and one that uses the tiles in order and releases them.
+int main() {
+  for (int turn = 0; turn < 4000; ++turn) {
+    srand(turn);
+    const int stages = turn % 2 ? 5 : 10, ahead = turn % 2 ? 2 : 2 + rand() % 2;
+    std::vector<int> tiles;  // whose, in the order in which they are used
+    for (int item = 1 + rand() % 8; item-- > 0;) {
+      const int n = 1 + rand() % (rand() % 2 ? 3 : 20);
+      for (int j = 0; j < ahead && j < n; ++j) tiles.push_back(0);
+      for (int j = 0; j < n; ++j) {
+        tiles.push_back(1);
+        if (j + ahead < n) tiles.push_back(0);
+      }
+    }
+    const int all = static_cast<int>(tiles.size());
+    std::vector<Bar> empty(2 * stages);
+    std::vector<Bar *> bars;
+    for (Bar &b : empty) bars.push_back(&b);
+    const int slow = rand() % (2 * stages);
+    std::vector<int> filled(all, 0), released(all, 0);
+    RingAt at[2], use;
+    int fill[2] = {0, 0}, used = 0, freed = 0, lag = rand() % 4;
+    auto load = [&](int w) -> int {
+      if (fill[w] == all) return 0;
+      RingAt &r = at[w];
+      if (tiles[fill[w]] == w) {
+        if (!empty[2 * r.stage + r.free()].test(r.free_phase())) return 0;
+        if (fill[w] >= stages && !released[fill[w] - stages]) return -1;
+        filled[fill[w]] = 1;
+      }
+      ++fill[w];
+      r.next(stages);
+      return 1;
+    };
+    for (int idle = 0; idle < 400;) {
+      int did = 0;
+      const int who = rand() % 4;
+      if (who <= 1) did = load(who);
+      else if (who == 2) did = deliver(bars, slow, idle > 60);
+      else if (used < all && filled[used]) {
+        ++used, did = 1;
+        // released up to `lag` tiles later, in order
+        while (freed < used && (used - freed > lag || used == all)) {
+          released[freed++] = 1;
+          ++empty[2 * use.stage + use.release()].due;
+          use.next(stages);
+        }
+      }
+      if (did < 0) return printf("turn %d: a tile is written over before it is released\n", turn), 1;
+      idle = did ? 0 : idle + 1;
+    }
+    if (used < all) return printf("turn %d: everyone waits\n", turn), 1;
+  }
+  return 0;
+}
+"""
+
 
 def run(tmp_path, text):
     src, exe = tmp_path / "waits.cpp", tmp_path / "waits"
@@ -129,3 +187,7 @@ def run(tmp_path, text):
 
 def test_a_sum_is_complete_before_it_is_scaled(tmp_path):
     run(tmp_path, SUMS)
+
+
+def test_a_place_is_released_before_it_is_filled(tmp_path):
+    run(tmp_path, RING)

@@ -94,6 +94,12 @@ typedef uint16_t kda_bf16;                 /* raw bfloat16 bit pattern */
  * tensor-core kernels; never set it otherwise. */
 #define KDA_TEST_STALL 0x10000u
 
+/* Test hook of kda_attn_paged, given as its window (the call has none then): the
+ * second of its CTAs first waits, with a small poll limit, on an mbarrier that
+ * nothing arrives on, gives up and leaves its share undone; rows that need it
+ * stay as they were, KDA_ERR_TIMEOUT is recorded.  Never set it otherwise. */
+#define KDA_ATTN_TEST_STALL (-0x10000)
+
 typedef struct CUstream_st *kda_stream_t;  /* same type as cudaStream_t */
 
 typedef enum {
@@ -509,7 +515,9 @@ int kda_kv_append(const kda_bf16 *k, int64_t ldk, const kda_bf16 *v, int64_t ldv
  *               rounding, slower for few tokens.
  * Precision: scores, sums and o before its rounding are fp32; the weights are
  * rounded to bf16 before they meet v.  The same call gives the same bits.
- * Bounded in-kernel waits that give up are recorded as KDA_ERR_TIMEOUT.
+ * Bounded in-kernel waits that give up are recorded as KDA_ERR_TIMEOUT; rows of o
+ * that need what such a wait stood for are left as they were, or hold a part of their
+ * columns.
  *   Errors: KDA_ERR_NULL, _SHAPE, _ALIGN, _UNSUPPORTED, _CUDA.
  */
 int kda_attn_paged(const kda_bf16 *q, int64_t ldq, const int32_t *cu_seqlens, int n,

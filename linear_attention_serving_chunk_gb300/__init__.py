@@ -33,6 +33,7 @@ PASS_STATE = 0x200
 # Test hook (KDA_TEST_STALL in kda.h): the kernel gives up on a wait nothing
 # arms and records KDA_ERR_TIMEOUT in the device status word.
 TEST_STALL = 0x10000
+ATTN_TEST_STALL = -0x10000  # KDA_ATTN_TEST_STALL, as the window of attn_paged
 
 KDA_OK = 0
 STATUS_NAMES = {0: "KDA_OK", 1: "KDA_ERR_NULL", 2: "KDA_ERR_SHAPE", 3: "KDA_ERR_ALIGN",

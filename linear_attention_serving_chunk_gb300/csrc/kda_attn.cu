@@ -89,15 +89,18 @@ struct AttnArgs {
   float scale2;   // scale times log2(e)
   uint8_t *ws;    // or NULL: no item is cut
   int *status;
+  int test_stall;  // KDA_ATTN_TEST_STALL
 };
 
-// The workspace: for each CTA what the first item that it cuts off needs, then the parts: 2 c is the
-// end or the middle of an item that an earlier CTA began, 2 c + 1 the beginning of one that CTA c began.
+// The workspace: for each CTA what the first item that it cuts off needs, and whether one of its waits gave up (then
+// its parts may not be there), then the parts: 2 c is the end or the middle of an item that an earlier CTA
+// began, 2 c + 1 the beginning of one that CTA c began.
 struct Cut {
   int rows, row0, token0, head, last;  // last: the CTA of the last part; rows 0: nothing is cut
   int pad[3];
 };
-constexpr size_t kCutBytes = sizeof(Cut) * kCtas;
+constexpr int kCutWords = sizeof(Cut) / 4, kFailed = kCutWords * kCtas;  // a word for each CTA from there on
+constexpr size_t kCutBytes = (4 * (kCutWords + 1) * kCtas + 127) / 128 * 128;  // (lines of parts begin where the memory's do)
 constexpr size_t kStatBytes = sizeof(float2) * kRows * 2 * kCtas;
 constexpr size_t ws_bytes(int D) { return kCutBytes + kStatBytes + sizeof(float) * kRows * 2 * kCtas * D; }
 
@@ -243,9 +246,13 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, cta = blockIdx.x;
   grid_launch_dependents();
+  auto start_ws = [&]() {  // no item is cut yet, no wait has given up
+    if (!a.ws || tid > kCutWords) return;
+    reinterpret_cast<int *>(a.ws)[tid < kCutWords ? cta * kCutWords + tid : kFailed + cta] = 0;
+  };
   if ((sb & 1023u) != 0) {  // the swizzled tiles need it
     grid_dependency_wait();
-    if (a.ws && tid < 8) reinterpret_cast<int *>(a.ws)[cta * 8 + tid] = 0;
+    start_ws();
     if (tid == 0) atomicOr(a.status, KDA_ERR_UNSUPPORTED);
     return;
   }
@@ -280,7 +287,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
   }
 
   grid_dependency_wait();
-  if (a.ws && tid < 8) reinterpret_cast<int *>(a.ws)[cta * 8 + tid] = 0;  // no item is cut yet
+  start_ws();
 
   // This CTA's share: all units, then the run in which the share begins.
   int64_t *const plan = reinterpret_cast<int64_t *>(smem + M::PLAN);
@@ -363,6 +370,19 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
   };
+
+  // What follows a wait that gave up: the code, and for the join that parts may be missing.
+  auto fail = [&]() {
+    atomicOr(a.status, KDA_ERR_TIMEOUT);
+    if (a.ws) reinterpret_cast<int *>(a.ws)[kFailed + cta] = 1;
+  };
+  // Test hook: a wait that nothing ends, before anything is issued.
+  if (a.test_stall && cta == 1) {
+    if (!mbar_wait_bounded(sb + M::FIN, 0, 1u << 10) && lane == 0) fail();
+    __syncthreads();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    return;
+  }
 
   if (warp >= 8) {
     set_registers<kOtherRegs, false>();
@@ -922,8 +942,9 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
       }
     };
     run();
+    asm volatile("cp.async.wait_all;" ::: "memory");  // (where a wait gave up)
   }
-  if (gave_up && lane == 0) atomicOr(a.status, KDA_ERR_TIMEOUT);
+  if (gave_up && lane == 0) fail();
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -935,7 +956,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
 // Joins the parts of each item that was cut, o = sum 2^(m_p - m) o_p / sum 2^(m_p - m) l_p.  A lane takes a
 // row and FOURS times four columns: what a warp reads lies in a row of memory.  Bound by latency, so the
 // fewer rows an item has, the fewer columns a lane takes and the more parts are on their way at once: a
-// sequence of a million keys in 152 parts.
+// sequence of a million keys in 152 parts.  An item of which a CTA gave up is left as it was.
 constexpr int kJoinThreads = 512;
 constexpr int kJoinWarps = kJoinThreads / 32;
 
@@ -991,11 +1012,20 @@ template <int D>
 __global__ void __launch_bounds__(kJoinThreads, 1) attn_join_kernel(const AttnArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();  // (the next call's start, which waits for this kernel's end)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Cut cut = reinterpret_cast<const Cut *>(a.ws)[blockIdx.x];
   constexpr int kHalf = D / 8;  // columns in fours
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int failed[(kCtas + 31) / 32];  // of all CTAs from this one on, on their way with the cut
+#pragma unroll
+  for (int i = 0; i < (kCtas + 31) / 32; ++i)
+    failed[i] = reinterpret_cast<const int *>(a.ws)[kFailed + min(static_cast<int>(blockIdx.x) + 32 * i + lane, kCtas - 1)];
   const int half = blockIdx.y & 1, first = blockIdx.y >> 1, lots = ((cut.rows + 31) / 32 - first + 1) / 2;
   if (lots <= 0) return;
+  int some = 0;
+#pragma unroll
+  for (int i = 0; i < (kCtas + 31) / 32; ++i)
+    if (static_cast<int>(blockIdx.x) + 32 * i + lane <= cut.last) some |= failed[i];
+  if (__any_sync(0xffffffffu, some)) return;
   const int each = lots == 1 ? kJoinWarps : lots == 2 ? kJoinWarps / 2 : kJoinWarps / 4;  // warps of 32 rows
   const int fours = kHalf > each ? kHalf / each : 1, lot = warp / each, four = (warp - lot * each) * fours;
   const int r = (first + 2 * lot) * 32 + lane;
@@ -1039,7 +1069,7 @@ size_t attn_workspace(int D) { return ws_bytes(D); }
 
 cudaError_t attn_launch(const AttnCall &c, int D, cudaStream_t st) {
   AttnArgs a{c.q, c.ldq, c.o, c.ldo, c.runs, c.seqs, c.H, c.G, c.window,
-             c.scale * 1.44269504088896340736f, static_cast<uint8_t *>(c.workspace), c.status};
+             c.scale * 1.44269504088896340736f, static_cast<uint8_t *>(c.workspace), c.status, c.test_stall};
   return D == 64 ? run<64>(a, c.cache, st) : run<128>(a, c.cache, st);
 }
 

@@ -48,6 +48,7 @@ struct AttnCall {
   float scale;
   void *workspace;   // attn_workspace(D) bytes, or NULL
   int *status;
+  bool test_stall;   // KDA_ATTN_TEST_STALL
 };
 
 enum PagesOp { kPagesGrow, kPagesFork, kPagesCompact };

@@ -106,6 +106,8 @@ int kda_attn_paged(const kda_bf16 *q, int64_t ldq, const int32_t *cu_seqlens, in
   if (int e = check_runs(cu_seqlens, n, total_tokens, &fixed_len)) return e;
   if (int e = check_table(table, lens, max_pages, n_slots, n_pages, page)) return e;
   if (int e = check_heads(H, D, cache, n_pages)) return e;
+  const bool test_stall = window == KDA_ATTN_TEST_STALL;
+  if (test_stall) window = 0;
   if (Hq <= 0 || Hq % H != 0 || Hq > 65535 || window < 0) return KDA_ERR_SHAPE;
   if (!slots && n > n_slots) return KDA_ERR_SHAPE;
   // (also refuses NaN; the kernel multiplies it by log2(e))
@@ -128,7 +130,7 @@ int kda_attn_paged(const kda_bf16 *q, int64_t ldq, const int32_t *cu_seqlens, in
   const bool cut = workspace && workspace_bytes >= attn_workspace(D);
   AttnCall c{q, ldq, o, ldo, Runs{cu_seqlens, nullptr, n, total_tokens, fixed_len},
              PagedSeqs{table, max_pages, lens, slots, n_slots, n_pages, page_shift(page)}, cache, H,
-             Hq / H, window, scale, cut ? workspace : nullptr, status_word(st)};
+             Hq / H, window, scale, cut ? workspace : nullptr, status_word(st), test_stall};
   if (!c.status) return KDA_ERR_CUDA;
   return launched(attn_launch(c, D, st));
 }

@@ -251,3 +251,29 @@ def test_cache_beyond_32_bits():
         cache[n_pages - 1 - 9 * i] = small.cache[p].cuda()
     o = kda.attn_paged(small.q.cuda(), cache, table.cuda(), small.lens.cuda(), slots=small.slots.cuda(), cu_seqlens=ints(small.cu))
     assert torch.equal(o, small.call())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_what_a_wait_that_gave_up_leaves(D):
+    """The hook makes one CTA give up before it begins: the rows that need its share keep what they held, whether
+    it is a part of an item or has items of its own, the others are right, and so is the next call."""
+    def stalled(b, **kw):
+        o = torch.full(b.q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+        b.call(window=kda.ATTN_TEST_STALL, o=o, **kw)
+        assert kda.device_status() == kda.KDA_ERR_TIMEOUT
+        return o
+
+    # one item in 152 parts, with a workspace that holds parts of an earlier call and with a new one
+    b = Batch([100000], [1], 4, 1, D, 64, seed=1)
+    workspace = torch.empty(kda.attn_workspace_bytes(1, 1, 4, 1, D), dtype=torch.uint8, device="cuda")
+    want = b.call(workspace=workspace)
+    assert (stalled(b, workspace=workspace) == 7).all() and (stalled(b) == 7).all()
+    assert torch.equal(b.call(workspace=workspace), want)
+    # 400 sequences of a token behind 100: some of them are in the second share, and none in two at once
+    b = Batch([100] * 400, [1] * 400, 4, 1, D, 64, seed=2)
+    want = b.call()
+    for kw in ({}, dict(workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))):
+        o = stalled(b, **kw)
+        kept = (o == 7).flatten(1).all(1)
+        assert 1 <= int(kept.sum()) <= 8 and torch.equal(o[~kept], want[~kept])
+        near(b.call(**kw), b.want())

@@ -500,7 +500,9 @@ int kda_kv_append(const kda_bf16 *k, int64_t ldk, const kda_bf16 *v, int64_t ldv
  *   q, o   [total, Hq, D] bf16, rows ldq / ldo elements apart, 16-byte aligned
  *          (ldq, ldo multiples of 8); H divides Hq, and query head h reads head
  *          h / (Hq / H) of the cache.  o may be q (with the same rows).
- *   scale  > 0 and at most 1e38; window >= 0 (0: all positions).
+ *   scale  > 0 and at most 1e38; window >= 0 (0: all positions).  Scores scale q . k
+ *          are held up to a magnitude of 2^30; a row with a larger one is undefined,
+ *          NaN where its weights have no sum.
  * The run's own keys and values are in the cache before (kda_kv_append).  Where a
  * row's window ends, entries of the table for pages that it no longer reaches are
  * not looked at.  A needed page outside [0, n_pages) is recorded and counts as keys

@@ -29,7 +29,9 @@
 // Scores, maxima, sums and O are fp32.  The weights are rounded to bf16 for their product with V,
 // which a row's sum does not see: by at most 2^-8 of each weight, in either direction.  A maximum is
 // kept until a score is more than 2^8 above it in the exponent's base: weights up to 256 lose nothing, and
-// most tiles then need no scaling of O.
+// most tiles then need no scaling of O.  The product with the scale is rounded in the maximum alone, which moves all
+// weights of a row by the same factor; from scores of 2^31 on that factor may leave fp32's range, and a row whose
+// sum is 0 then is NaN.  (A row sees itself: in range, its sum is not 0.)
 //
 // A warp whose rows are all beyond the item (three of four in a step of single tokens) computes
 // nothing.  Keys behind a row's position, or behind the window, weigh nothing whatever they are; the
@@ -751,7 +753,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
           reinterpret_cast<float2 *>(a.ws + kCutBytes)[it.part * kRows + row_of + r] = make_float2(m, l);
       };
       if (both || it.n == 1) {
-        const float f = l == 0.f ? 0.f : 1.f / l;
+        const float f = 1.f / l;
         if (live) {
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -800,7 +802,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
               other = ex2(t.x - base);
               l = l * mine + t.y * other;
               m = top;
-              inv = l == 0.f ? 0.f : 1.f / l;
+              inv = 1.f / l;
               put_stats();
             }
 #pragma unroll 1
@@ -997,7 +999,7 @@ __device__ void join_row(const AttnArgs &a, const Cut &cut, int r, int four) {
       }
     }
   }
-  const float f = l == 0.f ? 0.f : 1.f / l;
+  const float f = 1.f / l;
   const int row = cut.row0 + r, t = row / a.G, g = row - t * a.G;
   kda_bf16 *out = a.o + (static_cast<int64_t>(cut.token0) + t) * a.ldo +
                   (static_cast<int64_t>(cut.head) * a.G + g) * D + four * 4;

@@ -277,3 +277,19 @@ def test_what_a_wait_that_gave_up_leaves(D):
         kept = (o == 7).flatten(1).all(1)
         assert 1 <= int(kept.sum()) <= 8 and torch.equal(o[~kept], want[~kept])
         near(b.call(**kw), b.want())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cached,new", [([40, 3], [1, 9]), ([5000], [1]), ([300], [150])])
+def test_scores_at_the_end_of_the_range(D, cached, new):
+    """Scores of up to 2^30 decide for one key; a scale that takes them out of fp32 gives NaN, not zeros."""
+    b = Batch(cached, new, 2, 1, D, 64, seed=4)
+    # one key stands out in every row: the others' scores are closer than fp32 tells apart
+    for s, reach in zip(b.slots.tolist(), b.reach):
+        held = b.cache[b.table[s, 0].long()]
+        b.cache[b.table[s, :-(-reach // 64)].long(), 0] = 0.25
+        held[0, :, 0] = 0.5
+    b.q[:] = 0.5  # scores 0.25 D or 0.125 D times the scale
+    near(b.call(scale=2.0 ** 30 / (0.25 * D * 1.4427) * 0.99), b.want(scale=2.0 ** 30 / (0.25 * D * 1.4427) * 0.99))
+    for scale in (1e38, 3e37):
+        assert torch.isnan(b.call(scale=scale)).all()

@@ -485,6 +485,8 @@ int kda_verify_draft(const void *target, const void *draft, int prob_bytes, int 
  * The pages are there before (kda_pages_grow).  A token without a valid page
  * is not written and recorded.  Slots are distinct.  Tokens of k and v
  * outside all runs (in front of the first, behind the last) are not written.
+ * Offsets that decrease anywhere are recorded; a token that several runs claim
+ * then goes to one of them or nowhere, and no token goes anywhere else.
  *   Errors: KDA_ERR_NULL, _SHAPE, _ALIGN, _UNSUPPORTED, _CUDA.
  */
 int kda_kv_append(const kda_bf16 *k, int64_t ldk, const kda_bf16 *v, int64_t ldv,

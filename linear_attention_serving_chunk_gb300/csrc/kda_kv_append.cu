@@ -94,6 +94,17 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a,
     const int64_t at = where[token[j]];
     if (at >= 0) *reinterpret_cast<uint4 *>(a.cache + at + off[j]) = v[j];
   }
+  // Offsets that decrease between runs that are well-formed by themselves: no look-up of a token sees them.  (In front
+  // of the stores it costs 4 of 44 us, in the order of the loads.)
+  if (a.runs.cu) {
+    bool bad = false;
+    for (int64_t b = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; b < a.runs.n;
+         b += static_cast<int64_t>(gridDim.x) * kThreads) {
+      int64_t begin, end;
+      bad |= !seq_range(a.runs.cu, static_cast<int>(b), a.runs.total, begin, end);
+    }
+    if (bad) atomicOr(a.status, KDA_ERR_SHAPE);
+  }
 }
 
 }  // namespace

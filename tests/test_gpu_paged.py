@@ -328,3 +328,25 @@ def test_pages_captured_and_replayed_on_another_stream():
         g.replay()
         assert [int(c) for c in outs] == eager[i][0]
         assert all(torch.equal(a, b) for a, b in zip(state(), eager[i][1]))
+
+
+@pytest.mark.parametrize("lens", [[5, -2, 5], [0, 8, -8, 3], [2, 2, 2, 2, -1, 1] + [0] * 400, [1] * 3000 + [-3000] + [1] * 3000])
+def test_append_records_offsets_that_decrease(lens):
+    """Between runs that are well-formed by themselves: recorded, and what is written stands where one of
+    its token's runs puts it."""
+    page, H, D = 16, 1, 64
+    cu, n = ref.offsets(lens), len(lens)
+    total = max(cu)
+    k, v = noise(total, H, D, seed=1), noise(total, H, D, seed=2)
+    table = torch.arange(n, dtype=torch.int32).view(n, 1)
+    cache = noise(n, 2, H, page, D, seed=3)
+    c = cache.cuda()
+    kda.kv_append(k.cuda(), v.cuda(), c, table.cuda(), ints([0] * n), cu_seqlens=ints(cu))
+    assert kda.device_status() == kda.KDA_ERR_SHAPE
+    got = c.cpu().view(torch.int16)
+    for b in range(n):
+        for j in range(max(lens[b], 0)):
+            for i, x in enumerate((k, v)):
+                row = got[b, i, 0, j]
+                assert torch.equal(row, x[cu[b] + j, 0].view(torch.int16)) or torch.equal(row, cache[b, i, 0, j].view(torch.int16))
+        assert torch.equal(got[b, :, :, max(lens[b], 0):], cache[b, :, :, max(lens[b], 0):].view(torch.int16))

@@ -513,7 +513,8 @@ int kda_kv_append(const kda_bf16 *k, int64_t ldk, const kda_bf16 *v, int64_t ldv
  * hold behind a sequence's end is not used.  Rows of o outside all runs are
  * left as they were.
  *   workspace   device scratch, 16-byte aligned, not to be shared by calls that
- *               overlap on the GPU.  With fewer than
+ *               overlap on the GPU.  It and o overlap nothing that the call
+ *               reads (o = q apart): KDA_ERR_SHAPE.  With fewer than
  *               kda_attn_paged_workspace_bytes() bytes (or NULL) no sequence's
  *               keys are shared out between SMs: the same results up to
  *               rounding, slower for few tokens.

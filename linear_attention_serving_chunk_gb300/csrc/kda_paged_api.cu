@@ -1,5 +1,7 @@
 // C ABI of the paged cache's operators: host-side argument checks and launches, in the manner of
 // kda_serving_api.cu.
+#include <initializer_list>
+
 #include "kda_paged.cuh"
 
 namespace kda {
@@ -20,6 +22,16 @@ bool overlap(const void *p, int64_t bytes, const void *q, int64_t more) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
   return p && q && bytes > 0 && more > 0 && a < b + static_cast<uintptr_t>(more) &&
          b < a + static_cast<uintptr_t>(bytes);
+}
+
+struct Range {
+  const void *p;
+  int64_t bytes;
+};
+bool overlaps_any(const Range &r, std::initializer_list<Range> others) {
+  for (const Range &x : others)
+    if (overlap(r.p, r.bytes, x.p, x.bytes)) return true;
+  return false;
 }
 
 // Tokens of every run where they are all the same (0 with offsets), as in kda_serving_api.cu.
@@ -125,9 +137,14 @@ int kda_attn_paged(const kda_bf16 *q, int64_t ldq, const int32_t *cu_seqlens, in
   // q is read, and the cache, by blocks that run beside the writers of o; o may be q
   if ((o != q || ldo != ldq) && overlap(o, rows, q, 2 * ((total_tokens - 1) * ldq + cols)))
     return KDA_ERR_SHAPE;
-  if (overlap(o, rows, cache, 4LL * H * D * page * n_pages)) return KDA_ERR_SHAPE;
-  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool cut = workspace && workspace_bytes >= attn_workspace(D);
+  const Range held{cache, 4LL * H * D * page * n_pages}, pages{table, 4LL * n_slots * max_pages}, ends{lens, 4LL * n_slots},
+      at{slots, 4LL * n}, offsets{cu_seqlens, 4LL * (n + 1)}, out{o, rows},
+      scratch{workspace, cut ? static_cast<int64_t>(attn_workspace(D)) : 0};
+  if (overlaps_any(out, {held, pages, ends, at, offsets})) return KDA_ERR_SHAPE;
+  if (overlaps_any(scratch, {out, {q, 2 * ((total_tokens - 1) * ldq + cols)}, held, pages, ends, at, offsets}))
+    return KDA_ERR_SHAPE;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   AttnCall c{q, ldq, o, ldo, Runs{cu_seqlens, nullptr, n, total_tokens, fixed_len},
              PagedSeqs{table, max_pages, lens, slots, n_slots, n_pages, page_shift(page)}, cache, H,
              Hq / H, window, scale, cut ? workspace : nullptr, status_word(st), test_stall};

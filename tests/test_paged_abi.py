@@ -222,3 +222,23 @@ def test_units_of_items_in_closed_form(tmp_path):
     subprocess.run(["g++", "-O2", "-std=c++17", "-I" + csrc, str(src), "-o", str(exe)], check=True)
     assert subprocess.run([str(exe)], capture_output=True, text=True).stdout == ""
     assert subprocess.run([str(exe)]).returncode == 0
+
+
+SCRATCH = 152 * 2 * 256 * (8 + 4 * 64)  # bytes of the attention's parts at least, heads of 64
+
+
+@pytest.mark.parametrize("what", ["q", "o", "cache", "table", "lens", "slots", "cu"])
+@pytest.mark.parametrize("end", ["first", "last"])
+def test_attention_refuses_a_workspace_over_what_it_uses(L, what, end):
+    """What the call reads or returns at the workspace's first bytes, or at its last ones."""
+    ws, size = 64 * GB, kda.attn_workspace_bytes(2, 8, 4, 2, 64)
+    assert size >= SCRATCH
+    there = at(ws if end == "first" else ws + SCRATCH - 16)
+    assert call(L.kda_attn_paged, ATTN, dict(ws=at(ws), size=size, **{what: there})) == SHAPE
+    # where no part goes into it, or behind it, nothing is wrong but that there is no GPU
+    assert call(L.kda_attn_paged, dict(ATTN, total=0), dict(ws=at(ws), size=size, **{what: there})) == 0
+
+
+@pytest.mark.parametrize("what", ["table", "lens", "slots", "cu"])
+def test_attention_refuses_an_output_over_its_tables(L, what):
+    assert call(L.kda_attn_paged, ATTN, {what: at(3 * GB + 7 * 512 + 508)}) == SHAPE

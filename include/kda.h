@@ -472,6 +472,8 @@ int kda_verify_draft(const void *target, const void *draft, int prob_bytes, int 
  * lens[slot] + j.  Neither call changes lens: the caller adds what stands (all
  * of a prompt, kda_verify_draft's n_out of a drafted run).  A step is
  *   kda_pages_grow, kda_kv_append and kda_attn_paged in each layer, lens += ...
+ * What a call on pages writes overlaps nothing else that it is given, unless
+ * said otherwise: KDA_ERR_SHAPE.
  * Device-side entries are checked before use; a slot outside [0, n_slots), a
  * length that is negative or that its row cannot hold, and a page outside
  * [0, n_pages) that is needed are recorded as KDA_ERR_SHAPE.
@@ -481,7 +483,8 @@ int kda_verify_draft(const void *target, const void *draft, int prob_bytes, int 
  * kda_kv_append - write the keys and values of a batch of runs into the pages
  * of their sequences.
  *   k, v   [total, H, D] bf16, rows ldk / ldv elements apart, 16-byte aligned
- *          (ldk, ldv multiples of 8).  They do not lie in the cache.
+ *          (ldk, ldv multiples of 8).  Neither they nor the tables lie in the
+ *          cache: KDA_ERR_SHAPE.
  * The pages are there before (kda_pages_grow).  A token without a valid page
  * is not written and recorded.  Slots are distinct.  Tokens of k and v
  * outside all runs (in front of the first, behind the last) are not written.

@@ -34,6 +34,11 @@ bool overlaps_any(const Range &r, std::initializer_list<Range> others) {
   return false;
 }
 
+// The cache of all layers.  (check_layers keeps its pieces of 4 KB under 2^31.)
+Range pool_of(const kda_bf16 *cache, int layers, int n_pages, int H, int page, int D) {
+  return {cache, 4LL * H * page * D * n_pages * layers};
+}
+
 // Tokens of every run where they are all the same (0 with offsets), as in kda_serving_api.cu.
 int check_runs(const int32_t *cu_seqlens, int n, int64_t total, int64_t *fixed_len) {
   *fixed_len = 0;
@@ -96,10 +101,11 @@ int kda_kv_append(const kda_bf16 *k, int64_t ldk, const kda_bf16 *v, int64_t ldv
   if (total_tokens > 1 && ((ldk | ldv) & 7)) return KDA_ERR_ALIGN;
   if (total_tokens == 0) return KDA_OK;
   if (total_tokens * cols / 4096 >= 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
-  // rows that lie in the cache would be read by one block and written by another
+  // rows or tables that lie in the cache would be read by one block and written by another
   const int64_t bytes = 2 * cols * 2 * n_pages * page;
-  if (overlap(k, 2 * ((total_tokens - 1) * ldk + cols), cache, bytes) ||
-      overlap(v, 2 * ((total_tokens - 1) * ldv + cols), cache, bytes))
+  if (overlaps_any({cache, bytes}, {{k, 2 * ((total_tokens - 1) * ldk + cols)}, {v, 2 * ((total_tokens - 1) * ldv + cols)},
+                                    {table, 4LL * n_slots * max_pages}, {lens, 4LL * n_slots}, {slots, 4LL * n},
+                                    {cu_seqlens, 4LL * (n + 1)}}))
     return KDA_ERR_SHAPE;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   AppendArgs a{k, v, ldk, ldv, Runs{cu_seqlens, nullptr, n, total_tokens, fixed_len},
@@ -199,15 +205,12 @@ int kda_pages_fork(kda_bf16 *cache, int layers, int n_pages, int H, int page, in
     return KDA_ERR_ALIGN;
   const int64_t need = pages_ws_bytes(n), rows = 4LL * n_slots, all = rows * max_pages;
   if (!workspace || workspace_bytes < static_cast<size_t>(need)) return KDA_ERR_WORKSPACE;
-  struct Range { const void *p; int64_t bytes; };
   // written by one CTA while another reads it, or written twice
-  const Range out[] = {{table, all}, {lens, rows}, {left, 4}, {workspace, need}};
-  const Range in[] = {{src, 4LL * n}, {dst, 4LL * n}};
-  for (int i = 0; i < 4; ++i) {
+  const Range out[] = {{table, all}, {lens, rows}, {left, 4}, {workspace, need}, pool_of(cache, layers, n_pages, H, page, D)};
+  for (int i = 0; i < 5; ++i) {
     for (int j = 0; j < i; ++j)
       if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return KDA_ERR_SHAPE;
-    for (const Range &r : in)
-      if (overlap(out[i].p, out[i].bytes, r.p, r.bytes)) return KDA_ERR_SHAPE;
+    if (overlaps_any(out[i], {{src, 4LL * n}, {dst, 4LL * n}})) return KDA_ERR_SHAPE;
   }
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   PagesArgs a{};
@@ -246,6 +249,9 @@ int kda_pages_compact(kda_bf16 *cache, int layers, int n_pages, int H, int page,
       overlap(used, 4, table, all) || overlap(used, 4, lens, rows) ||
       overlap(workspace, need, table, all) || overlap(workspace, need, table_out, all) ||
       overlap(workspace, need, lens, rows) || overlap(workspace, need, used, 4))
+    return KDA_ERR_SHAPE;
+  if (overlaps_any(pool_of(cache, layers, n_pages, H, page, D),
+                   {{table, all}, {table_out, all}, {lens, rows}, {used, 4}, {workspace, need}}))
     return KDA_ERR_SHAPE;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   PagesArgs a{};

@@ -242,3 +242,20 @@ def test_attention_refuses_a_workspace_over_what_it_uses(L, what, end):
 @pytest.mark.parametrize("what", ["table", "lens", "slots", "cu"])
 def test_attention_refuses_an_output_over_its_tables(L, what):
     assert call(L.kda_attn_paged, ATTN, {what: at(3 * GB + 7 * 512 + 508)}) == SHAPE
+
+
+@pytest.mark.parametrize("what", ["table", "lens", "slots", "cu"])
+@pytest.mark.parametrize("end", [0, 10 * 2 * 2 * 16 * 64 * 2 - 4])
+def test_append_refuses_tables_in_the_cache(L, what, end):
+    assert call(L.kda_kv_append, APPEND, {what: at(4 * GB + end)}) == SHAPE
+
+
+POOL = 2 * 10 * 2 * 2 * 16 * 64 * 2  # bytes of the cache of FORK and COMPACT: two layers
+
+
+@pytest.mark.parametrize("end", [0, POOL - 16])
+def test_pages_refuse_tables_in_the_cache(L, end):
+    for what in ("table", "lens", "src", "dst", "left", "ws"):
+        assert call(L.kda_pages_fork, FORK, {what: at(4 * GB + end)}) == SHAPE
+    for what in ("table", "lens", "out", "used", "ws"):
+        assert call(L.kda_pages_compact, COMPACT, {what: at(4 * GB + end)}) == SHAPE

@@ -463,7 +463,10 @@ int kda_verify_draft(const void *target, const void *draft, int prob_bytes, int 
  *           slot without one.  A page is in use where a row of the table reaches
  *           it within its length: nothing else records it, a sequence is freed
  *           by setting its length to 0, and what a row holds behind its length
- *           is not looked at.
+ *           is not looked at.  An entry of -1 within the length is a page that the
+ *           sequence has given up, as those that no window reaches any more may be:
+ *           the operators on pages count nothing there, and a call that needs the
+ *           page records it.
  * page in {16, 32, 64, 128}, D in {64, 128}; n_pages and max_pages at most 2^20,
  * n_slots at most 2^13 where pages are given out, shared or moved.
  *
@@ -510,7 +513,8 @@ int kda_kv_append(const kda_bf16 *k, int64_t ldk, const kda_bf16 *v, int64_t ldv
  *          NaN where its weights have no sum.
  * The run's own keys and values are in the cache before (kda_kv_append).  Where a
  * row's window ends, entries of the table for pages that it no longer reaches are
- * not looked at.  A needed page outside [0, n_pages) is recorded and counts as keys
+ * not looked at: before the next token of slot s, pages i with (i + 1) page <=
+ * lens[s] - window + 1 may be given up (-1).  A needed page outside [0, n_pages) is recorded and counts as keys
  * and values of 0.  A key or value that is not finite makes the outputs of its
  * own sequence undefined; other sequences are not touched by it, and what pages
  * hold behind a sequence's end is not used.  Rows of o outside all runs are

@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kPThreads, 1) pages_plan_kernel(const PagesArg
     for (int j = 0; j < kEntries / 32; ++j) {
       if (i0 + 32 * j >= need) continue;
       if (p[j] >= 0 && p[j] < a.n_pages) atomicOr(&bits[p[j] >> 5], 1u << (p[j] & 31));
-      else bad = 1;
+      else if (p[j] != -1) bad = 1;  // (-1: given up)
     }
   }
 

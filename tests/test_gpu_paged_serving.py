@@ -156,3 +156,56 @@ def test_two_captured_calls_with_workspaces_of_their_own():
         torch.cuda.synchronize()
         assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
     assert kda.device_status() == 0
+
+
+def test_pages_behind_a_window_are_given_up():
+    """Sequences that only ever see the last positions give back the pages in front of them: the pool never holds
+    more, other sequences take the pages, and no call records anything."""
+    window, page, pages, slots_n = 40, 16, 16, 4
+    g = torch.Generator().manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, generator=g).bfloat16()  # noqa: E731
+    cache = torch.full((1, pages, 2, H, page, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    table, lens = torch.full((slots_n, 28), -1, dtype=torch.int32, device="cuda"), ints([0] * slots_n)
+    slots, history = ints([2, 0]), [[], []]
+    for turn in range(34):
+        n = (11, 6) if turn else (70, 5)
+        cu, total = ref.offsets(n), sum(n)
+        want = lens.clone()
+        want[slots.long()] += ints(n)
+        assert int(kda.pages_grow(table, lens, want, page, pages)) >= 0
+        q, k, v = rnd(total, Hq, D), rnd(total, H, D), rnd(total, H, D)
+        kda.kv_append(k.cuda(), v.cuda(), cache[0], table, lens, slots, ints(cu))
+        o = kda.attn_paged(q.cuda(), cache[0], table, lens, slots, ints(cu), window=window).double().cpu()
+        for b in range(2):  # against all keys and values that there were, in 64 bits
+            history[b].append((k[cu[b]:cu[b + 1]], v[cu[b]:cu[b + 1]]))
+            ks, vs = (torch.cat([h[i] for h in history[b]]).double() for i in (0, 1))
+            before = len(ks) - n[b]
+            i = torch.arange(before, len(ks))[:, None]
+            see = (torch.arange(len(ks)) <= i) & (torch.arange(len(ks)) > i - window)
+            for h in range(Hq):
+                x = q[cu[b]:cu[b + 1], h].double() @ ks[:, h // (Hq // H)].t() * D ** -0.5
+                w = torch.softmax(x.masked_fill(~see, float("-inf")), 1)
+                exact, size = w @ vs[:, h // (Hq // H)], w @ vs[:, h // (Hq // H)].abs()
+                err = (o[cu[b]:cu[b + 1], h] - exact).abs()
+                assert float((err - 2.0 ** -8 * exact.abs() - (2.0 ** -8 + 2.0 ** -14) * size).max()) <= 0
+        lens.copy_(want)
+        gone = ((lens - window + 1).clamp(min=0) // page)[:, None]
+        table.masked_fill_(torch.arange(table.shape[1], device="cuda") < gone, -1)
+        if turn % 5 == 4:
+            renamed, used = kda.pages_compact(cache, table, lens)
+            assert int(used) <= 8 and torch.equal(renamed < 0, (table < 0) | (torch.arange(28, device="cuda") * page >= lens[:, None]))
+            table.copy_(renamed)
+        if turn == 20:  # a fork copies what is given up as it is, and may go on
+            kda.pages_fork(cache, table, lens, ints([2]), ints([1]))
+            last = (int(lens[2]) - 1) // page
+            assert torch.equal(table[1, :last], table[2, :last]) and int(table[1, 0]) == -1 and int(lens[1]) == int(lens[2])
+            lens[1] = 0
+    assert int(lens[2]) > pages * page and kda.device_status() == 0
+    # what a call needs is not there: a last page to copy, and an entry that is neither a page nor given up
+    row = (int(lens[2]) - 1) // page
+    assert int(lens[2]) % page
+    for at, entry in ((row, -1), (0, -2), (1, pages)):
+        t = table.clone()
+        t[2, at] = entry
+        kda.pages_fork(cache.clone(), t, lens.clone(), ints([2]), ints([1]))
+        assert kda.device_status() == kda.KDA_ERR_SHAPE

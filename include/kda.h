@@ -467,6 +467,12 @@ int kda_verify_draft(const void *target, const void *draft, int prob_bytes, int 
  *           sequence has given up, as those that no window reaches any more may be:
  *           the operators on pages count nothing there, and a call that needs the
  *           page records it.
+ * Forks share their full pages, and nothing here writes a shared one, as long as
+ * no length is set back into it: kv_append would write over the other sequence's
+ * tokens, which no call checks.  (Within its last page, that no other row reaches,
+ * a sequence may be set back.)  A sequence d goes on from the first m tokens of s, or
+ * s itself does, by a fork from a slot t that is free: table[t] = table[s],
+ * lens[t] = m, kda_pages_fork from t to d (or to s), lens[t] = 0.
  * page in {16, 32, 64, 128}, D in {64, 128}; n_pages and max_pages at most 2^20,
  * n_slots at most 2^13 where pages are given out, shared or moved.
  *

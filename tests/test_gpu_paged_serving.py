@@ -209,3 +209,42 @@ def test_pages_behind_a_window_are_given_up():
         t[2, at] = entry
         kda.pages_fork(cache.clone(), t, lens.clone(), ints([2]), ints([1]))
         assert kda.device_status() == kda.KDA_ERR_SHAPE
+
+
+@pytest.mark.parametrize("m", [16, 17, 40, 48, 5])
+def test_a_sequence_goes_on_from_inside_a_shared_page(m):
+    """By a fork from a slot that holds the first m tokens: another sequence, and the sequence itself, go on from
+    there, and what the others hold stays."""
+    page, pages, most = 16, 24, 6
+    g = torch.Generator().manual_seed(m)
+    cache = torch.randn(LAYERS, pages, 2, H, page, D, generator=g).bfloat16().cuda()
+    table, lens = torch.full((5, most), -1, dtype=torch.int32, device="cuda"), ints([0] * 5)
+    kda.pages_grow(table, lens, ints([55, 0, 0, 0, 0]), page, pages)
+    lens[0] = 55
+    kda.pages_fork(cache, table, lens, ints([0]), ints([1]))  # three full pages are shared
+
+    def held(s):
+        return [ref.gathered(cache[i].cpu(), table.cpu(), s, int(lens[s])) for i in range(LAYERS)]
+
+    def same(a, b, n=None):
+        return all(torch.equal(x[:, :, :n], y[:, :, :n]) for x, y in zip(a, b))
+
+    def on(s, n):  # n more tokens of sequence s
+        want = lens.clone()
+        want[s] += n
+        assert int(kda.pages_grow(table, lens, want, page, pages)) >= 0
+        for i in range(LAYERS):
+            k, v = torch.randn(2, n, H, D, generator=g).bfloat16().cuda()
+            kda.kv_append(k, v, cache[i], table, lens, ints([s]), ints([0, n]))
+        lens.copy_(want)
+
+    first = held(0)
+    for d in (2, 0):  # 4 is the free slot
+        table[4], lens[4] = table[0], m
+        assert int(kda.pages_fork(cache, table, lens, ints([4]), ints([d]))) >= 0
+        lens[4] = 0
+        assert int(lens[d]) == m and same(held(d), first, m)
+        others = {s: held(s) for s in (0, 1, 2) if s != d}
+        on(d, 20)
+        assert same(held(d), first, m) and all(same(held(s), h) for s, h in others.items())
+    assert same(held(1), first) and kda.device_status() == 0

@@ -350,3 +350,84 @@ def test_append_records_offsets_that_decrease(lens):
                 row = got[b, i, 0, j]
                 assert torch.equal(row, x[cu[b] + j, 0].view(torch.int16)) or torch.equal(row, cache[b, i, 0, j].view(torch.int16))
         assert torch.equal(got[b, :, :, max(lens[b], 0):], cache[b, :, :, max(lens[b], 0):].view(torch.int16))
+
+
+@pytest.mark.parametrize("layers", [1, 2])
+@pytest.mark.parametrize("n_slots,most,page,n_pages", SHAPES[1:])
+@pytest.mark.parametrize("spare", [0, 3, 10000])
+def test_fork_of_rows_that_share_pages(n_slots, most, page, n_pages, layers, spare):
+    """Parents and rows that are given up share pages with rows that go on: what those reach is not handed out.
+    With a pool of few unused pages each of them counts."""
+    rng = random.Random(n_slots * layers + spare)
+    table, lens = draw_sequences(rng, n_slots, most, page, n_pages)
+    used = ref.in_use(table, lens, page, n_pages)
+    if spare < n_pages - len(used):  # the others belong to no pool
+        now = {p: i for i, p in enumerate(sorted(used))}
+        for b in range(n_slots):
+            for i in range(-(-int(lens[b]) // page)):
+                table[b, i] = now[int(table[b, i])]
+        n_pages = len(used) + spare
+    cache = noise(layers, n_pages, 2, 1, page, 64, seed=n_slots)
+    order = rng.sample(range(n_slots), n_slots)
+    parents = order[:max(1, n_slots // 3)]
+    dst = order[len(parents):][:max(1, n_slots // 2)]
+    src = [rng.choice(parents) for _ in dst]
+    want = ref.fork(cache, table, lens, src, dst, page)
+    c, t, ln = cache.cuda(), table.cuda(), lens.cuda()
+    left = kda.pages_fork(c, t, ln, ints(src), ints(dst))
+    assert left.tolist() == [want[3]]
+    assert torch.equal(t.cpu(), want[1]) and torch.equal(ln.cpu(), want[2]) and same(c, want[0])
+    # again, from the same parents: each row's own last page is given up, what it shares stays
+    want = ref.fork(want[0], want[1], want[2], src, dst, page)
+    left = kda.pages_fork(c, t, ln, ints(src), ints(dst))
+    assert left.tolist() == [want[3]]
+    assert torch.equal(t.cpu(), want[1]) and torch.equal(ln.cpu(), want[2]) and same(c, want[0])
+
+
+def test_pages_replayed_on_two_other_streams():
+    """One graph, captured on one stream and replayed on others in turn, on contents that change between."""
+    page, H, D, n_slots, most, n_pages = 16, 1, 64, 4, 6, 40
+    table, lens = ints([[-1] * most] * n_slots), ints([0] * n_slots)
+    cache = torch.zeros(1, n_pages, 2, H, page, D, dtype=torch.bfloat16, device="cuda")
+    want, src, dst, cu = ints([0] * n_slots), ints([0]), ints([3]), ints([0, 9, 30, 47])
+    k, v = (torch.zeros(47, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def step():
+        left = kda.pages_grow(table, lens, want, page, n_pages)
+        kda.kv_append(k, v, cache[0], table, lens, cu_seqlens=cu)
+        lens.copy_(want)
+        forked = kda.pages_fork(cache, table, lens, src, dst)
+        _, used = kda.pages_compact(cache, table, lens, table_out=table)
+        return left, forked, used
+
+    captured = torch.cuda.Stream()
+    captured.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=captured):
+        outs = step()
+    others = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for turn in range(6):
+        now = [7 * turn, 30 - 4 * turn, 16, 50]
+        rows, t = noise(2, 47, H, D, seed=turn), torch.full((n_slots, most), -1, dtype=torch.int32)
+        at = 1
+        for b, n in enumerate(now):
+            need = -(-n // page)
+            t[b, :need] = torch.arange(at, at + 3 * need, 3) % n_pages
+            at += 3 * need
+        full = noise(1, n_pages, 2, H, page, D, seed=20 + turn)
+        ln, wt = torch.tensor(now, dtype=torch.int32), torch.tensor([now[0] + 9, now[1] + 21, now[2] + 17, now[3]], dtype=torch.int32)
+        e_table, e_left = ref.grow(t, ln, wt, page, n_pages)
+        e_cache = ref.append(rows[0], rows[1], full[0], e_table, ln, [0, 1, 2], cu.tolist(), page)[None]
+        e_cache, e_table, e_lens, e_forked = ref.fork(e_cache, e_table, wt, [0], [3], page)
+        e_cache, e_table, e_used = ref.compact(e_cache, e_table, e_lens, page)
+        stream = others[turn % 2]
+        with torch.cuda.stream(stream):  # all of it on that stream, which the other one's turn is waited for
+            stream.wait_stream(others[(turn + 1) % 2])
+            stream.wait_stream(captured)
+            for x, y in ((table, t), (lens, ln), (want, wt), (k, rows[0]), (v, rows[1]), (cache, full)):
+                x.copy_(y)
+            g.replay()
+            counts = [int(c) for c in outs]
+        assert counts == [e_left, e_forked, e_used]
+        stream.synchronize()
+        assert torch.equal(table.cpu(), e_table) and torch.equal(lens.cpu(), e_lens) and same(cache, e_cache)

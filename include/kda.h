@@ -544,12 +544,14 @@ int kda_attn_paged(const kda_bf16 *q, int64_t ldq, const int32_t *cu_seqlens, in
                    const int32_t *slots, float scale, int window, kda_bf16 *o, int64_t ldo,
                    void *workspace, size_t workspace_bytes, kda_stream_t stream);
 
-/* Workspace bytes of kda_attn_paged (0: none needed, or unsupported sizes). */
+/* Workspace bytes of kda_attn_paged (0: none needed, or unsupported sizes): of D alone
+ * where any are, so one workspace serves all calls of a stream. */
 size_t kda_attn_paged_workspace_bytes(int n, int64_t total_tokens, int Hq, int H, int D);
 
 /*
  * kda_pages_grow - give rows of the table the pages that sequences of want[s]
- * instead of lens[s] tokens need (int32 [n_slots]; no more than lens[s]: none).
+ * instead of lens[s] tokens need (int32 [n_slots]; no more than lens[s]: none;
+ * negative, or more than the row holds: none, recorded).
  * The unused pages are given out in ascending order, to the rows in ascending
  * order.  A row gets all of its pages or none: from the first row on for which
  * too few are left, rows get -1 in their place.

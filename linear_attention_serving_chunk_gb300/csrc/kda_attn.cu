@@ -23,7 +23,7 @@
 // (tokens, drafted runs) give both the same rows and every other tile: then the keys are what counts,
 // and two chains hide each other's latency; their sums meet in shared memory at the end.  With heads
 // of 64 the sums leave room in TMEM for a third place of scores, which run ahead by one: their MMAs
-// take half as long, and with two places a warpgroup waits for them (955 against 770 us for 4096 tokens
+// take half as long, and with two places a warpgroup waits for them (955 against 790 us for 4096 tokens
 // behind 28,672, 32 heads of 64).
 //
 // Scores, maxima, sums and O are fp32.  The weights are rounded to bf16 for their product with V,
@@ -37,19 +37,17 @@
 // nothing.  Keys behind a row's position, or behind the window, weigh nothing whatever they are; the
 // rows of V behind the sequence are zeroed, for 0 times what lies there might not be 0.
 //
-// Prompt chunks are bound by the products, and those by shared memory: the scores of two tiles read 128 KB in
-// their 1024 cycles while 64 KB of K and V are written.  1160 to 1190 us for 4096 tokens behind 28,672, 32 heads of 128
-// over 8 of keys, 1.75 PFLOP/s where a large product of the library reaches 1.93 (1340 us back to back for
-// seconds, at the clock that the power limit leaves).  Single tokens are bound by memory: 645 us for 128
+// Prompt chunks are bound by the chain of each warpgroup, scores, weights, product, which the other one's hides in
+// part: the tensor core is busy for 68 to 73 % of the time, and without the exponentials a call takes 5 % less, with half
+// of the products 19 %.  4096 tokens behind 28,672, 32 heads of 128 over 8 of keys, take 1350 to 1390 us one
+// after another for a second, at the clock that the power limit leaves (1.5 PFLOP/s; a large product of the library
+// then keeps 1.74), and 1160 to 1190 in short bursts.  Single tokens are bound by memory: 646 us for 128
 // sequences of 1000 to 16,000 tokens, 4.49 GB.  Short calls are bound by latency: about 5 us until the
 // first scores, 1 us a tile (2 the first time, while its code comes), 3 us for the join.
 //
-// What it took, us for those chunks / those tokens: the MMAs issued by lane 0 1694 / 675 (each waits for its
-// operands to come into uniform registers); by an elected thread, with the warp's number and TMEM's address
-// uniform for all 1172 / 661; one warp that loads and one that works out items 1163 / 652; two that load
-// 1150 / 641 (heads of 64 in pages of 16: 526 to 357).  Not kept: the weights given in two halves, each as
-// soon as it is there (1804); rows of o through a transposition between lanes, 64 bytes in a row, which makes
-// the compiler spill registers in the loop over the keys (1350); 32-byte stores (no change).
+// The MMAs are issued by an elected thread, with the warp's number and TMEM's address uniform for all: by lane 0, each
+// waits for its operands to come into uniform registers (1694 us for those chunks in a burst).  Two warps load:
+// with one, single tokens take 652, and heads of 64 in pages of 16 526 instead of 357.
 #include <string.h>
 
 #include <type_traits>
